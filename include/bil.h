@@ -402,6 +402,34 @@ int bil_linear_gemm(const void *a, int a_layout, const void *b, int b_layout, in
                     bil_stream_t stream);
 
 /*
+ * bil_linear_logp_fp8_fwd -- the fused LM-head + logp on 8-bit operands
+ * (serving and scoring; there is no backward).  The logits are
+ *     z[r, c] = (sum_k hidden[r, k] * weight[c, k]) * weight_scale[c] * hidden_scale[r]
+ * with e4m3 hidden and weight (float32 accumulation on the tensor cores, K in
+ * increasing blocks of 128, the same order for every row and tile; the two
+ * scales multiplied in this order, each product rounded to float32), times
+ * rcp as in bil_logp_fwd.  logp, lse, entropy and the optional logits are as
+ * for bil_linear_logp_fwd, with the same tiles of BIL_LINEAR_TILE_V columns, so
+ * a row's bits depend on that row, the weight and the scales alone.
+ *
+ *  hidden        [n_rows, ld_hidden] e4m3 bytes (sign, 4 exponent bits, 3
+ *                mantissa bits, no infinities; a NaN byte makes its row NaN).
+ *  hidden_scale  [n_rows] float32, >= 0 (bil_rms_norm_quant's scale).
+ *  weight        [vocab, ld_weight] e4m3 bytes, one row per vocabulary column.
+ *  weight_scale  [vocab] float32 (bil_quantize_rows's scale).
+ *                Both matrices: 16-byte aligned base and a row stride of a
+ *                multiple of 16 bytes (BIL_E_ALIGN otherwise).
+ *  workspace     as for bil_linear_logp_fwd (bil_linear_logp_workspace_bytes).
+ * Other arguments as for bil_linear_logp_fwd.
+ */
+int bil_linear_logp_fp8_fwd(const void *hidden, const float *hidden_scale, const void *weight,
+                            const float *weight_scale, int64_t n_rows, int64_t hidden_size, int64_t ld_hidden,
+                            int64_t vocab, int64_t ld_weight, float temperature, const int64_t *target_ids,
+                            int64_t ignore_index, float *logp, float *lse, float *entropy, void *logits,
+                            int logits_dtype, int64_t ld_logits, void *workspace, int64_t workspace_bytes,
+                            int validate, bil_stream_t stream);
+
+/*
  * bil_sum_f32 -- dst[i] = ((srcs[0][i] + srcs[1][i]) + srcs[2][i]) + ... for
  * i < n: float32 sums in the order of `srcs` (1 <= count <= 16; `srcs` is a
  * host array of device pointers; dst may be one of the sources).  Adds the

@@ -17,6 +17,7 @@ from .linear import (  # noqa: F401
     gemm_nt,
     linear_logp,
     linear_logp_bwd,
+    linear_logp_fp8,
     linear_logp_grad,
     linear_logp_partials,
     matmul,

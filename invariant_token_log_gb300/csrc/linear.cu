@@ -23,8 +23,8 @@
 //               out 32 rows x 64 bytes at a time through two staging boxes
 //               of the warp's own and TMA stores;
 //   warp 6      the store GEMMs' lockstep service (see lockstep_service).
-// The accumulator of one tile is read while the next tile's MMAs run.  Three
-// epilogues make three kernels:
+// The accumulator of one tile is read while the next tile's MMAs run.  The
+// epilogues make the kernels:
 //   linear_partials_kernel   forward: A = hidden, B = weight; the tile's
 //                            partial of the operator (and, optionally, the
 //                            logits);
@@ -38,7 +38,11 @@
 //                            from 256 rows on the work unit is two 128-row A
 //                            tiles sharing one B tile (a 3-stage ring of
 //                            64 KB stages, both accumulators in tensor memory
-//                            at once).
+//                            at once);
+//   linear_partials8_kernel  forward on 8-bit operands: e4m3 hidden and weight,
+//                            tcgen05.mma kind::f8f6f4 over 128-element K
+//                            blocks (the same 128-byte lines), the partial
+//                            of the accumulator scaled by row and column.
 //
 // What fixes the bits of z[r, c] is the K order (K blocks in order, four
 // K=16 steps each, from a zeroed accumulator), the same for every row and
@@ -73,6 +77,7 @@ constexpr unsigned kWatchOwnDrain = 256u;  // producer or MMA issuer waited too 
 constexpr int kBM = 128;      // rows per tile: one tensor-memory lane per row
 constexpr int kBN = 256;      // vocabulary columns per tile = the operator's tile width here
 constexpr int kBK = 64;       // K per stage: 64 x 16 bits = one 128-byte swizzle row
+constexpr int kBK8 = 128;     // the same row of 8-bit operands
 constexpr int kUmmaK = 16;    // K of one tcgen05.mma kind::f16
 constexpr int kStages = 4;
 constexpr unsigned kStageABytes = kBM * kBK * 2;  // 16 KB
@@ -114,12 +119,17 @@ constexpr uint32_t kStoreBoxBytes = kStoreBox * kStoreBox * 2;           // 2 KB
 constexpr size_t kStagingBytes = BIL_EPILOGUE_TMA_STORE ? 4 * 2 * kStoreBoxBytes : 0;  // 4 warps x 2 buffers
 constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kStages * size_t(kStageBytes) + sizeof(LinearSmem) +
                               (BIL_EPILOGUE_TMA_STORE ? 1024 + kStagingBytes : 0);
+// The 8-bit forward keeps, past the staging boxes, each epilogue warp's copy of its tile's column scales.
+constexpr size_t kStagingBytes8 = kEpiWarps * 2 * kStoreBoxBytes;
+constexpr size_t kSmemBytes8 = 1024 + kStages * size_t(kStageBytes) + sizeof(LinearSmem) + 1024 + kStagingBytes8 +
+                               kEpiWarps * kBN * sizeof(float);
 
 // What the epilogue warps do with a finished accumulator tile.
 enum EpilogueMode {
   kModePartials = 0,  // the operator's tile partials (and, optionally, the logits)
   kModeGrad = 1,      // dZ = d(g logp + gh H)/dz, stored as 16-bit in [rows, vocab] and [vocab, rows]
   kModeStore = 2,     // C = A . B^T stored as it is (float32, or rounded to 16 bits)
+  kModePartials8 = 3, // kModePartials on e4m3 operands, scaled by row and by column
 };
 
 struct LinearParams {
@@ -158,6 +168,9 @@ struct LinearParams {
   int64_t ld_out;
   unsigned sync_tag;           // non-zero: the copy threads keep in step (see lockstep_service)
   int a_mn, b_mn;              // 1: the operand is stored [K, rows] (rows contiguous), else [rows, K]
+  // kModePartials8
+  const float* row_scale;      // [n_rows]
+  const float* col_scale;      // [shard_cols]
 };
 
 // ---------------------------------------------------------------------------
@@ -234,6 +247,18 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same for e4m3 operands (their type code in the descriptor is 0, as
+// fp16's is for kind::f16); a K step is 32 elements, again 32 bytes.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -447,6 +472,100 @@ __device__ __forceinline__ void row_partial(uint32_t taddr, int vcols, float rcp
                       kLn2);
   m_out = m;
   tl_out = tl;
+}
+
+// The partial of one row of one tile of the 8-bit forward.  The logits are
+//   z_c = v_c *rn sh,  v_c = acc_c *rn sw_c
+// (sw: the column's scale, sh >= 0: the row's); the partial takes the row's
+// scale out of the maximum and into the exponent's constant:
+//   mx = max over valid c of v_c (exact);  m = (mx *rn sh) *rn rcp
+//   t_c = (v_c -rn mx) *rn c,  c = (sh *rn rcp) *rn log2e
+// with e_c, the eight slots, the tree and the entropy sum of row_partial; the
+// target logit is (v_t *rn sh) *rn rcp.  `sw` is the warp's copy of the tile's
+// column scales in shared memory (every lane reads the same word: a
+// broadcast).  With `box_map` the logits z_c go out through the warp's staging
+// boxes.  Both passes run on packed float32 pairs.
+template <bool ENT>
+__device__ __forceinline__ void row_partial8(uint32_t taddr, int vcols, float rcp, float sh, const float* sw,
+                                             int64_t tloc, int out_dtype, float& m_out, float& s_out, float& u_out,
+                                             float& tl_out, const CUtensorMap* box_map, unsigned char* staging,
+                                             int box_x, int box_y, int lane, uint32_t* issued) {
+  uint32_t r[kChunk];
+  float mx = -INFINITY;
+  float tl = 0.0f;
+  const uint64_t sh2 = pk(sh, sh);
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += kChunk) {
+    tmem_ld32(taddr + c0, r);
+#pragma unroll
+    for (int k = 0; k < kChunk; k += 4) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
+      const uint64_t v0 = mul2(static_cast<uint64_t>(r[k]) | (static_cast<uint64_t>(r[k + 1]) << 32), w.x);
+      const uint64_t v1 = mul2(static_cast<uint64_t>(r[k + 2]) | (static_cast<uint64_t>(r[k + 3]) << 32), w.y);
+      const float v[4] = {lo_of(v0), hi_of(v0), lo_of(v1), hi_of(v1)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c0 + k + j < vcols) mx = fmaxf(mx, v[j]);
+        if (c0 + k + j == tloc) tl = v[j];
+      }
+      if (box_map != nullptr) {
+        const uint64_t z0 = mul2(v0, sh2), z1 = mul2(v1, sh2);
+        r[k] = __float_as_uint(lo_of(z0));
+        r[k + 1] = __float_as_uint(hi_of(z0));
+        r[k + 2] = __float_as_uint(lo_of(z1));
+        r[k + 3] = __float_as_uint(hi_of(z1));
+      }
+    }
+    if (box_map != nullptr && c0 < vcols) {
+      if (out_dtype == BIL_F32) {  // two boxes of 16 columns
+        uint32_t w0[16], w1[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          w0[j] = r[j];
+          w1[j] = r[16 + j];
+        }
+        store_box(staging, box_map, box_x + c0, box_y, lane, *issued, w0);
+        store_box(staging, box_map, box_x + c0 + 16, box_y, lane, *issued, w1);
+      } else {
+        uint32_t pk16[kChunk / 2];
+#pragma unroll
+        for (int j = 0; j < kChunk; j += 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+          pk16[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        store_box(staging, box_map, box_x + c0, box_y, lane, *issued, pk16);
+      }
+    }
+  }
+  const float shift = (mx == -INFINITY) ? 0.0f : mx;
+  const float c = __fmul_rn(__fmul_rn(sh, rcp), kLog2e);
+  uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
+  const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += kChunk) {
+    tmem_ld32(taddr + c0, r);
+#pragma unroll
+    for (int k = 0; k < kChunk / 2; ++k) {
+      const uint64_t w = *reinterpret_cast<const uint64_t*>(sw + c0 + 2 * k);
+      const uint64_t v = mul2(static_cast<uint64_t>(r[2 * k]) | (static_cast<uint64_t>(r[2 * k + 1]) << 32), w);
+      const uint64_t t = mul2(sub2(v, shift2), c2);
+      float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
+      if (c0 + 2 * k >= vcols) e0 = 0.0f;  // columns past the vocabulary add nothing
+      if (c0 + 2 * k + 1 >= vcols) e1 = 0.0f;
+      const uint64_t e = pk(e0, e1);
+      a2[k % 4] = add2(a2[k % 4], e);
+      if (ENT) u2[k % 4] = fma2(e, pk(fmaxf(lo_of(t), kNegMax), fmaxf(hi_of(t), kNegMax)), u2[k % 4]);
+    }
+  }
+  m_out = __fmul_rn(__fmul_rn(mx, sh), rcp);
+  s_out = __fadd_rn(__fadd_rn(__fadd_rn(lo_of(a2[0]), hi_of(a2[0])), __fadd_rn(lo_of(a2[1]), hi_of(a2[1]))),
+                    __fadd_rn(__fadd_rn(lo_of(a2[2]), hi_of(a2[2])), __fadd_rn(lo_of(a2[3]), hi_of(a2[3]))));
+  if (ENT)
+    u_out = __fmul_rn(
+        __fadd_rn(__fadd_rn(__fadd_rn(lo_of(u2[0]), hi_of(u2[0])), __fadd_rn(lo_of(u2[1]), hi_of(u2[1]))),
+                  __fadd_rn(__fadd_rn(lo_of(u2[2]), hi_of(u2[2])), __fadd_rn(lo_of(u2[3]), hi_of(u2[3])))),
+        kLn2);
+  tl_out = __fmul_rn(__fmul_rn(tl, sh), rcp);
 }
 
 // float -> 16-bit storage, round to nearest even.
@@ -691,6 +810,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
   static_assert(kStagesH >= 3 && kStagesH <= kStages, "the stage ring fits the shared memory of the 1-half layout");
   constexpr int kAccBufs = HALVES == 1 ? 2 : 1;
   constexpr int kRowsPerUnit = HALVES * kBM;
+  constexpr bool kOp8 = MODE == kModePartials8;
+  constexpr int kStageK = kOp8 ? kBK8 : kBK;  // K elements per stage: one 128-byte line either way
   extern __shared__ unsigned char smem_raw[];
   // Stage buffers start on a 1024-byte boundary (the 128-byte swizzle pattern
   // repeats every 8 rows = 1024 bytes).
@@ -761,14 +882,14 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
           } else {
 #pragma unroll
             for (int h = 0; h < HALVES; ++h)
-              tma_load_2d(a_dst + h * kStageABytes, &tmap_hidden, kb * kBK, (m * HALVES + h) * kBM, &sm.full[s]);
+              tma_load_2d(a_dst + h * kStageABytes, &tmap_hidden, kb * kStageK, (m * HALVES + h) * kBM, &sm.full[s]);
           }
           if (MODE == kModeStore && p.b_mn) {
 #pragma unroll
             for (int j = 0; j < kBN / kMnBox; ++j)
               tma_load_2d(b_dst + j * kMnBoxBytes, &tmap_weight, n * kBN + j * kMnBox, kb * kBK, &sm.full[s]);
           } else {
-            tma_load_2d(b_dst, &tmap_weight, kb * kBK, n * kBN, &sm.full[s]);
+            tma_load_2d(b_dst, &tmap_weight, kb * kStageK, n * kBN, &sm.full[s]);
           }
         }
       }
@@ -813,7 +934,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
             for (int h = 0; h < HALVES; ++h) {
               const uint32_t ah = a_addr + h * kStageABytes;  // an MN-major half is two boxes: the same 16 KB
               const uint64_t adesc = a_mn ? smem_desc_mn(ah + k * kUmmaK * 128) : smem_desc(ah + k * kUmmaK * 2);
-              umma_f16(d_tmem + static_cast<uint32_t>(h * kAccCols), adesc, bdesc, p.idesc, (kb | k) != 0 ? 1u : 0u);
+              if (kOp8)
+                umma_f8(d_tmem + static_cast<uint32_t>(h * kAccCols), adesc, bdesc, p.idesc, (kb | k) != 0 ? 1u : 0u);
+              else
+                umma_f16(d_tmem + static_cast<uint32_t>(h * kAccCols), adesc, bdesc, p.idesc, (kb | k) != 0 ? 1u : 0u);
             }
           }
           umma_commit(&sm.empty[s]);  // the stage is free once these MMAs have read it
@@ -877,6 +1001,38 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
           if (ENT) p.part_ent[at] = active ? ut : 0.0f;
           if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
         }
+      } else if constexpr (MODE == kModePartials8) {
+        unsigned char* staging_all = reinterpret_cast<unsigned char*>(
+            (reinterpret_cast<uintptr_t>(&sm + 1) + 1023) & ~static_cast<uintptr_t>(1023));
+        float* sw = reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN;
+        const int64_t t = valid ? p.targets[row] : p.ignore_index;
+        const bool active = valid && t != p.ignore_index;
+        const int64_t tloc = active ? t - static_cast<int64_t>(p.tile_begin + n) * kBN : -1;
+        const float sh = valid ? p.row_scale[row] : 0.0f;
+        // the tile's column scales, while its MMAs run (the warp's reads of the last tile's are done)
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kBN / kLanes; ++j) {
+          const int c = j * kLanes + lane;
+          sw[c] = c < vcols ? __ldg(p.col_scale + col0 + c) : 0.0f;
+        }
+        __syncwarp();
+        if (!warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear)) break;
+        tc_fence_after();
+        float mt, st, ut = 0.0f, tl;
+        row_partial8<ENT>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl,
+                          p.logits != nullptr ? &tmap_out : nullptr, staging_all + q * 2 * kStoreBoxBytes,
+                          static_cast<int>(col0), static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+        if (valid) {
+          const int64_t at = row * p.ld_part + p.tile_begin + n;
+          p.part_max[at] = active ? mt : -INFINITY;
+          p.part_sum[at] = active ? st : 0.0f;
+          if (ENT) p.part_ent[at] = active ? ut : 0.0f;
+          if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
+        }
       } else if constexpr (MODE == kModeGrad) {
         RowMeta meta{p.ignore_index, 0.0f, 0.0f, 0.0f, 0.0f};
         if (valid) {
@@ -924,7 +1080,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
       }
     }
     // the staging boxes stay in use until their stores have completed
-    if (BIL_EPILOGUE_TMA_STORE && lane == 0 && store_boxes != 0) bulk_wait_all();
+    if ((BIL_EPILOGUE_TMA_STORE || kOp8) && lane == 0 && store_boxes != 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -944,6 +1100,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmap_weight,
                            const __grid_constant__ CUtensorMap tmap_out, const LinearParams p) {
   gemm_body<kModePartials, ENT, 0>(tmap_hidden, tmap_weight, tmap_out, p);
+}
+
+// Forward on e4m3 operands with a scale per row of each.
+template <bool ENT>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_partials8_kernel(const __grid_constant__ CUtensorMap tmap_hidden,
+                            const __grid_constant__ CUtensorMap tmap_weight,
+                            const __grid_constant__ CUtensorMap tmap_logits, const LinearParams p) {
+  gemm_body<kModePartials8, ENT, BIL_F32>(tmap_hidden, tmap_weight, tmap_logits, p);
 }
 
 // Backward, first pass: hidden . weight^T recomputed, dZ stored (16-bit DT).
@@ -1020,6 +1185,21 @@ int make_map(CUtensorMap* map, const void* ptr, int dtype, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? BIL_OK : BIL_E_CUDA;
 }
 
+// The same for e4m3 elements: boxes of box_rows x 128 elements, the tensor
+// cores' type being in the instruction descriptor alone.
+int make_map8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return BIL_E_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK8), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BIL_OK : BIL_E_CUDA;
+}
+
 // The tensor map an epilogue stores a [rows, cols] output (row stride ld
 // elements) through from the warps' staging boxes: 32 rows of 64 bytes, i.e.
 // 32 columns of a 16-bit type or 16 of float32, no swizzle (a box in shared
@@ -1048,16 +1228,16 @@ typedef void (*GemmKernel)(CUtensorMap, CUtensorMap, CUtensorMap, LinearParams);
 // mo: the output's tensor map for an epilogue that stores with TMA (the
 // gradient pass's dZ), else any valid map (unused).
 int launch_gemm(GemmKernel kernel, const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mo,
-                const LinearParams& p, cudaStream_t stream) {
+                const LinearParams& p, cudaStream_t stream, size_t smem_bytes = kSmemBytes) {
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
-  if (static_cast<size_t>(smem_optin) < kSmemBytes) return BIL_E_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
+  if (static_cast<size_t>(smem_optin) < smem_bytes) return BIL_E_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes)) !=
       cudaSuccess)
     return BIL_E_CUDA;
   const int64_t total = static_cast<int64_t>(p.num_m) * p.num_n;
   const int grid = static_cast<int>(std::min<int64_t>(total, sms));
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(mh, mw, mo, p);
+  kernel<<<grid, kThreads, smem_bytes, stream>>>(mh, mw, mo, p);
   return cudaGetLastError() == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
@@ -1425,6 +1605,85 @@ int bil_linear_logp_fwd(const void* hidden, const void* weight, int dtype, int64
     return st;
   return bil_logp_merge(pm, ps, pe, n_rows, static_cast<int32_t>(num_tiles), num_tiles, tl, target_ids,
                         ignore_index, vocab, logp, lse, entropy, 0, stream);
+}
+
+int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const void* weight,
+                            const float* weight_scale, int64_t n_rows, int64_t hidden_size, int64_t ld_hidden,
+                            int64_t vocab, int64_t ld_weight, float temperature, const int64_t* target_ids,
+                            int64_t ignore_index, float* logp, float* lse, float* entropy, void* logits,
+                            int logits_dtype, int64_t ld_logits, void* workspace, int64_t workspace_bytes,
+                            int validate, bil_stream_t stream) {
+  bil_internal::NvtxRange nvtx_range("bil_linear_logp_fp8_fwd");
+  if (n_rows < 0 || hidden_size < 1 || vocab < 1 || ld_hidden < hidden_size || ld_weight < hidden_size)
+    return BIL_E_INVALID_ARG;
+  if (!workspace_fits(n_rows, vocab)) return BIL_E_UNSUPPORTED;
+  const int64_t num_tiles = (vocab + kBN - 1) / kBN;
+  if (num_tiles > INT32_MAX / 2) return BIL_E_UNSUPPORTED;
+  const int64_t el = logits_dtype == BIL_F32 ? 4 : 2;
+  if (logits != nullptr) {
+    if (logits_dtype != BIL_F32 && logits_dtype != BIL_BF16) return BIL_E_DTYPE;
+    if (ld_logits < vocab) return BIL_E_INVALID_ARG;
+    if (!bil_internal::extent_ok(n_rows, ld_logits, el)) return BIL_E_UNSUPPORTED;
+  }
+  if (!bil_internal::extent_ok(n_rows, ld_hidden, 1) || !bil_internal::extent_ok(vocab, ld_weight, 1))
+    return BIL_E_UNSUPPORTED;
+  float rcp = 1.0f;
+  if (int st = bil_internal::temperature_rcp(temperature, &rcp)) return st;
+  if (n_rows == 0) return BIL_OK;
+  const Workspace w = workspace_layout(n_rows, num_tiles, entropy != nullptr);
+  if (hidden == nullptr || hidden_scale == nullptr || weight == nullptr || weight_scale == nullptr ||
+      target_ids == nullptr || logp == nullptr || workspace == nullptr)
+    return BIL_E_INVALID_ARG;
+  if (workspace_bytes < static_cast<int64_t>(w.total)) return BIL_E_INVALID_ARG;
+  if (!rows16(hidden, ld_hidden, 1) || !rows16(weight, ld_weight, 1) || !aligned_to(workspace, 256))
+    return BIL_E_ALIGN;
+  if (!aligned_to(hidden_scale, 4) || !aligned_to(weight_scale, 4) || !aligned_to(target_ids, 8) ||
+      !aligned_to(logp, 4) || (lse && !aligned_to(lse, 4)) || (entropy && !aligned_to(entropy, 4)))
+    return BIL_E_ALIGN;
+  if (logits != nullptr && !rows16(logits, ld_logits, el)) return BIL_E_ALIGN;
+  if (n_rows > INT32_MAX - kBM || vocab > INT32_MAX - kBN || hidden_size > INT32_MAX - kBK8)
+    return BIL_E_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (validate) {
+    if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
+  }
+  const int a_rows = static_cast<int>(n_rows < kBM ? n_rows : kBM);  // as in bil_linear_logp_partials
+  CUtensorMap mh, mw;
+  if (int st = make_map8(&mh, hidden, n_rows, hidden_size, ld_hidden, a_rows)) return st;
+  if (int st = make_map8(&mw, weight, vocab, hidden_size, ld_weight, kBN)) return st;
+  CUtensorMap mo = mw;
+  if (logits != nullptr) {
+    if (int st = make_store_map(&mo, logits, logits_dtype, n_rows, vocab, ld_logits)) return st;
+  }
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const bool ent = entropy != nullptr;
+  LinearParams p{};
+  p.n_rows = n_rows;
+  p.shard_cols = vocab;
+  p.num_n = static_cast<int>(num_tiles);
+  p.num_m = static_cast<int>((n_rows + kBM - 1) / kBM);
+  p.k_blocks = static_cast<int>((hidden_size + kBK8 - 1) / kBK8);
+  p.targets = target_ids;
+  p.ignore_index = ignore_index;
+  p.rcp = rcp;
+  p.part_max = reinterpret_cast<float*>(ws);
+  p.part_sum = reinterpret_cast<float*>(ws + w.part);
+  p.part_ent = ent ? reinterpret_cast<float*>(ws + 2 * w.part) : nullptr;
+  p.ld_part = num_tiles;
+  p.target_logit = reinterpret_cast<float*>(ws + w.part * (ent ? 3 : 2));
+  p.logits = static_cast<unsigned char*>(logits);
+  p.logits_dtype = logits_dtype;
+  p.ld_logits = ld_logits;
+  p.idesc = make_idesc(false);  // type code 0: e4m3 for kind::f8f6f4
+  p.a_box_bytes = static_cast<unsigned>(a_rows) * kBK8;
+  p.m_group = kMGroup;
+  p.row_scale = hidden_scale;
+  p.col_scale = weight_scale;
+  if (int st = launch_gemm(ent ? linear_partials8_kernel<true> : linear_partials8_kernel<false>, mh, mw, mo, p, s,
+                           kSmemBytes8))
+    return st;
+  return bil_logp_merge(p.part_max, p.part_sum, p.part_ent, n_rows, static_cast<int32_t>(num_tiles), num_tiles,
+                        p.target_logit, target_ids, ignore_index, vocab, logp, lse, entropy, 0, stream);
 }
 
 int bil_sum_f32(const float* const* srcs, int count, int64_t n, float* dst, bil_stream_t stream) {

@@ -20,7 +20,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .logp import IGNORE_INDEX, _need_cuda, _ptr, _stream, logp_bwd
+from .logp import IGNORE_INDEX, _need_cuda, _on_device, _ptr, _stream, _stream_handle, _targets1d, logp_bwd
 
 LINEAR_TILE_V = _lib.LINEAR_TILE_V
 _IN_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
@@ -135,6 +135,74 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target_ids: torch.Te
         _ptr(t), ignore_index, _ptr(logp), _ptr(lse), _ptr(ent), _ptr(logits),
         _OUT_DTYPES.get(logits_dtype, _lib.F32), logits.stride(0) if logits is not None else 0, _ptr(workspace),
         workspace.numel() * workspace.element_size(), int(validate), _stream(dev)))
+    out = [logp.reshape(lead), lse.reshape(lead)]
+    if return_entropy:
+        out.append(ent.reshape(lead))
+    if return_logits:
+        out.append(logits.reshape(*lead, vocab))
+    return tuple(out)
+
+
+def _matrix8(x: torch.Tensor, what: str) -> torch.Tensor:
+    """[*lead, H] e4m3 -> [N, H] with unit column stride and 16-byte aligned rows (a view when
+    one exists, else a copy whose rows are padded to 16 bytes)."""
+    if x.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"{what} must be float8_e4m3fn, not {x.dtype}")
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    if x2.shape[0] and (x2.stride(-1) != 1 or _ld(x2) % 16 or x2.data_ptr() % 16):
+        buf = torch.empty((x2.shape[0], -(-x2.shape[1] // 16) * 16), dtype=x2.dtype, device=x2.device)
+        x2 = buf[:, :x2.shape[1]].copy_(x2)
+    return x2
+
+
+def _scales(s: torch.Tensor, n: int, device: torch.device, what: str) -> torch.Tensor:
+    if s.dtype != torch.float32 or s.numel() != n or s.device != device:
+        raise ValueError(f"{what} must be float32, one per row ({n}), on the operands' device")
+    return s.reshape(-1).contiguous()
+
+
+def linear_logp_fp8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch.Tensor,
+                    weight_scale: torch.Tensor, target_ids: torch.Tensor, ignore_index: int = IGNORE_INDEX,
+                    temperature: float = 1.0, return_entropy: bool = False, return_logits: bool = False,
+                    logits_dtype: torch.dtype = torch.float32, validate: bool = False,
+                    workspace: torch.Tensor | None = None):
+    """Fused LM-head + logp on 8-bit operands: (logp, lse[, entropy][, logits]) as
+    ``linear_logp``, for float8_e4m3fn hidden [*lead, H] with a float32 scale per row
+    (``rms_norm_quant``) and weight [V, H] with one per vocabulary row
+    (``quantize_rows``, once per weight).  z[r, c] = (hidden_r . weight_c) *
+    weight_scale[c] * hidden_scale[r], accumulated in float32 on the tensor cores.
+    For serving and scoring: it has no backward."""
+    _need_cuda(hidden, hidden_scale, weight, weight_scale, target_ids, workspace)
+    lead = hidden.shape[:-1]
+    if tuple(target_ids.shape) != tuple(lead):
+        raise ValueError(f"target_ids shape {tuple(target_ids.shape)} != hidden's leading shape {tuple(lead)}")
+    h2, w2 = _matrix8(hidden, "hidden"), _matrix8(weight, "weight")
+    if h2.shape[1] != w2.shape[1]:
+        raise ValueError(f"hidden size {h2.shape[1]} != weight's {w2.shape[1]}")
+    n, vocab = h2.shape[0], w2.shape[0]
+    dev = h2.device
+    if w2.device != dev:
+        raise ValueError("hidden and weight must be on one device")
+    hs, ws = _scales(hidden_scale, n, dev, "hidden_scale"), _scales(weight_scale, vocab, dev, "weight_scale")
+    t = _targets1d(target_ids, lead, dev)
+    logp = torch.empty(n, dtype=torch.float32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    ent = torch.empty(n, dtype=torch.float32, device=dev) if return_entropy else None
+    logits = None
+    if return_logits:
+        if logits_dtype not in _OUT_DTYPES:
+            raise TypeError("logits_dtype must be float32 or bfloat16")
+        logits = torch.empty((n, _pad8(vocab)), dtype=logits_dtype, device=dev)[:, :vocab]
+    need = workspace_bytes(n, vocab, return_entropy)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
+    _lib.check("bil_linear_logp_fp8_fwd", _on_device(
+        dev.index, _lib.load().bil_linear_logp_fp8_fwd, _ptr(h2), _ptr(hs), _ptr(w2), _ptr(ws), n, h2.shape[1],
+        _ld(h2), vocab, _ld(w2), float(temperature), _ptr(t), ignore_index, _ptr(logp), _ptr(lse), _ptr(ent),
+        _ptr(logits), _OUT_DTYPES.get(logits_dtype, _lib.F32), logits.stride(0) if logits is not None else 0,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), int(validate), _stream_handle(dev.index)))
     out = [logp.reshape(lead), lse.reshape(lead)]
     if return_entropy:
         out.append(ent.reshape(lead))
