@@ -429,6 +429,86 @@ int bil_linear_logp_fp8_fwd(const void *hidden, const float *hidden_scale, const
                             int logits_dtype, int64_t ld_logits, void *workspace, int64_t workspace_bytes,
                             int validate, bil_stream_t stream);
 
+/* Widest row of the norm calls (elements): a row stays in one block's registers. */
+#define BIL_MAX_NORM_WIDTH 16384
+
+/*
+ * bil_rms_norm_fwd -- root-mean-square norm with the residual's addition:
+ *     h = round(x + residual) in the rows' type (residual NULL: h = x)
+ *     rstd = 1 / sqrt(mean_c h_c^2 + eps),  y = round((h * rstd) * weight)
+ * in float32 between the loads and the rounding to the rows' type.  A row's
+ * bits depend on that row, the weight, eps and the width alone.
+ *
+ *  x             [n_rows, ld_x] elements of type `dtype` (BIL_F32, BIL_BF16 or
+ *                BIL_F16), 1 <= width <= BIL_MAX_NORM_WIDTH columns read.
+ *  residual      NULL, or [n_rows, ld_residual] of dtype; then h, [n_rows, ld_h]
+ *                of dtype, receives the sum (it may be the residual's own
+ *                buffer, or x's).
+ *  weight        [width] of weight_dtype: dtype or BIL_F32.
+ *  eps           finite, >= 0.
+ *  y             [n_rows, ld_y] of dtype.
+ *  rstd          [n_rows] float32 for the backward, or NULL.
+ * Rows need no alignment beyond their element's (a read may take the rest of a
+ * 16-byte unit that holds an element of the row, a write never does); rows on
+ * 16-byte boundaries are read and written fastest.
+ */
+int bil_rms_norm_fwd(const void *x, const void *residual, const void *weight, int dtype, int weight_dtype,
+                     int64_t n_rows, int64_t width, int64_t ld_x, int64_t ld_residual, float eps, void *y,
+                     int64_t ld_y, void *h, int64_t ld_h, float *rstd, bil_stream_t stream);
+
+/*
+ * bil_rms_norm_quant -- the same norm with an output in 8 bits and a scale per
+ * row, as bil_linear_logp_fp8_fwd reads it: with y as above in float32 (not
+ * rounded) and a = max(max_c |y_c|, 2^-100),
+ *     scale = a / 448,   q_c = e4m3(y_c * (448 / a))   (to nearest even)
+ * so that q_c * scale stands for y_c.  A NaN, or an infinity in the row, makes
+ * every q_c * scale of the row NaN.
+ *
+ *  q             [n_rows, ld_q] bytes.
+ *  scale         [n_rows] float32, > 0 (NaN or infinite for such a row).
+ * Other arguments as for bil_rms_norm_fwd.
+ */
+int bil_rms_norm_quant(const void *x, const void *residual, const void *weight, int dtype, int weight_dtype,
+                       int64_t n_rows, int64_t width, int64_t ld_x, int64_t ld_residual, float eps, void *q,
+                       int64_t ld_q, float *scale, void *h, int64_t ld_h, bil_stream_t stream);
+
+/*
+ * bil_quantize_rows -- q and scale of bil_rms_norm_quant for y = x: the 8-bit
+ * form of a weight, once per weight.  Arguments as there.
+ */
+int bil_quantize_rows(const void *x, int dtype, int64_t n_rows, int64_t width, int64_t ld_x, void *q, int64_t ld_q,
+                      float *scale, bil_stream_t stream);
+
+/*
+ * bil_rms_norm_bwd_workspace_bytes -- bytes of device workspace that
+ * bil_rms_norm_bwd needs on the current device for n_rows rows of `width`.
+ */
+int bil_rms_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int64_t *bytes);
+
+/*
+ * bil_rms_norm_bwd -- backward of bil_rms_norm_fwd.  With u = h * rstd and
+ * v = dy * weight:
+ *     dx = rstd * (v - u * mean_c(v u)) + dh,   dweight = sum over rows of dy * u
+ * dx is the gradient of x and of the residual alike.  dx's bits depend on the
+ * row alone; dweight's are reproducible for a given n_rows on a given GPU (its
+ * rows are summed in a fixed order, no atomics).
+ *
+ *  dy            [n_rows, ld_dy] of dtype: the gradient of y.
+ *  h             [n_rows, ld_h]: the forward's h (x where it had no residual).
+ *  rstd          [n_rows]: the forward's.
+ *  dh            NULL, or [n_rows, ld_dh] of dtype: the gradient of h as an
+ *                output of its own (the residual stream going on).
+ *  dx            [n_rows, ld_dx] of dtype (it may be dy's, or dh's buffer).
+ *  dweight       [width] float32.  n_rows = 0 sets it to zero.
+ *  workspace     16-byte aligned device memory of at least
+ *                bil_rms_norm_bwd_workspace_bytes bytes; two calls in flight at
+ *                once need two.
+ */
+int bil_rms_norm_bwd(const void *dy, const void *h, const void *weight, const float *rstd, const void *dh, int dtype,
+                     int weight_dtype, int64_t n_rows, int64_t width, int64_t ld_dy, int64_t ld_h, int64_t ld_dh,
+                     void *dx, int64_t ld_dx, float *dweight, void *workspace, int64_t workspace_bytes,
+                     bil_stream_t stream);
+
 /*
  * bil_sum_f32 -- dst[i] = ((srcs[0][i] + srcs[1][i]) + srcs[2][i]) + ... for
  * i < n: float32 sums in the order of `srcs` (1 <= count <= 16; `srcs` is a

@@ -34,3 +34,11 @@ from .logp import (  # noqa: F401
     logp_tile_partials,
     watchdog_status,
 )
+from .norm import (  # noqa: F401
+    RMSNorm,
+    quantize_rows,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_quant,
+)

@@ -17,6 +17,7 @@ MAX_TILE_BYTES = 64 * 1024
 MAX_FUSED_TILES = 2048
 MAX_EXTENT_BYTES = 1 << 48
 LINEAR_TILE_V = 256
+MAX_NORM_WIDTH = 16384
 LINEAR_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 LAYOUT_K_MAJOR, LAYOUT_MN_MAJOR = 0, 1
 
@@ -48,6 +49,12 @@ SIGNATURES = {
     "bil_linear_gemm": (_i32, [_p, _i32, _p, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i32, _i64, _p]),
     "bil_linear_logp_fp8_fwd": (_i32, [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p, _p, _p, _i32,
                                        _i64, _p, _i64, _i32, _p]),
+    "bil_rms_norm_fwd": (_i32, [_p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _i64, _p, _p]),
+    "bil_rms_norm_quant": (_i32, [_p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p, _i64, _p]),
+    "bil_quantize_rows": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _p]),
+    "bil_rms_norm_bwd_workspace_bytes": (_i32, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "bil_rms_norm_bwd": (_i32, [_p, _p, _p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i64,
+                                _p]),
     "bil_sum_f32": (_i32, [ctypes.POINTER(ctypes.c_void_p), _i32, _i64, _p, _p]),
     "bil_probe_exp_rate": (_i32, [ctypes.c_int32, ctypes.c_int32, _p, _p, _p]),
     "bil_linear_logp_fwd_static": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p, _p, _i32,
