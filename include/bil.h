@@ -217,6 +217,64 @@ int bil_logp_bwd(const void *logits, int dtype, int64_t n_rows, int64_t vocab, i
                  const float *grad_entropy, void *dlogits, int dlogits_dtype, int64_t ld_out,
                  int64_t out_cols, bil_stream_t stream);
 
+/* Most alternatives of a row (k) that the calls below take. */
+#define BIL_MAX_TOPK 128
+
+/*
+ * bil_logp_topk_workspace_bytes -- bytes of device workspace that
+ * bil_logp_topk_fwd needs on the current device (entropy != 0: with the
+ * entropy output): the tiles' partials and the candidates of the parts a row is
+ * cut into.
+ */
+int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, int32_t k, int entropy,
+                                  int64_t *bytes);
+
+/*
+ * bil_logp_topk_fwd -- bil_logp_fwd with the row's k largest alternatives, in
+ * one pass over the logits.  logp, lse and entropy are bil_logp_fwd's bits for
+ * the same tile_v.  The alternatives are the first k columns of [0, vocab) in
+ * the order of (stored logit descending, column ascending); -0 equals +0, and a
+ * NaN counts as less than -inf.  Alternative j has log-probability
+ * z_{ids_j} - LSE, rounded as logp is (the target's equals logp bit for bit).
+ *
+ *  k             1 <= k <= min(vocab, BIL_MAX_TOPK) (BIL_E_INVALID_ARG above the
+ *                vocabulary, BIL_E_UNSUPPORTED above BIL_MAX_TOPK).
+ *  top_ids       [n_rows, k] int64 columns, best first; -1 for ignored rows.
+ *  top_logp      [n_rows, k] float32; +0.0 for ignored rows.  (A row whose target
+ *                is outside the vocabulary has its alternatives all the same.)
+ *  workspace     256-byte aligned device memory of at least
+ *                bil_logp_topk_workspace_bytes bytes, scratch; two calls in
+ *                flight at once need two.
+ * vocab and n_rows up to 2^31 - 1, at most BIL_MAX_FUSED_TILES tiles.  Other
+ * arguments as for bil_logp_fwd.
+ */
+int bil_logp_topk_fwd(const void *logits, int dtype, int64_t n_rows, int64_t vocab, int64_t ld,
+                      const int64_t *target_ids, int64_t ignore_index, int32_t tile_v, float temperature, int32_t k,
+                      float *logp, float *lse, float *entropy, int64_t *top_ids, float *top_logp, void *workspace,
+                      int64_t workspace_bytes, int validate, bil_stream_t stream);
+
+/*
+ * bil_logp_topk_bwd -- backward of bil_logp_topk_fwd: the gradient of
+ * g * logp + sum_j gk_j * top_logp_j + gh * H with respect to the stored logits,
+ *     W = g [c = t] + sum_j gk_j [c = ids_j],  G = g + sum_j gk_j
+ *     d_c = (W - G p - gh (p (a + H))) [* rcp],  a = z - lse, p = exp(a)
+ * Columns with W = 0 and no part in the row's list get bil_logp_bwd's bits for
+ * the upstream gradient G.  An entry of top_ids outside [0, vocab) adds to G
+ * and to no column; a column named more than once gets the sum.
+ *
+ *  top_ids       [n_rows, k] int64: the forward's, or any other columns whose
+ *                log-probabilities were taken against the same lse.
+ *  grad_top      [n_rows, k] float32: gk.
+ *  workspace     [n_rows] float32 device scratch (receives G).
+ * Other arguments as for bil_logp_bwd (ignored rows are +0.0, rows whose target
+ * is outside the vocabulary NaN).
+ */
+int bil_logp_topk_bwd(const void *logits, int dtype, int64_t n_rows, int64_t vocab, int64_t ld,
+                      const int64_t *target_ids, int64_t ignore_index, float temperature, const int64_t *top_ids,
+                      int32_t k, const float *lse, const float *grad_logp, const float *grad_top, const float *entropy,
+                      const float *grad_entropy, void *dlogits, int dlogits_dtype, int64_t ld_out, int64_t out_cols,
+                      float *workspace, bil_stream_t stream);
+
 /*
  * bil_stream_shape -- the pipeline shape the forward and tile-partials kernels
  * use for a tile of tile_v elements of `dtype` (fused != 0: the fused forward

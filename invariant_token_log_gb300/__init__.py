@@ -42,3 +42,9 @@ from .norm import (  # noqa: F401
     rms_norm_fwd,
     rms_norm_quant,
 )
+from .topk import (  # noqa: F401
+    BatchInvariantLogpTopk,
+    batch_invariant_logp_topk,
+    logp_topk,
+    logp_topk_bwd,
+)

@@ -17,6 +17,7 @@ MAX_TILE_BYTES = 64 * 1024
 MAX_FUSED_TILES = 2048
 MAX_EXTENT_BYTES = 1 << 48
 LINEAR_TILE_V = 256
+MAX_TOPK = 128
 MAX_NORM_WIDTH = 16384
 LINEAR_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 LAYOUT_K_MAJOR, LAYOUT_MN_MAJOR = 0, 1
@@ -33,6 +34,12 @@ SIGNATURES = {
     "bil_logp_merge": (_i32, [_p, _p, _p, _i64, ctypes.c_int32, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i32, _p]),
     "bil_logp_bwd": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _f, _p, _p, _p, _p, _p, _i32, _i64, _i64,
                             _p]),
+    "bil_logp_topk_workspace_bytes": (_i32, [_i32, _i64, _i64, ctypes.c_int32, ctypes.c_int32, _i32,
+                                             ctypes.POINTER(_i64)]),
+    "bil_logp_topk_fwd": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, ctypes.c_int32, _f, ctypes.c_int32, _p, _p, _p, _p,
+                                 _p, _p, _i64, _i32, _p]),
+    "bil_logp_topk_bwd": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _f, _p, ctypes.c_int32, _p, _p, _p, _p, _p, _p,
+                                 _i32, _i64, _i64, _p, _p]),
     "bil_stream_shape": (_i32, [_i32, ctypes.c_int32, _i64, _i32, _i32, ctypes.POINTER(_i32),
                                 ctypes.POINTER(_i32), ctypes.POINTER(_i64)]),
     "bil_watchdog_status": (_i32, [ctypes.POINTER(_u), _i32]),

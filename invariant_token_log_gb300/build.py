@@ -18,7 +18,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bil.cu", "linear.cu", "norm.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bil.cu", "linear.cu", "norm.cu", "topk.cu")]
 HEADERS = [os.path.join(ROOT, "include", "bil.h")] + [
     os.path.join(HERE, "csrc", f) for f in ("device_common.cuh", "launch.cuh", "logp_device.cuh", "internal.h")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

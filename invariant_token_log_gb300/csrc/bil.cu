@@ -16,7 +16,8 @@
 //   merge_kernel                fixed-order merge of [N, T] partials -> logp, lse.
 //   bwd_kernel                  dlogits = g * (onehot - exp(x - lse)); rows aligned,
 //                               at offsets shared by input and output, or scalar.
-// The fused LM-head is in linear.cu.
+// The fused LM-head is in linear.cu, the forward with the row's largest
+// alternatives in topk.cu, the norm in norm.cu.
 //
 // The forward streams each row exactly once.  A producer warp moves whole
 // tiles HBM -> shared memory with 1-D bulk asynchronous copies
@@ -646,6 +647,9 @@ int bil_watchdog_status(unsigned int* flags, int clear) {
   unsigned int linear = 0;
   if (int st = bil_internal::linear_watchdog(&linear, clear)) return st;
   *flags |= linear;
+  unsigned int topk = 0;
+  if (int st = bil_internal::topk_watchdog(&topk, clear)) return st;
+  *flags |= topk;
   return BIL_OK;
 }
 

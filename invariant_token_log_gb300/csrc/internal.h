@@ -51,4 +51,7 @@ class BIL_INTERNAL NvtxRange {
 // bil_watchdog_status); cleared when `clear` is non-zero.
 BIL_INTERNAL int linear_watchdog(unsigned int* flags, int clear);
 
+// The same of the kernels in topk.cu.
+BIL_INTERNAL int topk_watchdog(unsigned int* flags, int clear);
+
 }  // namespace bil_internal
