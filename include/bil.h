@@ -222,9 +222,8 @@ int bil_logp_bwd(const void *logits, int dtype, int64_t n_rows, int64_t vocab, i
 
 /*
  * bil_logp_topk_workspace_bytes -- bytes of device workspace that
- * bil_logp_topk_fwd needs on the current device (entropy != 0: with the
- * entropy output): the tiles' partials and the candidates of the parts a row is
- * cut into.
+ * bil_logp_topk_fwd needs (entropy != 0: with the entropy output): the tiles'
+ * partials and the maxima of their chunks.  Host arithmetic only.
  */
 int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, int32_t k, int entropy,
                                   int64_t *bytes);

@@ -3,31 +3,30 @@
 //
 // The alternatives of a row are the first k of its columns in the order of
 // (stored logit descending, column ascending), NaN last; their log-probability
-// is z - LSE, as the target's.  One pass over the logits gives everything:
+// is z - LSE, as the target's.  Two kernels:
 //
-//   topk_stream_kernel  a warp takes a contiguous run of a row's tiles (a unit:
-//                       the whole row where there are enough rows), streams
-//                       them through two shared-memory stages of its own with
-//                       bulk copies, and gives each tile's (max, sum-exp[,
-//                       entropy sum]) partial, by the library's one arithmetic
-//                       contract, and the unit's k best columns;
-//   topk_merge_kernel   a row's partials in the one fixed order (merge_lse: so
-//                       logp, lse and the entropy are bil_logp_fwd's bits) and
-//                       its units' lists into one.
+//   topk_stream_kernel  one pass over the logits.  A warp takes a run of a
+//                       row's tiles and gives each tile's (max, sum-exp[,
+//                       entropy sum]) partial by the library's one arithmetic
+//                       contract, and with it what it has on the way there: the
+//                       maximum of each lane's columns (a chunk: up to 128
+//                       columns of a 4096-column tile).
+//   topk_row_kernel     a row a block.  One warp merges the partials in the one
+//                       fixed order (merge_lse: logp, lse and the entropy are
+//                       bil_logp_fwd's bits).  Four warps find the columns from
+//                       the chunks' maxima: of 128 (k > 32: 256) groups of
+//                       chunks, the k-th largest maximum has k columns at or
+//                       above it, and few chunks reach it (about 22 columns in
+//                       as many of 1216 chunks for k = 20 of 151936), so that
+//                       only those are read again, 1.7% of the row.
 //
-// The k best are a list sorted across the warp's lanes (slot 32 r + lane), each
-// entry one 64-bit word: the logit's bits made monotone, above the column's
-// complement, so that a larger word is a better column and ties are decided.
-// A lane's maximum over a tile, which the partial needs anyway, is compared
-// with the list's k-th: most tiles past a row's first hold nothing better and
-// cost one comparison and a vote.  Otherwise the tile's groups are gone
-// through in column order, so that a column equal to the k-th never enters: a
-// row of one value costs k insertions.  A unit's first tile starts from a
-// bound instead of an empty list: the k-th largest of the 32 lanes' maxima (k
-// <= 32) has k columns at or above it.
+// The choice of columns thus costs the pass over the logits one store a tile,
+// whatever k is.  (Measured before, 4096 x 151936 bf16, k = 20: a list of the
+// best columns kept by the streaming warp, sorted across its lanes, took 437 to
+// 528 us; most of its instructions went into the columns that came in early
+// and left again.)
 //
-// Bound: HBM, one read of the logits (16384 x 151936 bf16: 4.98 GB), with the
-// issue slots of the reduction close behind.
+// Bound: HBM, one read of the logits (16384 x 151936 bf16: 4.98 GB).
 //
 //   topk_grad_sum_kernel  g + sum_j gk_j, what the softmax term is scaled by;
 //   (bil_logp_bwd)        d = -(g + sum gk) p - gh p (a + H), one pass;
@@ -43,9 +42,7 @@
 
 namespace {
 
-constexpr int kTopkStages = 2;    // stages of a warp
-constexpr int kTopkMaxWarps = 8;  // warps of a block
-constexpr int kTopkMaxUnits = 64; // units a row is cut into at most (two lists a lane in the merge)
+constexpr int kTopkMaxWarps = 8;  // warps of a block of the stream kernel
 
 typedef unsigned long long u64;
 
@@ -62,49 +59,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
-__device__ __forceinline__ u64 entry_of(uint32_t key, int64_t column) {
+// An entry: the key above the column's complement, so that a larger word is a
+// better column and no two are equal.
+__device__ __forceinline__ u64 entry_of(uint32_t key, int column) {
   return (static_cast<u64>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(column));
 }
 __device__ __forceinline__ int64_t entry_column(u64 e) { return 0xffffffffu - static_cast<uint32_t>(e); }
-
-// The best entries so far, slot 32 r + lane in v[r], descending; 0: none.
-template <int R>
-struct Best {
-  u64 v[R];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = 0;
-  }
-  __device__ __forceinline__ void insert(u64 c, int lane) {
-    int pos = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) pos += __popc(__ballot_sync(0xffffffffu, v[r] > c));
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-      u64 prev = __shfl_up_sync(0xffffffffu, v[r], 1);
-      if (r > 0) {
-        const u64 last = __shfl_sync(0xffffffffu, v[r > 0 ? r - 1 : 0], kLanes - 1);
-        if (lane == 0) prev = last;
-      }
-      const int slot = r * kLanes + lane;
-      if (slot >= pos) v[r] = slot == pos ? c : prev;
-    }
-  }
-  __device__ __forceinline__ u64 at(int slot) const {
-    u64 e = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (r == slot / kLanes) e = __shfl_sync(0xffffffffu, v[r], slot % kLanes);
-    return e;
-  }
-};
 
 struct TopkParams {
   const unsigned char* logits;
   int64_t n_rows, vocab, ld;
   int tile_v, num_tiles;
-  int chunk;  // tiles of a unit
-  int units;  // units of a row
+  int unit_tiles;  // tiles of a unit: what one warp of the stream kernel takes at a time
+  int units;       // units of a row
+  int tile_chunks; // chunks of a tile: its lanes that hold columns (32, or fewer in narrow tiles)
   const int64_t* targets;
   int64_t ignore_index;
   float rcp;
@@ -112,9 +80,13 @@ struct TopkParams {
   float* part_max;  // [n_rows, num_tiles]
   float* part_sum;
   float* part_ent;
-  u64* cand;  // [n_rows, units, k]
+  unsigned char* chunk_max;  // [n_rows, num_tiles, tile_chunks] of the logits' type
   unsigned stage_bytes;
 };
+
+// ---------------------------------------------------------------------------
+// The pass over the logits.
+// ---------------------------------------------------------------------------
 
 // Where a warp is in its units: unit u, tile within it.  Units of ignored
 // rows are passed over.
@@ -127,8 +99,8 @@ struct UnitCursor {
     for (; more(p); unit += stride) {
       row = unit / p.units;
       if (p.targets[row] == p.ignore_index) continue;
-      tile = static_cast<int>(unit - row * p.units) * p.chunk;
-      end = min(tile + p.chunk, p.num_tiles);
+      tile = static_cast<int>(unit - row * p.units) * p.unit_tiles;
+      end = min(tile + p.unit_tiles, p.num_tiles);
       return;
     }
   }
@@ -139,85 +111,87 @@ struct UnitCursor {
   }
 };
 
-// The tile's columns that are better than the list's k-th, into the list.
-// tk: the smallest key that enters (kept up to date).
-template <int DT, int WOFF, int R>
-__device__ __noinline__ void scan_tile_t(const unsigned char* tile, unsigned off, unsigned sh, int valid, int64_t col0,
-                                         int lane, int k, Best<R>& best, uint32_t& tk) {
+// A tile in registers: the lane's maximum, and the sums for the tile's maximum
+// (the operations of tile_reduce_regs_t, in its order).
+template <int DT, bool FULL>
+__device__ __forceinline__ float regs_max(const TileRegs<DT>& r, int valid, int lane) {
+  const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
+  uint32_t mx[Group<DT>::kW];
+  Group<DT>::max_init(mx);
+#pragma unroll
+  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i)
+    if (FULL || i < ng) Group<DT>::max_acc(mx, r.w[i]);
+  return Group<DT>::max_fin(mx);
+}
+
+template <int DT, bool FULL, bool ENT>
+__device__ __forceinline__ TilePartial regs_sums(const TileRegs<DT>& r, int valid, int lane, float mx_all, float rcp) {
+  const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
+  const float m = rcp == 1.0f ? mx_all : __fmul_rn(mx_all, rcp);
+  const float shift = (mx_all == -INFINITY) ? 0.0f : mx_all;
+  const float c = __fmul_rn(rcp, kLog2e);
+  const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
+  uint64_t a[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i)
+    if (FULL || i < ng) Group<DT>::template sum_acc<ENT, false>(a, u, r.w[i], shift2, c2);
+  return finish_tile<ENT>(m, a, u);
+}
+
+// The lane's maximum of a tile in shared memory (tiles past what registers hold).
+template <int DT, int WOFF>
+__device__ __forceinline__ float smem_max_t(const unsigned char* tile, int valid, int lane, unsigned sh) {
   const int groups = (valid + kGroup - 1) / kGroup;
   const int rem = valid % kGroup;
-  for (int g0 = 0; g0 < groups; g0 += kLanes) {
-    const int g = g0 + lane;
-    uint32_t key = 0;
-    if (g < groups) {
-      uint32_t w[Group<DT>::kW], mx[Group<DT>::kW];
-      load_group<DT, WOFF>(tile, g, sh, w);
-      if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
-      Group<DT>::max_init(mx);
-      Group<DT>::max_acc(mx, w);
-      key = order_key(Group<DT>::max_fin(mx));
-    }
-    unsigned mask = __ballot_sync(0xffffffffu, g < groups && key >= tk);
-    while (mask != 0u) {
-      const int src = __ffs(mask) - 1;
-      mask &= mask - 1;
-      const int e0 = (g0 + src) * kGroup, e = e0 + lane;
-      const bool in = lane < kGroup && e < valid;
-      const uint32_t ek = in ? order_key(Elem<DT>::one(tile + off + static_cast<size_t>(e) * Elem<DT>::kBytes)) : 0u;
-      unsigned sub = __ballot_sync(0xffffffffu, in && ek >= tk);
-      while (sub != 0u) {
-        const int j = __ffs(sub) - 1;
-        sub &= sub - 1;
-        const uint32_t kj = __shfl_sync(0xffffffffu, ek, j);
-        if (kj < tk) continue;  // the bound has risen
-        best.insert(entry_of(kj, col0 + e0 + j), lane);
-        const u64 kth = best.at(k - 1);
-        if (kth != 0) tk = static_cast<uint32_t>(kth >> 32) + 1u;
-      }
-    }
+  uint32_t mx[Group<DT>::kW];
+  Group<DT>::max_init(mx);
+  for (int g = lane; g < groups; g += kLanes) {
+    uint32_t w[Group<DT>::kW];
+    load_group<DT, WOFF>(tile, g, sh, w);
+    if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+    Group<DT>::max_acc(mx, w);
   }
+  return Group<DT>::max_fin(mx);
 }
 
-template <int DT, bool SHIFTED, int R>
-__device__ __forceinline__ void scan_tile(const unsigned char* tile, unsigned off, int valid, int64_t col0, int lane,
-                                          int k, Best<R>& best, uint32_t& tk) {
+template <int DT, bool SHIFTED>
+__device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, int lane, unsigned off) {
   const unsigned sh = 8u * (off & 3u);
-  if (!SHIFTED || off == 0) return scan_tile_t<DT, -1, R>(tile, 0, 0, valid, col0, lane, k, best, tk);
+  if (!SHIFTED || off == 0) return smem_max_t<DT, -1>(tile, valid, lane, 0);
   switch (off >> 2) {
-    case 0: return scan_tile_t<DT, 0, R>(tile, off, sh, valid, col0, lane, k, best, tk);
-    case 1: return scan_tile_t<DT, 1, R>(tile, off, sh, valid, col0, lane, k, best, tk);
-    case 2: return scan_tile_t<DT, 2, R>(tile, off, sh, valid, col0, lane, k, best, tk);
-    default: return scan_tile_t<DT, 3, R>(tile, off, sh, valid, col0, lane, k, best, tk);
+    case 0: return smem_max_t<DT, 0>(tile, valid, lane, sh);
+    case 1: return smem_max_t<DT, 1>(tile, valid, lane, sh);
+    case 2: return smem_max_t<DT, 2>(tile, valid, lane, sh);
+    default: return smem_max_t<DT, 3>(tile, valid, lane, sh);
   }
 }
 
-// The k-th largest (k <= 32) of the lanes' keys, in every lane.
-__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t key, int k, int lane) {
-  int above = 0;
-#pragma unroll
-  for (int j = 0; j < kLanes; ++j) {
-    const uint32_t o = __shfl_sync(0xffffffffu, key, j);
-    above += (o > key || (o == key && j < lane)) ? 1 : 0;
-  }
-  const int src = __ffs(__ballot_sync(0xffffffffu, above == k - 1)) - 1;
-  return __shfl_sync(0xffffffffu, key, src);
+// A maximum of stored values, in their type (exact).
+template <int DT>
+__device__ __forceinline__ void store_value(unsigned char* base, int64_t i, float v) {
+  if (DT == BIL_F32)
+    reinterpret_cast<float*>(base)[i] = v;
+  else if (DT == BIL_BF16)
+    reinterpret_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<__half*>(base)[i] = __float2half_rn(v);
 }
 
-template <int DT, bool ALIGNED, bool ENT, int R>
+template <int DT, bool ALIGNED, bool ENT>
 __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(const TopkParams p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ uint64_t full_bars[kTopkMaxWarps][kTopkStages];
+  __shared__ uint64_t full_bars[kTopkMaxWarps];
   __shared__ int abort_flag;
   constexpr int EB = Elem<DT>::kBytes;
   const int warp = threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
   const int warps = blockDim.x / kLanes;
   volatile int* abort = &abort_flag;
-  uint64_t* full = full_bars[warp];
-  unsigned char* ring = smem_raw + static_cast<size_t>(warp) * kTopkStages * p.stage_bytes;
+  uint64_t* full = &full_bars[warp];
+  unsigned char* stage = smem_raw + static_cast<size_t>(warp) * p.stage_bytes;
   if (threadIdx.x == 0) *abort = 0;
   if (lane == 0) {
-    for (int s = 0; s < kTopkStages; ++s) mbar_init(&full[s], 1);
+    mbar_init(full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -226,76 +200,50 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
 
   // Consecutive units go to different blocks.
   const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
-  const int64_t first = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
   const uint64_t policy = evict_first_policy();
-  UnitCursor ahead{first, 0, 0, 0}, at{first, 0, 0, 0};
-  ahead.settle(p, stride);
-  at = ahead;
-  int64_t issued = 0, taken = 0;
+  UnitCursor at{static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, 0, 0, 0};
+  at.settle(p, stride);
 
-  // The next tile's copy into stage issued % 2 (its last reader is done).  The
-  // 16-byte aligned span that covers the tile, as in the streaming forward.
-  auto issue = [&]() {
-    if (!ahead.more(p)) return;
-    if (lane == 0) {
-      const int64_t col0 = static_cast<int64_t>(ahead.tile) * p.tile_v;
-      const int valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - col0));
-      const unsigned char* src = p.logits + (ahead.row * p.ld + col0) * EB;
-      const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
-      const unsigned bytes = static_cast<unsigned>(align_up(off + static_cast<size_t>(valid) * EB, 16));
-      const int s = static_cast<int>(issued % kTopkStages);
-      mbar_arrive_expect_tx(&full[s], bytes);
-      bulk_g2s(ring + static_cast<size_t>(s) * p.stage_bytes, src - off, bytes, &full[s], policy);
-    }
-    ++issued;
-    ahead.next(p, stride);
-  };
-  for (int s = 0; s < kTopkStages; ++s) issue();
-
-  Best<R> best;
-  best.clear();
-  uint32_t tk = 0;
-  bool start = true;
-  while (at.more(p)) {
-    const int s = static_cast<int>(taken % kTopkStages);
-    if (!warp_wait(&full[s], static_cast<unsigned>((taken / kTopkStages) & 1), abort, kWatchFull)) break;
-    ++taken;
-    const int64_t col0 = static_cast<int64_t>(at.tile) * p.tile_v;
+  // The copy of the tile at `c` into the warp's stage (its last reader is
+  // done): the 16-byte aligned span that covers the tile, as in the streaming
+  // forward.
+  auto issue = [&](const UnitCursor& c) {
+    if (lane != 0 || !c.more(p)) return;
+    const int64_t col0 = static_cast<int64_t>(c.tile) * p.tile_v;
     const int valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - col0));
-    const unsigned char* src = p.logits + (at.row * p.ld + col0) * EB;
+    const unsigned char* src = p.logits + (c.row * p.ld + col0) * EB;
     const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
-    const unsigned char* tile = ring + static_cast<size_t>(s) * p.stage_bytes;
-    const bool in_regs = p.tile_v <= TileRegs<DT>::kMaxTile;
+    const unsigned bytes = static_cast<unsigned>(align_up(off + static_cast<size_t>(valid) * EB, 16));
+    mbar_arrive_expect_tx(full, bytes);
+    bulk_g2s(stage, src - off, bytes, full, policy);
+  };
+  issue(at);
 
-    // candidates, given the lane's maximum over the tile
-    auto offer = [&](float lane_max) {
-      const uint32_t key = order_key(lane_max);
-      if (start && p.k <= kLanes) {
-        tk = kth_of_lanes(key, p.k, lane);
-        // a lane whose columns are all NaN, or that has none, also says -inf: no bound then
-        if (tk <= kKeyNegInf) tk = 0;
-      }
-      start = false;
-      if (__any_sync(0xffffffffu, key >= tk))
-        scan_tile<DT, !ALIGNED, R>(tile, off, valid, col0, lane, p.k, best, tk);
-    };
-
+  unsigned parity = 0;
+  bool ok = true;
+  while (at.more(p)) {
+    ok = warp_wait(full, parity, abort, kWatchFull);
+    if (!ok) break;
+    parity ^= 1u;
+    const UnitCursor now = at;
+    at.next(p, stride);
+    const int64_t col0 = static_cast<int64_t>(now.tile) * p.tile_v;
+    const int valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - col0));
+    const unsigned char* src = p.logits + (now.row * p.ld + col0) * EB;
+    const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
+    const int64_t o = now.row * p.num_tiles + now.tile;
     TilePartial tp;
-    if (in_regs) {
+    float lane_max;
+    if (p.tile_v <= TileRegs<DT>::kMaxTile) {
+      const bool whole = valid == TileRegs<DT>::kMaxTile;
       TileRegs<DT> regs;
-      tile_load_regs<DT, !ALIGNED>(tile, valid, lane, regs, off);
-      {
-        const int ng = lane_groups(valid, lane);
-        uint32_t mx[Group<DT>::kW];
-        Group<DT>::max_init(mx);
-#pragma unroll
-        for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i)
-          if (i < ng) Group<DT>::max_acc(mx, regs.w[i]);
-        offer(Group<DT>::max_fin(mx));
-      }
+      tile_load_regs<DT, !ALIGNED>(stage, valid, lane, regs, off);
       __syncwarp();  // the stage has been read
-      issue();
-      tp = tile_reduce_regs<DT, ENT, false>(regs, valid, lane, p.rcp);
+      issue(at);
+      lane_max = whole ? regs_max<DT, true>(regs, valid, lane) : regs_max<DT, false>(regs, valid, lane);
+      const float mx_all = warp_max(lane_max);
+      tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
+                 : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
       if (ENT && tp.u != tp.u) {  // as in the streaming forward: u from a clamped pass
         if (ALIGNED) {
           tile_load_regs<DT>(src, valid, lane, regs);
@@ -305,59 +253,315 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
         tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
       }
     } else {
-      float m = -INFINITY;
-      for (int e = lane; e < valid; e += kLanes) m = fmaxf(m, Elem<DT>::one(tile + off + static_cast<size_t>(e) * EB));
-      offer(m);
-      tp = tile_reduce_smem<DT, ENT, !ALIGNED>(tile, valid, lane, p.rcp, off);
+      lane_max = smem_max<DT, !ALIGNED>(stage, valid, lane, off);
+      tp = tile_reduce_smem<DT, ENT, !ALIGNED>(stage, valid, lane, p.rcp, off);
       __syncwarp();
-      issue();
+      issue(at);
     }
+    if (lane < p.tile_chunks) store_value<DT>(p.chunk_max, o * p.tile_chunks + lane, lane_max);
     if (lane == 0) {
-      const int64_t o = at.row * p.num_tiles + at.tile;
       p.part_max[o] = tp.m;
       p.part_sum[o] = tp.s;
       if (ENT) p.part_ent[o] = tp.u;
     }
-    if (at.tile + 1 == at.end) {
-      u64* out = p.cand + at.unit * p.k;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (r * kLanes + lane < p.k) out[r * kLanes + lane] = best.v[r];
-      best.clear();
-      tk = 0;
-      start = true;
-    }
-    at.next(p, stride);
   }
-  // A warp that gave up waits (bounded) for its own copies in flight.
-  if (lane == 0) {
-    for (; taken < issued; ++taken)
-      if (!thread_wait_watch(&full[taken % kTopkStages], static_cast<unsigned>((taken / kTopkStages) & 1), abort,
-                             kWatchDrain, &g_watchdog, false))
-        break;
+  // A warp that gave up waits (bounded) for its own copy in flight.
+  if (!ok && lane == 0) thread_wait_watch(full, parity, abort, kWatchDrain, &g_watchdog, false);
+}
+
+// ---------------------------------------------------------------------------
+// The row.
+// ---------------------------------------------------------------------------
+
+constexpr int kSelWarps = 4;                     // warps that choose the columns
+constexpr int kSelThreads = kSelWarps * kLanes;
+constexpr int kRowThreads = kSelThreads + kLanes;  // and one that merges the partials
+constexpr int kCandidates = 1024;                // entries the selection holds
+constexpr int kDigitBits = 11;                   // of a pass of the radix selection
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kQueue = 2 * kLanes;               // chunks a warp holds between two rounds of reading
+
+__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSelThreads) : "memory"); }
+
+struct alignas(16) SelShared {
+  union {
+    u64 cand[kCandidates];
+    uint32_t bins[kBins];
+  };
+  uint32_t group_max[2 * kSelThreads];
+  int queue[kSelWarps][kQueue];
+  u64 merged[BIL_MAX_TOPK];
+  int count;
+  uint32_t bound;
+  int above;
+};
+static_assert(sizeof(uint32_t) * kBins <= sizeof(u64) * kCandidates, "the bins share the candidates' space");
+
+// The columns of one row by way of its chunks.
+template <int DT>
+struct RowColumns {
+  static constexpr int EB = Elem<DT>::kBytes;
+  const unsigned char* row;    // column 0
+  const unsigned char* chunks; // the row's chunk maxima
+  int vocab, tile_v, tile_chunks, num_chunks;
+  int warp, lane;
+  int* queue;
+
+  __device__ __forceinline__ uint32_t chunk_key(int c) const {
+    return order_key(Elem<DT>::one(chunks + static_cast<size_t>(c) * EB));
+  }
+  // keys of the 8 columns of a group from column c0; `n` exist (the others count as none: key 0)
+  __device__ __forceinline__ void keys8(int c0, int n, uint32_t (&key)[kGroup]) const {
+    const unsigned char* p = row + static_cast<int64_t>(c0) * EB;
+    float v[kGroup];
+    if (n == kGroup && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      uint32_t w[Group<DT>::kW];
+      Group<DT>::load(p, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t x = Group<DT>::xpair(w, j);
+        v[2 * j] = lo_of(x);
+        v[2 * j + 1] = hi_of(x);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) v[j] = j < n ? Elem<DT>::one(p + j * EB) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) key[j] = order_key(v[j]);
+  }
+  // fn(key, column) for the columns of the queue's first n chunks: half a warp a
+  // chunk, a lane a group of 8, two chunks in flight.
+  template <typename F>
+  __device__ __forceinline__ void read_queue(int n, F fn) const {
+    __syncwarp();
+    for (int i = lane / 16; i < n; i += 4) {
+      int c0[2], steps[2], cols[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool have = i + 2 * q < n;
+        const int c = queue[have ? i + 2 * q : 0];
+        const int tile = c / tile_chunks, l = c - tile * tile_chunks;
+        const int valid = min(tile_v, vocab - tile * tile_v);
+        c0[q] = tile * tile_v;
+        cols[q] = valid;
+        steps[q] = have ? l * kGroup : valid;  // first column of the chunk, in the tile
+      }
+      for (int s = (lane % 16) * kLanes * kGroup; s < tile_v; s += 16 * kLanes * kGroup) {
+        uint32_t key[2][kGroup];
+        int left[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int e = steps[q] + s;
+          left[q] = min(kGroup, cols[q] - e);
+          if (left[q] > 0) keys8(c0[q] + e, left[q], key[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (left[q] <= 0) continue;
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j)
+            if (j < left[q]) fn(key[q][j], c0[q] + steps[q] + s + j);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  // fn(key, column) for every column of the chunks whose maximum is `least` or
+  // more (the four warps share them).
+  template <typename F>
+  __device__ __forceinline__ void visit(uint32_t least, F fn) const {
+    int n = 0;
+    for (int c0 = warp * kLanes; c0 < num_chunks; c0 += kSelThreads) {
+      const int c = c0 + lane;
+      const bool in = c < num_chunks && chunk_key(c) >= least;
+      const unsigned vote = __ballot_sync(0xffffffffu, in);
+      if (vote == 0u) continue;
+      if (in) queue[n + __popc(vote & ((1u << lane) - 1u))] = c;
+      n += __popc(vote);
+      if (n > kQueue - kLanes) {
+        read_queue(n, fn);
+        n = 0;
+      }
+    }
+    if (n != 0) read_queue(n, fn);
+  }
+};
+
+// The row's k best columns, best first, into sm.merged (kSelThreads threads).
+template <int DT>
+__device__ void select_columns(const RowColumns<DT>& cols, int k, SelShared& sm) {
+  const int tid = threadIdx.x;
+  // 1. the groups' maxima: thread i has chunks i, i + 128, ...; for k > 32 in two groups, odd and even.
+  {
+    uint32_t m[2] = {0, 0};
+    int j = 0;
+    for (int c = tid; c < cols.num_chunks; c += kSelThreads, j ^= 1) m[j] = max(m[j], cols.chunk_key(c));
+    if (k <= kLanes) m[0] = max(m[0], m[1]);
+    sm.group_max[tid] = m[0];
+    if (k > kLanes) sm.group_max[kSelThreads + tid] = m[1];
+    if (tid == 0) {
+      sm.count = 0;
+      sm.bound = 0;
+    }
+  }
+  sel_sync();
+  // 2. the k-th largest of them: it has k columns at or above it (0 where there are fewer groups than k)
+  {
+    const int groups = k <= kLanes ? kSelThreads : 2 * kSelThreads;
+    for (int i = tid; i < groups; i += kSelThreads) {
+      const uint32_t mine = sm.group_max[i];
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < groups; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&sm.group_max[j]);
+        above += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
+                 (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
+      }
+      if (above == k - 1) sm.bound = mine;
+    }
+  }
+  sel_sync();
+  uint32_t least = sm.bound;  // columns with this key or more are wanted
+  auto append = [&](uint32_t key, int c) {
+    if (key < least) return;
+    const int at = atomicAdd(&sm.count, 1);
+    if (at < kCandidates) sm.cand[at] = entry_of(key, c);
+  };
+  // 3. those columns; at and below -inf the bound says nothing (a chunk of NaN also says -inf)
+  bool enough = false;  // sm.cand holds all columns >= least, k of them at least
+  if (least > kKeyNegInf) {
+    cols.visit(least, append);
+    sel_sync();
+    enough = sm.count <= kCandidates;
+  } else {
+    least = kKeyNegInf;
+  }
+  if (!enough) {
+    // Too many columns reach the bound, or there is none: the columns above it.
+    const uint32_t floor_key = least;
+    least = floor_key + 1;
+    sel_sync();
+    if (tid == 0) sm.count = 0;
+    sel_sync();
+    cols.visit(least, append);
+    sel_sync();
+    int found = sm.count;
+    sel_sync();  // every thread has read the count before any may change it
+    if (found > kCandidates) {
+      // Radix selection over the keys above floor_key, from the top digit, until few enough are left: `prefix`
+      // and above, `fixed` bits of it known.
+      uint32_t prefix = 0;
+      int fixed = 0, taken = 0;  // taken: columns above prefix's range
+      for (;;) {
+        const int bits = min(kDigitBits, 32 - fixed), shift = 32 - fixed - bits;
+        sel_sync();
+        for (int i = tid; i < kBins; i += kSelThreads) sm.bins[i] = 0;
+        sel_sync();
+        const uint32_t lo = max(least, prefix);
+        cols.visit(lo, [&](uint32_t key, int) {
+          if (key < lo || (fixed != 0 && (key >> (32 - fixed)) != (prefix >> (32 - fixed)))) return;
+          atomicAdd(&sm.bins[(key >> shift) & ((1u << bits) - 1u)], 1u);
+        });
+        sel_sync();
+        if (cols.warp == 0) {
+          // from the highest bin down: the bin that holds the k-th column
+          int sum = taken, digit = -1, before = 0;
+          for (int b0 = (1 << bits) - kLanes; b0 >= 0 && digit < 0; b0 -= kLanes) {
+            const int n = static_cast<int>(sm.bins[b0 + kLanes - 1 - cols.lane]);  // lane 0: the highest
+            int upto = n;
+#pragma unroll
+            for (int o = 1; o < kLanes; o *= 2) {
+              const int v = __shfl_up_sync(0xffffffffu, upto, o);
+              if (cols.lane >= o) upto += v;
+            }
+            const unsigned vote = __ballot_sync(0xffffffffu, sum + upto >= k);
+            if (vote != 0u) {
+              const int src = __ffs(vote) - 1;
+              digit = b0 + kLanes - 1 - src;
+              before = sum + __shfl_sync(0xffffffffu, upto - n, src);
+              found = sum + __shfl_sync(0xffffffffu, upto, src);
+            }
+            sum += __shfl_sync(0xffffffffu, upto, kLanes - 1);
+          }
+          if (cols.lane == 0) {
+            sm.bound = prefix | (static_cast<uint32_t>(max(digit, 0)) << shift);
+            sm.above = before;
+            sm.count = found;
+          }
+        }
+        sel_sync();
+        prefix = sm.bound;
+        taken = sm.above;
+        found = sm.count;  // columns >= prefix
+        fixed += bits;
+        if (found <= kCandidates || fixed == 32) break;
+      }
+      // `prefix` and above hold k columns; where even those are too many (equal logits), the ones above it
+      // are fewer than k and the rest is found below
+      least = found <= kCandidates ? max(least, prefix) : prefix + 1;
+      sel_sync();
+      if (tid == 0) sm.count = 0;
+      sel_sync();
+      cols.visit(least, append);
+      sel_sync();
+      found = sm.count;
+      sel_sync();
+    }
+    // Equal columns just below `least`, then NaN, in column order: one warp, tile by tile.
+    if (found < k) {
+      if (cols.warp == 0) {
+        uint32_t want = least - 1;
+        for (;;) {
+          for (int tile = 0; tile * cols.tile_chunks < cols.num_chunks && found < k; ++tile) {
+            const bool any = cols.lane < cols.tile_chunks &&
+                             cols.chunk_key(tile * cols.tile_chunks + cols.lane) >= max(want, kKeyNegInf);
+            if (!__any_sync(0xffffffffu, any)) continue;
+            const int valid = min(cols.tile_v, cols.vocab - tile * cols.tile_v);
+            for (int e0 = 0; e0 < valid && found < k; e0 += kLanes) {
+              const int c = tile * cols.tile_v + e0 + cols.lane;
+              const bool in = e0 + cols.lane < valid &&
+                              order_key(Elem<DT>::one(cols.row + static_cast<int64_t>(c) * Elem<DT>::kBytes)) == want;
+              const unsigned vote = __ballot_sync(0xffffffffu, in);
+              const int at = found + __popc(vote & ((1u << cols.lane) - 1u));
+              if (in && at < k) sm.cand[at] = entry_of(want, c);
+              found = min(k, found + __popc(vote));
+            }
+          }
+          if (found >= k || want == 0) break;
+          want = 0;
+        }
+        if (cols.lane == 0) sm.count = found;
+      }
+      sel_sync();
+    }
+  }
+  // 4. in order: an entry's place is the number of entries above it
+  const int n = sm.count;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const u64 mine = sm.cand[i];
+    int above = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) above += sm.cand[j] > mine ? 1 : 0;
+    if (above < k) sm.merged[above] = mine;
   }
 }
 
-// A row a block: warp 0 merges the partials, warp 1 the units' lists (each
-// sorted; every round takes the best of the heads), and both write the row.
-constexpr int kTopkMergeThreads = 2 * kLanes;
-
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(kTopkMergeThreads) topk_merge_kernel(const TopkParams p, float* logp, float* lse,
-                                                                       float* entropy, int64_t* top_ids, float* top_logp) {
-  extern __shared__ u64 lists[];  // [units, k] where a row has more than one unit
-  __shared__ u64 merged[BIL_MAX_TOPK];
+__global__ void __launch_bounds__(kRowThreads) topk_row_kernel(const TopkParams p, float* logp, float* lse,
+                                                               float* entropy, int64_t* top_ids, float* top_logp) {
+  __shared__ SelShared sm;
   __shared__ float scratch[kMergeScratch];
   __shared__ float row_lse;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
   const int64_t row = blockIdx.x;
   const int64_t t = p.targets[row];
   int64_t* ids = top_ids + row * p.k;
   float* top = top_logp + row * p.k;
   if (t == p.ignore_index) {
-    for (int j = threadIdx.x; j < p.k; j += kTopkMergeThreads) {
+    for (int j = threadIdx.x; j < p.k; j += kRowThreads) {
       ids[j] = -1;
       top[j] = 0.0f;
     }
@@ -368,7 +572,8 @@ __global__ void __launch_bounds__(kTopkMergeThreads) topk_merge_kernel(const Top
     }
     return;
   }
-  if (threadIdx.x < kLanes) {
+  const unsigned char* src = p.logits + row * p.ld * Elem<DT>::kBytes;
+  if (warp == kSelWarps) {
     const int64_t o = row * p.num_tiles;
     float H = 0.0f;
     const float L = merge_lse<ENT, true>(p.part_max + o, p.part_sum + o, ENT ? p.part_ent + o : nullptr, p.num_tiles,
@@ -377,7 +582,7 @@ __global__ void __launch_bounds__(kTopkMergeThreads) topk_merge_kernel(const Top
       row_lse = L;
       float z = __int_as_float(0x7fc00000);
       if (t >= 0 && t < p.vocab) {
-        z = Elem<DT>::one(p.logits + (row * p.ld + t) * Elem<DT>::kBytes);
+        z = Elem<DT>::one(src + t * Elem<DT>::kBytes);
         if (p.rcp != 1.0f) z = __fmul_rn(z, p.rcp);
       }
       logp[row] = __fsub_rn(z, L);
@@ -385,39 +590,21 @@ __global__ void __launch_bounds__(kTopkMergeThreads) topk_merge_kernel(const Top
       if (ENT) entropy[row] = H;
     }
   } else {
-    const u64* cand = p.cand + row * p.units * p.k;
-    if (p.units == 1) {
-      for (int j = lane; j < p.k; j += kLanes) merged[j] = cand[j];
-    } else {
-      for (int j = lane; j < p.units * p.k; j += kLanes) lists[j] = cand[j];
-      __syncwarp();
-      int h[2] = {0, 0};
-      u64 head[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int l = lane + q * kLanes;
-        head[q] = l < p.units ? lists[l * p.k] : 0;
-      }
-      for (int j = 0; j < p.k; ++j) {
-        const u64 mine = head[0] > head[1] ? head[0] : head[1];
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32));
-        const uint32_t lo = __reduce_max_sync(
-            0xffffffffu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
-        const u64 won = (static_cast<u64>(hi) << 32) | lo;
-        if (lane == 0) merged[j] = won;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (won != 0 && head[q] == won) {
-            ++h[q];
-            head[q] = h[q] < p.k ? lists[(lane + q * kLanes) * p.k + h[q]] : 0;
-          }
-        }
-      }
-    }
+    RowColumns<DT> cols;
+    cols.row = src;
+    cols.num_chunks = p.num_tiles * p.tile_chunks;
+    cols.chunks = p.chunk_max + row * cols.num_chunks * Elem<DT>::kBytes;
+    cols.vocab = static_cast<int>(p.vocab);
+    cols.tile_v = p.tile_v;
+    cols.tile_chunks = p.tile_chunks;
+    cols.warp = warp;
+    cols.lane = lane;
+    cols.queue = sm.queue[warp];
+    select_columns<DT>(cols, p.k, sm);
   }
   __syncthreads();
-  for (int j = threadIdx.x; j < p.k; j += kTopkMergeThreads) {
-    const u64 e = merged[j];
+  for (int j = threadIdx.x; j < p.k; j += kRowThreads) {
+    const u64 e = sm.merged[j];
     float z = key_value(static_cast<uint32_t>(e >> 32));
     if (p.rcp != 1.0f) z = __fmul_rn(z, p.rcp);
     ids[j] = entry_column(e);
@@ -508,56 +695,52 @@ __global__ void __launch_bounds__(BIL_MAX_TOPK + kLanes) topk_grad_fix_kernel(co
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// How the stream kernel is laid out: warps of a block, blocks of an SM.  Two
-// blocks an SM where that leaves them four warps each or more (the partials
-// need up to 128 registers a thread: 16 warps), else one block.
+// How the stream kernel is laid out: warps of a block, blocks of an SM.  One
+// stage a warp: a tile is in registers (or, past 8 KB, being reduced) while the
+// others' copies are in flight, and 16 warps (at up to 128 registers a thread)
+// keep 128 KB of them on the way, twice what the latency needs.  Two blocks an
+// SM where that leaves them four warps each or more, else one.
 constexpr size_t kSmSmemBytes = 228 * 1024;  // an SM's shared memory, 1 KB of it reserved for each block
 void stream_layout(size_t stage_bytes, int* warps, int* blocks) {
-  const size_t per_warp = kTopkStages * stage_bytes;
   for (*blocks = 2; *blocks >= 1; --*blocks) {
-    const size_t room = kSmSmemBytes / *blocks - 1024 - 256;  // 256: the barriers
-    *warps = static_cast<int>(std::min<size_t>(kTopkMaxWarps, room / per_warp));
+    const size_t room = kSmSmemBytes / *blocks - 1024 - 128;  // 128: the barriers
+    *warps = static_cast<int>(std::min<size_t>(kTopkMaxWarps, room / stage_bytes));
     if (*blocks == 1 || *warps >= 4) return;
   }
 }
 
 // Tiles of a unit: the cut of the rows that gives the least time, a warp's time
-// being its units' tiles plus three quarters of a tile a unit for the filling of
-// an empty list.  By the sizes alone (not by the alignment).
-int unit_tiles(int64_t n_rows, int num_tiles, int k, int64_t warps) {
-  const int most = std::min<int>(kTopkMaxUnits, 40 * 1024 / (8 * k));  // the merge's lists in shared memory
+// being its units' tiles and a quarter of a tile a unit for the change of row.
+int unit_tiles(int64_t n_rows, int num_tiles, int64_t warps) {
   int best = num_tiles;
   double least = 0.0;
-  for (int u = 1; u <= std::min(num_tiles, most); ++u) {
-    const int chunk = (num_tiles + u - 1) / u;
-    const int64_t units = n_rows * ((num_tiles + chunk - 1) / chunk);
-    const double cost = static_cast<double>((units + warps - 1) / warps) * (chunk + 0.75);
+  for (int u = 1; u <= std::min(num_tiles, 64); ++u) {
+    const int tiles = (num_tiles + u - 1) / u;
+    const int64_t units = n_rows * ((num_tiles + tiles - 1) / tiles);
+    const double cost = static_cast<double>((units + warps - 1) / warps) * (tiles + 0.25);
     if (u == 1 || cost < least) {
       least = cost;
-      best = chunk;
+      best = tiles;
     }
   }
   return best;
 }
 
-struct TopkPlan {
-  int chunk, units;
-  size_t part, cand, total;  // bytes: one partial array, the lists, all
-};
-
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
-int topk_plan(int dtype, int64_t n_rows, int num_tiles, int tile_v, int k, bool ent, TopkPlan* plan) {
-  int sms = 0, smem = 0;
-  if (int st = bil_internal::device_limits(&sms, &smem)) return st;
-  int warps = 0, blocks = 0;
-  stream_layout(static_cast<size_t>(tile_v) * bil_internal::elem_bytes(dtype), &warps, &blocks);
-  plan->chunk = unit_tiles(n_rows, num_tiles, k, static_cast<int64_t>(sms) * warps * blocks);
-  plan->units = (num_tiles + plan->chunk - 1) / plan->chunk;
-  plan->part = round256(static_cast<size_t>(n_rows) * num_tiles * sizeof(float));
-  plan->cand = round256(static_cast<size_t>(n_rows) * plan->units * k * sizeof(u64));
-  plan->total = plan->part * (ent ? 3 : 2) + plan->cand;
-  return BIL_OK;
+// The workspace: chunk maxima, then the partials.
+struct TopkWorkspace {
+  int tile_chunks;
+  size_t chunks, part, total;  // bytes: the chunk maxima, one partial array, all
+};
+
+TopkWorkspace topk_workspace(int dtype, int64_t n_rows, int64_t num_tiles, int tile_v, bool ent) {
+  TopkWorkspace w;
+  w.tile_chunks = std::min(kLanes, tile_v / kGroup);
+  w.chunks = round256(static_cast<size_t>(n_rows) * num_tiles * w.tile_chunks * bil_internal::elem_bytes(dtype));
+  w.part = round256(static_cast<size_t>(n_rows) * num_tiles * sizeof(float));
+  w.total = w.chunks + w.part * (ent ? 3 : 2);
+  return w;
 }
 
 // The sizes both the workspace query and the forward check.
@@ -569,46 +752,43 @@ int check_topk_sizes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, i
   return BIL_OK;
 }
 
-template <int DT, bool ALIGNED, bool ENT, int R>
-int launch_topk_t(const TopkParams& p, cudaStream_t stream) {
+template <int DT, bool ALIGNED, bool ENT>
+int launch_topk_t(TopkParams p, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp,
+                  cudaStream_t stream) {
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  p.stage_bytes =
+      static_cast<unsigned>(align_up(static_cast<size_t>(p.tile_v) * Elem<DT>::kBytes + (ALIGNED ? 0 : 16), 128));
   int warps = 0, blocks = 0;
   stream_layout(p.stage_bytes, &warps, &blocks);
-  const int64_t units = p.n_rows * p.units;
   const int64_t slots = static_cast<int64_t>(sms) * blocks;
+  p.unit_tiles = unit_tiles(p.n_rows, p.num_tiles, slots * warps);
+  p.units = (p.num_tiles + p.unit_tiles - 1) / p.unit_tiles;
+  const int64_t units = p.n_rows * p.units;
   // few units: one warp a block, so that they spread over the SMs
   warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps, (units + slots - 1) / slots)));
   const int64_t grid = std::min<int64_t>(slots, (units + warps - 1) / warps);
-  const size_t smem = static_cast<size_t>(warps) * kTopkStages * p.stage_bytes;
+  const size_t smem = static_cast<size_t>(warps) * p.stage_bytes;
   if (smem > static_cast<size_t>(smem_optin)) return BIL_E_UNSUPPORTED;
-  auto kernel = topk_stream_kernel<DT, ALIGNED, ENT, R>;
+  auto kernel = topk_stream_kernel<DT, ALIGNED, ENT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return BIL_E_CUDA;
-  return launch_pdl(kernel, grid, warps * kLanes, smem, stream, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+  if (launch_pdl(kernel, grid, warps * kLanes, smem, stream, 1, p) != cudaSuccess) return BIL_E_CUDA;
+  return launch_pdl(topk_row_kernel<DT, ENT>, p.n_rows, kRowThreads, 0, stream, 1, p, logp, lse, entropy, top_ids,
+                    top_logp) == cudaSuccess
+             ? BIL_OK
+             : BIL_E_CUDA;
 }
 
 template <int DT>
-int launch_topk(TopkParams p, bool ent, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp,
-                cudaStream_t stream) {
-  constexpr int EB = Elem<DT>::kBytes;
-  const bool vec = aligned_to(p.logits, 16) && (p.n_rows <= 1 || (p.ld * EB) % 16 == 0) && (p.tile_v * EB) % 16 == 0;
-  p.stage_bytes = static_cast<unsigned>(align_up(static_cast<size_t>(p.tile_v) * EB + (vec ? 0 : 16), 128));
-  const bool one = p.k <= kLanes;
-  int st;
+int launch_topk(const TopkParams& p, bool ent, float* logp, float* lse, float* entropy, int64_t* top_ids,
+                float* top_logp, cudaStream_t stream) {
+  const bool vec = aligned_to(p.logits, 16) && (p.n_rows <= 1 || (p.ld * Elem<DT>::kBytes) % 16 == 0);
   if (vec)
-    st = ent ? (one ? launch_topk_t<DT, true, true, 1>(p, stream) : launch_topk_t<DT, true, true, 4>(p, stream))
-             : (one ? launch_topk_t<DT, true, false, 1>(p, stream) : launch_topk_t<DT, true, false, 4>(p, stream));
-  else
-    st = ent ? (one ? launch_topk_t<DT, false, true, 1>(p, stream) : launch_topk_t<DT, false, true, 4>(p, stream))
-             : (one ? launch_topk_t<DT, false, false, 1>(p, stream) : launch_topk_t<DT, false, false, 4>(p, stream));
-  if (st) return st;
-  const size_t smem = p.units > 1 ? static_cast<size_t>(p.units) * p.k * sizeof(u64) : 0;
-  const cudaError_t e = ent ? launch_pdl(topk_merge_kernel<DT, true>, p.n_rows, kTopkMergeThreads, smem, stream, 1, p,
-                                         logp, lse, entropy, top_ids, top_logp)
-                            : launch_pdl(topk_merge_kernel<DT, false>, p.n_rows, kTopkMergeThreads, smem, stream, 1, p,
-                                         logp, lse, entropy, top_ids, top_logp);
-  return e == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+    return ent ? launch_topk_t<DT, true, true>(p, logp, lse, entropy, top_ids, top_logp, stream)
+               : launch_topk_t<DT, true, false>(p, logp, lse, entropy, top_ids, top_logp, stream);
+  return ent ? launch_topk_t<DT, false, true>(p, logp, lse, entropy, top_ids, top_logp, stream)
+             : launch_topk_t<DT, false, false>(p, logp, lse, entropy, top_ids, top_logp, stream);
 }
 
 template <int DT>
@@ -645,9 +825,7 @@ int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int3
   if (bytes == nullptr) return BIL_E_INVALID_ARG;
   int64_t num_tiles = 0;
   if (int st = check_topk_sizes(dtype, n_rows, vocab, tile_v, k, &num_tiles)) return st;
-  TopkPlan plan;
-  if (int st = topk_plan(dtype, n_rows, static_cast<int>(num_tiles), tile_v, k, entropy != 0, &plan)) return st;
-  *bytes = static_cast<int64_t>(plan.total);
+  *bytes = static_cast<int64_t>(topk_workspace(dtype, n_rows, num_tiles, tile_v, entropy != 0).total);
   return BIL_OK;
 }
 
@@ -673,9 +851,8 @@ int bil_logp_topk_fwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
       !aligned_to(top_logp, 4) || !aligned_to(workspace, 256))
     return BIL_E_ALIGN;
   const bool ent = entropy != nullptr;
-  TopkPlan plan;
-  if (int st = topk_plan(dtype, n_rows, static_cast<int>(num_tiles), tile_v, k, ent, &plan)) return st;
-  if (workspace_bytes < static_cast<int64_t>(plan.total)) return BIL_E_INVALID_ARG;
+  const TopkWorkspace w = topk_workspace(dtype, n_rows, num_tiles, tile_v, ent);
+  if (workspace_bytes < static_cast<int64_t>(w.total)) return BIL_E_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
@@ -688,16 +865,15 @@ int bil_logp_topk_fwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
   p.ld = ld;
   p.tile_v = tile_v;
   p.num_tiles = static_cast<int>(num_tiles);
-  p.chunk = plan.chunk;
-  p.units = plan.units;
+  p.tile_chunks = w.tile_chunks;
   p.targets = target_ids;
   p.ignore_index = ignore_index;
   p.rcp = rcp;
   p.k = k;
-  p.cand = reinterpret_cast<u64*>(ws);
-  p.part_max = reinterpret_cast<float*>(ws + plan.cand);
-  p.part_sum = reinterpret_cast<float*>(ws + plan.cand + plan.part);
-  p.part_ent = ent ? reinterpret_cast<float*>(ws + plan.cand + 2 * plan.part) : nullptr;
+  p.chunk_max = ws;
+  p.part_max = reinterpret_cast<float*>(ws + w.chunks);
+  p.part_sum = reinterpret_cast<float*>(ws + w.chunks + w.part);
+  p.part_ent = ent ? reinterpret_cast<float*>(ws + w.chunks + 2 * w.part) : nullptr;
   switch (dtype) {
     case BIL_BF16: return launch_topk<BIL_BF16>(p, ent, logp, lse, entropy, top_ids, top_logp, s);
     case BIL_F16: return launch_topk<BIL_F16>(p, ent, logp, lse, entropy, top_ids, top_logp, s);

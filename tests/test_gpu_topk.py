@@ -204,6 +204,24 @@ def test_nan(k, dtype):
     check(x, targets(6, vocab, 11), k)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("k", [1, 20, 33, 128])
+def test_concentrated_columns(k, dtype):
+    """Thousands of large logits where few lanes of few tiles hold them, distinct, few-valued and equal: the
+    columns above any bound taken over lanes are many."""
+    vocab = 40000
+    x = rows(6, vocab, dtype, 12, scale=1.0)
+    c = torch.arange(vocab, device="cuda")
+    lane, tile = c // 8 % 32, c // 4096
+    noise = torch.rand(vocab, generator=gen(13), device="cuda")
+    for r, (lanes, tiles) in enumerate(((10, 1), (10, 10), (1, 10), (32, 1))):
+        where = (lane < lanes) & (tile < tiles)
+        x[r] = torch.where(where, 50 + 100 * noise, x[r].float()).to(dtype)
+    x[4] = torch.where(lane < 5, 60 + (4 * noise).floor(), x[4].float()).to(dtype)
+    x[5] = torch.where((lane == 7) & (tile > 4), torch.full_like(noise, 40.0), x[5].float()).to(dtype)
+    check(x, targets(6, vocab, 12), k)
+
+
 @pytest.mark.parametrize("n", [3, 200, 3000])
 def test_rows_bitwise_across_batches(n):
     """A row's results do not depend on how the batch is cut."""
