@@ -8,23 +8,24 @@
 //   topk_stream_kernel  one pass over the logits.  A warp takes a run of a
 //                       row's tiles and gives each tile's (max, sum-exp[,
 //                       entropy sum]) partial by the library's one arithmetic
-//                       contract, and with it what it has on the way there: the
-//                       maximum of each lane's columns (a chunk: up to 128
-//                       columns of a 4096-column tile).
-//   topk_row_kernel     a row a block.  One warp merges the partials in the one
-//                       fixed order (merge_lse: logp, lse and the entropy are
-//                       bil_logp_fwd's bits).  Four warps find the columns from
+//                       contract, and the maximum of every 64 columns (a
+//                       chunk), which it reduces on the way to the tile's.
+//   topk_row_kernel     the row.  The partials are merged in the one fixed
+//                       order (merge_lse: logp, lse and the entropy are
+//                       bil_logp_fwd's bits).  The columns are found by way of
 //                       the chunks' maxima: of 128 (k > 32: 256) groups of
 //                       chunks, the k-th largest maximum has k columns at or
-//                       above it, and few chunks reach it (about 22 columns in
-//                       as many of 1216 chunks for k = 20 of 151936), so that
-//                       only those are read again, 1.7% of the row.
+//                       above it, and few chunks reach it (about 22 of 2374 for
+//                       k = 20 of 151936 columns), so that only those are read
+//                       again: 22 lines of 128 bytes.
 //
-// The choice of columns thus costs the pass over the logits one store a tile,
-// whatever k is.  (Measured before, 4096 x 151936 bf16, k = 20: a list of the
-// best columns kept by the streaming warp, sorted across its lanes, took 437 to
-// 528 us; most of its instructions went into the columns that came in early
-// and left again.)
+// The choice of columns thus costs the pass over the logits little, whatever k
+// is.  Measured otherwise, 4096 x 151936 bf16, k = 20: a list of the best
+// columns kept by the streaming warp, sorted across its lanes, 437 to 528 us
+// (most of its instructions went into columns that came in early and left
+// again); chunks of a lane's 128 columns, whose maximum the lane has anyway, 240
+// to 265 us (they lie in 16 places 512 bytes apart, and the row kernel was bound
+// by the 45 KB of DRAM lines it read again per row).
 //
 // Bound: HBM, one read of the logits (16384 x 151936 bf16: 4.98 GB).
 //
@@ -43,6 +44,7 @@
 namespace {
 
 constexpr int kTopkMaxWarps = 8;  // warps of a block of the stream kernel
+constexpr int kChunk = 64;        // columns of a chunk
 
 typedef unsigned long long u64;
 
@@ -72,7 +74,7 @@ struct TopkParams {
   int tile_v, num_tiles;
   int unit_tiles;  // tiles of a unit: what one warp of the stream kernel takes at a time
   int units;       // units of a row
-  int tile_chunks; // chunks of a tile: its lanes that hold columns (32, or fewer in narrow tiles)
+  int tile_chunks; // chunks of a tile
   const int64_t* targets;
   int64_t ignore_index;
   float rcp;
@@ -80,7 +82,8 @@ struct TopkParams {
   float* part_max;  // [n_rows, num_tiles]
   float* part_sum;
   float* part_ent;
-  unsigned char* chunk_max;  // [n_rows, num_tiles, tile_chunks] of the logits' type
+  unsigned char* chunk_max;  // [n_rows, num_tiles, tile_chunks] of the logits' type, -inf up to the row's pitch
+  int64_t chunk_pitch;       // bytes of a row of chunk maxima, a multiple of 16
   unsigned stage_bytes;
 };
 
@@ -111,19 +114,95 @@ struct UnitCursor {
   }
 };
 
-// A tile in registers: the lane's maximum, and the sums for the tile's maximum
-// (the operations of tile_reduce_regs_t, in its order).
-template <int DT, bool FULL>
-__device__ __forceinline__ float regs_max(const TileRegs<DT>& r, int valid, int lane) {
-  const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
-  uint32_t mx[Group<DT>::kW];
-  Group<DT>::max_init(mx);
-#pragma unroll
-  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i)
-    if (FULL || i < ng) Group<DT>::max_acc(mx, r.w[i]);
-  return Group<DT>::max_fin(mx);
+// A maximum of stored values, in their type (exact).
+template <int DT>
+__device__ __forceinline__ void store_value(unsigned char* base, int64_t i, float v) {
+  if (DT == BIL_F32)
+    reinterpret_cast<float*>(base)[i] = v;
+  else if (DT == BIL_BF16)
+    reinterpret_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<__half*>(base)[i] = __float2half_rn(v);
 }
 
+// The chunk maxima of up to kMaxTile columns (16 groups of a 16-bit type a
+// lane, 8 of float32).  Group i of lane l is columns 8 (l + 32 i) on, so chunk
+// c + 4 i is group i of the eight lanes 8 c on.  Eight registers a lane, a
+// 16-bit type's with the maxima of the groups 2 a and 2 a + 1; three exchanges
+// within the eight lanes, each halving what a lane still holds, leave register
+// l % 8 reduced in lane l: seven shuffles.
+template <int DT>
+struct ChunkMax {
+  static constexpr int EB = Elem<DT>::kBytes;
+  static constexpr int kW = Group<DT>::kW;
+  static constexpr int kGroups = EB == 4 ? 8 : 16;
+  static constexpr uint32_t kNone = EB == 4 ? Elem<DT>::kNegInf : Elem<DT>::kNegInf * 0x10001u;
+  uint32_t r[8];
+
+  __device__ static __forceinline__ uint32_t max_of(uint32_t a, uint32_t b) {
+    if constexpr (EB == 4)
+      return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else
+      return Elem<DT>::max2(a, b);
+  }
+  // a group's words to one (16-bit types: a pair whose halves are still to be compared)
+  __device__ static __forceinline__ uint32_t group(const uint32_t (&w)[kW]) {
+    uint32_t m = max_of(max_of(w[0], w[1]), max_of(w[2], w[3]));
+    if constexpr (EB == 4) m = max_of(m, max_of(max_of(w[kW - 4], w[kW - 3]), max_of(w[kW - 2], w[kW - 1])));
+    return m;
+  }
+  // groups 2 a and 2 a + 1 of a 16-bit type
+  __device__ __forceinline__ void pair(int a, uint32_t even, uint32_t odd) {
+    r[a] = max_of(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+  }
+  // Reduces, stores the chunks first + 0, 1, ... that are below `chunks`, and returns the lane's maximum.
+  __device__ __forceinline__ float finish(unsigned char* out, int first, int chunks, int lane) {
+#pragma unroll
+    for (int half = 4; half > 0; half /= 2) {
+      const bool upper = (lane & half) != 0;
+#pragma unroll
+      for (int q = 0; q < half; ++q) {
+        const uint32_t give = upper ? r[q] : r[q + half], keep = upper ? r[q + half] : r[q];
+        r[q] = max_of(keep, __shfl_xor_sync(0xffffffffu, give, half));
+      }
+    }
+    const int a = lane % 8, c = lane / 8;
+    if constexpr (EB == 4) {
+      const float v = fmaxf(-INFINITY, __uint_as_float(r[0]));  // NaN never wins
+      if (first + c + 4 * a < chunks) store_value<DT>(out, first + c + 4 * a, v);
+      return v;
+    } else {
+      float lo, hi;
+      Elem<DT>::pair(r[0], lo, hi);
+      lo = fmaxf(-INFINITY, lo);
+      hi = fmaxf(-INFINITY, hi);
+      if (first + c + 8 * a < chunks) store_value<DT>(out, first + c + 8 * a, lo);
+      if (first + c + 8 * a + 4 < chunks) store_value<DT>(out, first + c + 8 * a + 4, hi);
+      return fmaxf(lo, hi);
+    }
+  }
+};
+
+// A tile in registers: its chunk maxima, to `out`, and the lane's part of the tile's.
+template <int DT, bool FULL>
+__device__ __forceinline__ float regs_max(const TileRegs<DT>& t, int valid, int lane, unsigned char* out, int chunks) {
+  using C = ChunkMax<DT>;
+  const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
+  C c;
+#pragma unroll
+  for (int a = 0; a < 8; ++a) {
+    if constexpr (C::EB == 4) {
+      c.r[a] = FULL || a < ng ? C::group(t.w[a]) : C::kNone;
+    } else {
+      const uint32_t even = FULL || 2 * a < ng ? C::group(t.w[2 * a]) : C::kNone;
+      const uint32_t odd = FULL || 2 * a + 1 < ng ? C::group(t.w[2 * a + 1]) : C::kNone;
+      c.pair(a, even, odd);
+    }
+  }
+  return c.finish(out, 0, chunks, lane);
+}
+
+// The sums for the tile's maximum (the operations of tile_reduce_regs_t, in its order).
 template <int DT, bool FULL, bool ENT>
 __device__ __forceinline__ TilePartial regs_sums(const TileRegs<DT>& r, int valid, int lane, float mx_all, float rcp) {
   const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
@@ -138,43 +217,53 @@ __device__ __forceinline__ TilePartial regs_sums(const TileRegs<DT>& r, int vali
   return finish_tile<ENT>(m, a, u);
 }
 
-// The lane's maximum of a tile in shared memory (tiles past what registers hold).
+// The same of a tile in shared memory (tiles past what registers hold).
+// groups of the columns of a tile's chunks
+__device__ __forceinline__ int tile_groups(int chunks) { return chunks * (kChunk / kGroup); }
+
 template <int DT, int WOFF>
-__device__ __forceinline__ float smem_max_t(const unsigned char* tile, int valid, int lane, unsigned sh) {
+__device__ __forceinline__ float smem_max_t(const unsigned char* tile, int valid, int lane, unsigned sh,
+                                            unsigned char* out, int chunks) {
+  using C = ChunkMax<DT>;
   const int groups = (valid + kGroup - 1) / kGroup;
   const int rem = valid % kGroup;
-  uint32_t mx[Group<DT>::kW];
-  Group<DT>::max_init(mx);
-  for (int g = lane; g < groups; g += kLanes) {
-    uint32_t w[Group<DT>::kW];
-    load_group<DT, WOFF>(tile, g, sh, w);
-    if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
-    Group<DT>::max_acc(mx, w);
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int g0 = 0; g0 < tile_groups(chunks); g0 += C::kGroups * kLanes) {
+    C c;
+    uint32_t last = 0;
+#pragma unroll
+    for (int i = 0; i < C::kGroups; ++i) {
+      const int g = g0 + i * kLanes + lane;
+      uint32_t now = C::kNone;
+      if (g < groups) {
+        uint32_t w[Group<DT>::kW];
+        load_group<DT, WOFF>(tile, g, sh, w);
+        if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+        now = C::group(w);
+      }
+      if constexpr (C::EB == 4)
+        c.r[i % 8] = now;
+      else if (i % 2 == 1)
+        c.pair(i / 2, last, now);
+      last = now;
+    }
+    m = fmaxf(m, c.finish(out, g0 / 8, chunks, lane));
   }
-  return Group<DT>::max_fin(mx);
+  return m;
 }
 
 template <int DT, bool SHIFTED>
-__device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, int lane, unsigned off) {
+__device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, int lane, unsigned off,
+                                          unsigned char* out, int chunks) {
   const unsigned sh = 8u * (off & 3u);
-  if (!SHIFTED || off == 0) return smem_max_t<DT, -1>(tile, valid, lane, 0);
+  if (!SHIFTED || off == 0) return smem_max_t<DT, -1>(tile, valid, lane, 0, out, chunks);
   switch (off >> 2) {
-    case 0: return smem_max_t<DT, 0>(tile, valid, lane, sh);
-    case 1: return smem_max_t<DT, 1>(tile, valid, lane, sh);
-    case 2: return smem_max_t<DT, 2>(tile, valid, lane, sh);
-    default: return smem_max_t<DT, 3>(tile, valid, lane, sh);
+    case 0: return smem_max_t<DT, 0>(tile, valid, lane, sh, out, chunks);
+    case 1: return smem_max_t<DT, 1>(tile, valid, lane, sh, out, chunks);
+    case 2: return smem_max_t<DT, 2>(tile, valid, lane, sh, out, chunks);
+    default: return smem_max_t<DT, 3>(tile, valid, lane, sh, out, chunks);
   }
-}
-
-// A maximum of stored values, in their type (exact).
-template <int DT>
-__device__ __forceinline__ void store_value(unsigned char* base, int64_t i, float v) {
-  if (DT == BIL_F32)
-    reinterpret_cast<float*>(base)[i] = v;
-  else if (DT == BIL_BF16)
-    reinterpret_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
-  else
-    reinterpret_cast<__half*>(base)[i] = __float2half_rn(v);
 }
 
 template <int DT, bool ALIGNED, bool ENT>
@@ -233,15 +322,15 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
     const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
     const int64_t o = now.row * p.num_tiles + now.tile;
     TilePartial tp;
-    float lane_max;
+    unsigned char* chunks = p.chunk_max + now.row * p.chunk_pitch + static_cast<int64_t>(now.tile) * p.tile_chunks * EB;
     if (p.tile_v <= TileRegs<DT>::kMaxTile) {
       const bool whole = valid == TileRegs<DT>::kMaxTile;
       TileRegs<DT> regs;
       tile_load_regs<DT, !ALIGNED>(stage, valid, lane, regs, off);
       __syncwarp();  // the stage has been read
       issue(at);
-      lane_max = whole ? regs_max<DT, true>(regs, valid, lane) : regs_max<DT, false>(regs, valid, lane);
-      const float mx_all = warp_max(lane_max);
+      const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, chunks, p.tile_chunks)
+                                          : regs_max<DT, false>(regs, valid, lane, chunks, p.tile_chunks));
       tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
                  : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
       if (ENT && tp.u != tp.u) {  // as in the streaming forward: u from a clamped pass
@@ -253,12 +342,15 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
         tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
       }
     } else {
-      lane_max = smem_max<DT, !ALIGNED>(stage, valid, lane, off);
+      smem_max<DT, !ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks);
       tp = tile_reduce_smem<DT, ENT, !ALIGNED>(stage, valid, lane, p.rcp, off);
       __syncwarp();
       issue(at);
     }
-    if (lane < p.tile_chunks) store_value<DT>(p.chunk_max, o * p.tile_chunks + lane, lane_max);
+    if (now.tile == p.num_tiles - 1) {  // the rest of the row's last 16 bytes
+      const int pad = p.num_tiles * p.tile_chunks + lane;
+      if (pad < p.chunk_pitch / EB) store_value<DT>(p.chunk_max + now.row * p.chunk_pitch, pad, -INFINITY);
+    }
     if (lane == 0) {
       p.part_max[o] = tp.m;
       p.part_sum[o] = tp.s;
@@ -273,299 +365,400 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
 // The row.
 // ---------------------------------------------------------------------------
 
-constexpr int kSelWarps = 4;                     // warps that choose the columns
-constexpr int kSelThreads = kSelWarps * kLanes;
-constexpr int kRowThreads = kSelThreads + kLanes;  // and one that merges the partials
-constexpr int kCandidates = 1024;                // entries the selection holds
-constexpr int kDigitBits = 11;                   // of a pass of the radix selection
+// A row is taken by one warp where there are many rows (their latencies hide
+// behind each other: 32 rows at a time on an SM), or by five where there are
+// few (four choose the columns, one merges the partials).  SW: the warps that
+// choose.
+constexpr int kFewRowWarps = 4;
+constexpr int kCandidates = 512;     // entries the selection holds
+constexpr int kDigitBits = 10;       // of a pass of the radix selection
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kQueue = 2 * kLanes;               // chunks a warp holds between two rounds of reading
+constexpr int kStep = 4;             // 16-byte units of chunk maxima a lane looks at together
+constexpr int kQueue = 320;          // chunks a warp holds between two rounds of reading
+constexpr int kInFlight = 4;         // chunks eight lanes read at a time
 
-__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSelThreads) : "memory"); }
-
+template <int SW>
 struct alignas(16) SelShared {
   union {
     u64 cand[kCandidates];
     uint32_t bins[kBins];
   };
-  uint32_t group_max[2 * kSelThreads];
-  int queue[kSelWarps][kQueue];
+  uint32_t group_max[SW == 1 ? 4 : 8 * kLanes];
+  int queue[SW][kQueue];
+  int queued[SW];
   u64 merged[BIL_MAX_TOPK];
+  float scratch[kMergeScratch];
   int count;
   uint32_t bound;
   int above;
+  float lse;
 };
 static_assert(sizeof(uint32_t) * kBins <= sizeof(u64) * kCandidates, "the bins share the candidates' space");
 
+// The warps that choose a row's columns wait for each other.
+template <int SW>
+__device__ __forceinline__ void sel_sync() {
+  if constexpr (SW == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync 1, %0;" ::"n"(SW * kLanes) : "memory");
+}
+
 // The columns of one row by way of its chunks.
-template <int DT>
+template <int DT, int SW>
 struct RowColumns {
   static constexpr int EB = Elem<DT>::kBytes;
   const unsigned char* row;    // column 0
   const unsigned char* chunks; // the row's chunk maxima
-  int vocab, tile_v, tile_chunks, num_chunks;
+  int units;                   // 16-byte units of them
+  int vocab, tile_v, tile_chunks, num_tiles;
   int warp, lane;
   int* queue;
+  int* queued;
 
-  __device__ __forceinline__ uint32_t chunk_key(int c) const {
-    return order_key(Elem<DT>::one(chunks + static_cast<size_t>(c) * EB));
-  }
-  // keys of the 8 columns of a group from column c0; `n` exist (the others count as none: key 0)
-  __device__ __forceinline__ void keys8(int c0, int n, uint32_t (&key)[kGroup]) const {
-    const unsigned char* p = row + static_cast<int64_t>(c0) * EB;
-    float v[kGroup];
-    if (n == kGroup && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      uint32_t w[Group<DT>::kW];
-      Group<DT>::load(p, w);
+  static constexpr int kUnit = 16 / EB;  // maxima of a unit
+  __device__ __forceinline__ uint4 unit(int u) const { return reinterpret_cast<const uint4*>(chunks)[u]; }
+  // the unit's maxima, each into its own of 8 (16-bit) or 4 of 8 (float32: the set `half`)
+  __device__ static __forceinline__ void fold(float (&m)[8], uint4 w, int half) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t x = Group<DT>::xpair(w, j);
-        v[2 * j] = lo_of(x);
-        v[2 * j + 1] = hi_of(x);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (EB == 4) {
+        const float v = __uint_as_float(x[j]);
+        if (half == 0)
+          m[j] = fmaxf(m[j], v);
+        else
+          m[4 + j] = fmaxf(m[4 + j], v);
+      } else {
+        float lo, hi;
+        Elem<DT>::pair(x[j], lo, hi);
+        m[2 * j] = fmaxf(m[2 * j], lo);
+        m[2 * j + 1] = fmaxf(m[2 * j + 1], hi);
       }
+    }
+  }
+  // whether a chunk of the tile reaches a key (every lane)
+  __device__ __forceinline__ bool tile_reaches(int tile, uint32_t least) const {
+    bool in = false;
+    for (int c = lane; c < tile_chunks; c += kLanes)
+      in |= order_key(Elem<DT>::one(chunks + (static_cast<int64_t>(tile) * tile_chunks + c) * EB)) >= least;
+    return __any_sync(0xffffffffu, in) != 0;
+  }
+  static constexpr int kW = Group<DT>::kW;
+
+  // the words of the `n` columns from column c0 (n <= 8)
+  __device__ __forceinline__ void load8(int c0, int n, uint32_t (&w)[kW]) const {
+    const unsigned char* p = row + static_cast<int64_t>(c0) * EB;
+    if (n == kGroup && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      Group<DT>::load(p, w);
     } else {
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) v[j] = j < n ? Elem<DT>::one(p + j * EB) : -INFINITY;
-    }
+      for (int j = 0; j < kW; ++j) w[j] = 0;
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) key[j] = order_key(v[j]);
-  }
-  // fn(key, column) for the columns of the queue's first n chunks: half a warp a
-  // chunk, a lane a group of 8, two chunks in flight.
-  template <typename F>
-  __device__ __forceinline__ void read_queue(int n, F fn) const {
-    __syncwarp();
-    for (int i = lane / 16; i < n; i += 4) {
-      int c0[2], steps[2], cols[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const bool have = i + 2 * q < n;
-        const int c = queue[have ? i + 2 * q : 0];
-        const int tile = c / tile_chunks, l = c - tile * tile_chunks;
-        const int valid = min(tile_v, vocab - tile * tile_v);
-        c0[q] = tile * tile_v;
-        cols[q] = valid;
-        steps[q] = have ? l * kGroup : valid;  // first column of the chunk, in the tile
+      for (int j = 0; j < kGroup; ++j) {
+        if (j >= n) continue;
+        if constexpr (EB == 4)
+          w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+        else
+          w[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j & 1));
       }
-      for (int s = (lane % 16) * kLanes * kGroup; s < tile_v; s += 16 * kLanes * kGroup) {
-        uint32_t key[2][kGroup];
-        int left[2];
+    }
+  }
+  // fn(value, column) for the columns that are `least` or more of the queue's
+  // first n chunks: eight lanes a chunk, a lane a group of 8 columns,
+  // kInFlight chunks at a time.
+  template <typename F>
+  __device__ __forceinline__ void read_queue(int n, float least, F fn) const {
+    __syncwarp();
+    for (int i = lane / 8; i < n; i += 4 * kInFlight) {
+      uint32_t w[kInFlight][kW];
+      int first[kInFlight], left[kInFlight];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int e = steps[q] + s;
-          left[q] = min(kGroup, cols[q] - e);
-          if (left[q] > 0) keys8(c0[q] + e, left[q], key[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (left[q] <= 0) continue;
-#pragma unroll
-          for (int j = 0; j < kGroup; ++j)
-            if (j < left[q]) fn(key[q][j], c0[q] + steps[q] + s + j);
+      for (int q = 0; q < kInFlight; ++q) {
+        left[q] = 0;
+        if (i + 4 * q < n) {
+          const int c = queue[i + 4 * q];
+          const int tile = c / tile_chunks;
+          const int e = (c - tile * tile_chunks) * kChunk + (lane % 8) * kGroup;
+          first[q] = tile * tile_v + e;
+          left[q] = min(kGroup, min(tile_v, vocab - tile * tile_v) - e);
+          if (left[q] > 0) load8(first[q], left[q], w[q]);
         }
       }
+#pragma unroll
+      for (int q = 0; q < kInFlight; ++q) {
+        if (left[q] <= 0) continue;
+        unsigned take = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t x = Group<DT>::xpair(w[q], j);
+          take |= (lo_of(x) >= least ? 1u << (2 * j) : 0u) | (hi_of(x) >= least ? 2u << (2 * j) : 0u);
+        }
+        take &= (1u << left[q]) - 1u;
+        while (take != 0u) {
+          const int j = __ffs(take) - 1;
+          take &= take - 1;
+          uint64_t x = Group<DT>::xpair(w[q], 0);
+#pragma unroll
+          for (int h = 1; h < 4; ++h) x = j / 2 == h ? Group<DT>::xpair(w[q], h) : x;
+          fn((j & 1) ? hi_of(x) : lo_of(x), first[q] + j);
+        }
+      }
     }
     __syncwarp();
   }
-  // fn(key, column) for every column of the chunks whose maximum is `least` or
-  // more (the four warps share them).
+  // fn(value, column) for every column that is `least` or more (the row's
+  // warps share the chunks whose maximum is).
   template <typename F>
-  __device__ __forceinline__ void visit(uint32_t least, F fn) const {
-    int n = 0;
-    for (int c0 = warp * kLanes; c0 < num_chunks; c0 += kSelThreads) {
-      const int c = c0 + lane;
-      const bool in = c < num_chunks && chunk_key(c) >= least;
-      const unsigned vote = __ballot_sync(0xffffffffu, in);
-      if (vote == 0u) continue;
-      if (in) queue[n + __popc(vote & ((1u << lane) - 1u))] = c;
-      n += __popc(vote);
-      if (n > kQueue - kLanes) {
-        read_queue(n, fn);
-        n = 0;
+  __device__ __forceinline__ void visit(float least, F fn) const {
+    if (lane == 0) *queued = 0;
+    __syncwarp();
+#pragma unroll 1
+    for (int u0 = warp * kLanes; u0 < units; u0 += kStep * SW * kLanes) {
+      uint4 w[kStep];
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        const int u = u0 + q * SW * kLanes + lane;
+        if (u < units) w[q] = unit(u);
+      }
+#pragma unroll 1
+      for (int q = 0; q < kStep; ++q) {
+        const int u = u0 + q * SW * kLanes + lane;
+        uint4 now = w[0];
+        if (q == 1) now = w[1];
+        if (q == 2) now = w[2];
+        if (q == 3) now = w[3];
+        float m[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        fold(m, now, 0);
+        unsigned take = 0;
+        if (u < units) {
+#pragma unroll
+          for (int j = 0; j < kUnit; ++j) take |= m[j] >= least ? 1u << j : 0u;
+        }
+        while (take != 0u) {
+          const int c = u * kUnit + __ffs(take) - 1;
+          take &= take - 1;
+          if (c < num_tiles * tile_chunks) queue[atomicAdd(queued, 1)] = c;  // not the padding
+        }
+        __syncwarp();
+        const int n = __shfl_sync(0xffffffffu, *queued, 0);
+        const bool last = q == kStep - 1 && u0 + kStep * SW * kLanes >= units;
+        if (n > kQueue - kUnit * kLanes || (last && n != 0)) {
+          read_queue(n, least, fn);
+          if (lane == 0) *queued = 0;
+          __syncwarp();
+        }
       }
     }
-    if (n != 0) read_queue(n, fn);
   }
 };
 
-// The row's k best columns, best first, into sm.merged (kSelThreads threads).
-template <int DT>
-__device__ void select_columns(const RowColumns<DT>& cols, int k, SelShared& sm) {
-  const int tid = threadIdx.x;
-  // 1. the groups' maxima: thread i has chunks i, i + 128, ...; for k > 32 in two groups, odd and even.
+// The row's k best columns, best first, into sm.merged (the row's SW warps).
+template <int DT, int SW>
+__device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, int k, SelShared<SW>& sm) {
+  const int tid = cols.warp * kLanes + cols.lane;
+  // 1. the maxima of 128 groups of chunks (k > 32: 256): which chunks make a group does not matter
+  constexpr int kSets = 8 / SW;  // groups of a thread
+  uint32_t key[8];
   {
-    uint32_t m[2] = {0, 0};
-    int j = 0;
-    for (int c = tid; c < cols.num_chunks; c += kSelThreads, j ^= 1) m[j] = max(m[j], cols.chunk_key(c));
-    if (k <= kLanes) m[0] = max(m[0], m[1]);
-    sm.group_max[tid] = m[0];
-    if (k > kLanes) sm.group_max[kSelThreads + tid] = m[1];
-    if (tid == 0) {
-      sm.count = 0;
-      sm.bound = 0;
-    }
-  }
-  sel_sync();
-  // 2. the k-th largest of them: it has k columns at or above it (0 where there are fewer groups than k)
-  {
-    const int groups = k <= kLanes ? kSelThreads : 2 * kSelThreads;
-    for (int i = tid; i < groups; i += kSelThreads) {
-      const uint32_t mine = sm.group_max[i];
-      int above = 0;
-#pragma unroll 4
-      for (int j = 0; j < groups; j += 4) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&sm.group_max[j]);
-        above += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
-                 (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
-      }
-      if (above == k - 1) sm.bound = mine;
-    }
-  }
-  sel_sync();
-  uint32_t least = sm.bound;  // columns with this key or more are wanted
-  auto append = [&](uint32_t key, int c) {
-    if (key < least) return;
-    const int at = atomicAdd(&sm.count, 1);
-    if (at < kCandidates) sm.cand[at] = entry_of(key, c);
-  };
-  // 3. those columns; at and below -inf the bound says nothing (a chunk of NaN also says -inf)
-  bool enough = false;  // sm.cand holds all columns >= least, k of them at least
-  if (least > kKeyNegInf) {
-    cols.visit(least, append);
-    sel_sync();
-    enough = sm.count <= kCandidates;
-  } else {
-    least = kKeyNegInf;
-  }
-  if (!enough) {
-    // Too many columns reach the bound, or there is none: the columns above it.
-    const uint32_t floor_key = least;
-    least = floor_key + 1;
-    sel_sync();
-    if (tid == 0) sm.count = 0;
-    sel_sync();
-    cols.visit(least, append);
-    sel_sync();
-    int found = sm.count;
-    sel_sync();  // every thread has read the count before any may change it
-    if (found > kCandidates) {
-      // Radix selection over the keys above floor_key, from the top digit, until few enough are left: `prefix`
-      // and above, `fixed` bits of it known.
-      uint32_t prefix = 0;
-      int fixed = 0, taken = 0;  // taken: columns above prefix's range
-      for (;;) {
-        const int bits = min(kDigitBits, 32 - fixed), shift = 32 - fixed - bits;
-        sel_sync();
-        for (int i = tid; i < kBins; i += kSelThreads) sm.bins[i] = 0;
-        sel_sync();
-        const uint32_t lo = max(least, prefix);
-        cols.visit(lo, [&](uint32_t key, int) {
-          if (key < lo || (fixed != 0 && (key >> (32 - fixed)) != (prefix >> (32 - fixed)))) return;
-          atomicAdd(&sm.bins[(key >> shift) & ((1u << bits) - 1u)], 1u);
-        });
-        sel_sync();
-        if (cols.warp == 0) {
-          // from the highest bin down: the bin that holds the k-th column
-          int sum = taken, digit = -1, before = 0;
-          for (int b0 = (1 << bits) - kLanes; b0 >= 0 && digit < 0; b0 -= kLanes) {
-            const int n = static_cast<int>(sm.bins[b0 + kLanes - 1 - cols.lane]);  // lane 0: the highest
-            int upto = n;
+    float m[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int u0 = tid; u0 < cols.units; u0 += 6 * SW * kLanes) {
+      uint4 w[6];
 #pragma unroll
-            for (int o = 1; o < kLanes; o *= 2) {
-              const int v = __shfl_up_sync(0xffffffffu, upto, o);
-              if (cols.lane >= o) upto += v;
-            }
-            const unsigned vote = __ballot_sync(0xffffffffu, sum + upto >= k);
-            if (vote != 0u) {
-              const int src = __ffs(vote) - 1;
-              digit = b0 + kLanes - 1 - src;
-              before = sum + __shfl_sync(0xffffffffu, upto - n, src);
-              found = sum + __shfl_sync(0xffffffffu, upto, src);
-            }
-            sum += __shfl_sync(0xffffffffu, upto, kLanes - 1);
-          }
-          if (cols.lane == 0) {
-            sm.bound = prefix | (static_cast<uint32_t>(max(digit, 0)) << shift);
-            sm.above = before;
-            sm.count = found;
-          }
-        }
-        sel_sync();
-        prefix = sm.bound;
-        taken = sm.above;
-        found = sm.count;  // columns >= prefix
-        fixed += bits;
-        if (found <= kCandidates || fixed == 32) break;
+      for (int q = 0; q < 6; ++q)
+        if (u0 + q * SW * kLanes < cols.units) w[q] = cols.unit(u0 + q * SW * kLanes);
+#pragma unroll
+      for (int q = 0; q < 6; ++q)
+        if (u0 + q * SW * kLanes < cols.units) cols.fold(m, w[q], q & 1);
+    }
+#pragma unroll
+    for (int q = kSets; q < 8; ++q) m[q % kSets] = fmaxf(m[q % kSets], m[q]);
+    if (k <= kLanes) {
+#pragma unroll
+      for (int q = 0; q < kSets / 2; ++q) {
+        m[q] = fmaxf(m[q], m[q + kSets / 2]);
+        m[q + kSets / 2] = -INFINITY;
       }
-      // `prefix` and above hold k columns; where even those are too many (equal logits), the ones above it
-      // are fewer than k and the rest is found below
-      least = found <= kCandidates ? max(least, prefix) : prefix + 1;
-      sel_sync();
-      if (tid == 0) sm.count = 0;
-      sel_sync();
-      cols.visit(least, append);
-      sel_sync();
+    }
+#pragma unroll
+    for (int q = 0; q < kSets; ++q) {
+      if constexpr (SW == 1)
+        key[q] = order_key(m[q]);
+      else
+        sm.group_max[q * SW * kLanes + tid] = order_key(m[q]);
+    }
+    if (tid == 0) sm.count = 0;
+  }
+  sel_sync<SW>();
+  // 2. the k-th largest of them, to the upper 16 bits of its key (all of a bfloat16): it has k columns at or
+  // above it
+  if (cols.warp == 0) {
+    if constexpr (SW != 1) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) key[q] = sm.group_max[q * kLanes + cols.lane];
+    }
+    uint32_t bound = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t up = bound | (1u << bit);
+      int above = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) above += __popc(__ballot_sync(0xffffffffu, key[q] >= up));
+      if (k > kLanes) {
+#pragma unroll
+        for (int q = 4; q < 8; ++q) above += __popc(__ballot_sync(0xffffffffu, key[q] >= up));
+      }
+      if (above >= k) bound = up;
+    }
+    if (cols.lane == 0) sm.bound = bound;
+  }
+  sel_sync<SW>();
+  // 3. The columns of that key or more, if there are no more of them than fit.  Else (many equal or
+  // crowded columns), and where the bound is -inf, which says nothing (a chunk of NaN says -inf too): those
+  // above it; if there are too many of these, a radix selection over their keys first, from the top digit.
+  enum { kReach, kAbove, kDigits, kLast } step = kReach;
+  uint32_t least = sm.bound;
+  uint32_t prefix = 0;        // of the k-th key, `fixed` bits known; `taken` columns are above its range
+  int fixed = 0, bits = 0, shift = 0, taken = 0, found = 0;
+  if (least <= kKeyNegInf) {
+    least = kKeyNegInf + 1;
+    step = kAbove;
+  }
+#pragma unroll 1
+  for (;;) {
+    cols.visit(key_value(least), [&](float x, int c) {
+      const uint32_t key = order_key(x);
+      if (step == kDigits) {
+        if (fixed == 0 || (key >> (32 - fixed)) == (prefix >> (32 - fixed)))
+          atomicAdd(&sm.bins[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      } else {
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kCandidates) sm.cand[at] = entry_of(key, c);
+      }
+    });
+    sel_sync<SW>();
+    if (step != kDigits) {
       found = sm.count;
-      sel_sync();
-    }
-    // Equal columns just below `least`, then NaN, in column order: one warp, tile by tile.
-    if (found < k) {
-      if (cols.warp == 0) {
-        uint32_t want = least - 1;
-        for (;;) {
-          for (int tile = 0; tile * cols.tile_chunks < cols.num_chunks && found < k; ++tile) {
-            const bool any = cols.lane < cols.tile_chunks &&
-                             cols.chunk_key(tile * cols.tile_chunks + cols.lane) >= max(want, kKeyNegInf);
-            if (!__any_sync(0xffffffffu, any)) continue;
-            const int valid = min(cols.tile_v, cols.vocab - tile * cols.tile_v);
-            for (int e0 = 0; e0 < valid && found < k; e0 += kLanes) {
-              const int c = tile * cols.tile_v + e0 + cols.lane;
-              const bool in = e0 + cols.lane < valid &&
-                              order_key(Elem<DT>::one(cols.row + static_cast<int64_t>(c) * Elem<DT>::kBytes)) == want;
-              const unsigned vote = __ballot_sync(0xffffffffu, in);
-              const int at = found + __popc(vote & ((1u << cols.lane) - 1u));
-              if (in && at < k) sm.cand[at] = entry_of(want, c);
-              found = min(k, found + __popc(vote));
-            }
-          }
-          if (found >= k || want == 0) break;
-          want = 0;
-        }
-        if (cols.lane == 0) sm.count = found;
+      sel_sync<SW>();  // every thread has read the count before any may change it
+      if (found <= kCandidates || step == kLast) break;
+      if (step == kReach) {
+        ++least;
+        step = kAbove;
+      } else {
+        step = kDigits;
       }
-      sel_sync();
+    } else {
+      if (cols.warp == 0) {
+        // from the highest bin down: the bin that holds the k-th column
+        int sum = taken, digit = -1, before = 0, upto_digit = 0;
+        for (int b0 = max((1 << bits) - kLanes, 0); b0 >= 0 && digit < 0; b0 -= kLanes) {
+          const int n = static_cast<int>(sm.bins[b0 + kLanes - 1 - cols.lane]);  // lane 0: the highest
+          int upto = n;
+#pragma unroll
+          for (int o = 1; o < kLanes; o *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (cols.lane >= o) upto += v;
+          }
+          const unsigned vote = __ballot_sync(0xffffffffu, sum + upto >= k);
+          if (vote != 0u) {
+            const int src = __ffs(vote) - 1;
+            digit = b0 + kLanes - 1 - src;
+            before = sum + __shfl_sync(0xffffffffu, upto - n, src);
+            upto_digit = sum + __shfl_sync(0xffffffffu, upto, src);
+          }
+          sum += __shfl_sync(0xffffffffu, upto, kLanes - 1);
+        }
+        if (cols.lane == 0) {
+          sm.bound = prefix | (static_cast<uint32_t>(max(digit, 0)) << shift);
+          sm.above = before;
+          sm.count = upto_digit;
+        }
+      }
+      sel_sync<SW>();
+      prefix = sm.bound;
+      taken = sm.above;
+      found = sm.count;  // columns of `prefix` or more
+      sel_sync<SW>();
+      fixed += bits;
+      least = max(least, prefix);
+      if (found <= kCandidates || fixed == 32) {
+        // too many even so (equal columns): those above it, fewer than k, and the rest is found below
+        if (found > kCandidates) least = prefix + 1;
+        step = kLast;
+      }
     }
+    if (step == kDigits) {
+      bits = min(kDigitBits, 32 - fixed);
+      shift = 32 - fixed - bits;
+      for (int i = tid; i < kBins; i += SW * kLanes) sm.bins[i] = 0;
+    } else if (tid == 0) {
+      sm.count = 0;
+    }
+    sel_sync<SW>();
+  }
+  if (found < k) {
+    // Equal columns just below `least`, then NaN, in column order: one warp, tile by tile.
+    if (cols.warp == 0) {
+      uint32_t want = least - 1;
+      for (;;) {
+        for (int tile = 0; tile < cols.num_tiles && found < k; ++tile) {
+          if (!cols.tile_reaches(tile, max(want, kKeyNegInf))) continue;
+          const int valid = min(cols.tile_v, cols.vocab - tile * cols.tile_v);
+          for (int e0 = 0; e0 < valid && found < k; e0 += kLanes) {
+            const int c = tile * cols.tile_v + e0 + cols.lane;
+            const bool in = e0 + cols.lane < valid &&
+                            order_key(Elem<DT>::one(cols.row + static_cast<int64_t>(c) * Elem<DT>::kBytes)) == want;
+            const unsigned vote = __ballot_sync(0xffffffffu, in);
+            const int at = found + __popc(vote & ((1u << cols.lane) - 1u));
+            if (in && at < k) sm.cand[at] = entry_of(want, c);
+            found = min(k, found + __popc(vote));
+          }
+        }
+        if (found >= k || want == 0) break;
+        want = 0;
+      }
+    }
+    found = k;
   }
   // 4. in order: an entry's place is the number of entries above it
-  const int n = sm.count;
-  for (int i = tid; i < n; i += kSelThreads) {
+  const int n = found;
+  if (tid == 0 && n < kCandidates) sm.cand[n] = 0;  // the pair of the last one
+  sel_sync<SW>();
+  for (int i = tid; i < n; i += SW * kLanes) {
     const u64 mine = sm.cand[i];
     int above = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) above += sm.cand[j] > mine ? 1 : 0;
+    for (int j = 0; j < n; j += 2) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sm.cand[j]);
+      above += (o.x > mine ? 1 : 0) + (o.y > mine ? 1 : 0);
+    }
     if (above < k) sm.merged[above] = mine;
   }
 }
 
-template <int DT, bool ENT>
-__global__ void __launch_bounds__(kRowThreads) topk_row_kernel(const TopkParams p, float* logp, float* lse,
-                                                               float* entropy, int64_t* top_ids, float* top_logp) {
-  __shared__ SelShared sm;
-  __shared__ float scratch[kMergeScratch];
-  __shared__ float row_lse;
+template <int DT, bool ENT, int SW>
+__global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes)
+    topk_row_kernel(const TopkParams p, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp) {
+  constexpr int kRows = SW == 1 ? 4 : 1;  // rows of a block
+  __shared__ SelShared<SW> shared[kRows];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
-  const int64_t row = blockIdx.x;
+  const int64_t row = SW == 1 ? static_cast<int64_t>(blockIdx.x) * kRows + warp : blockIdx.x;
+  if (row >= p.n_rows) return;  // a warp of its own: no barrier follows
+  SelShared<SW>& sm = shared[SW == 1 ? warp : 0];
   const int64_t t = p.targets[row];
   int64_t* ids = top_ids + row * p.k;
   float* top = top_logp + row * p.k;
+  const int tid = SW == 1 ? lane : static_cast<int>(threadIdx.x);
+  constexpr int kThreads = SW == 1 ? kLanes : (SW + 1) * kLanes;
   if (t == p.ignore_index) {
-    for (int j = threadIdx.x; j < p.k; j += kRowThreads) {
+    for (int j = tid; j < p.k; j += kThreads) {
       ids[j] = -1;
       top[j] = 0.0f;
     }
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       logp[row] = 0.0f;
       if (lse != nullptr) lse[row] = 0.0f;
       if (ENT) entropy[row] = 0.0f;
@@ -573,13 +766,28 @@ __global__ void __launch_bounds__(kRowThreads) topk_row_kernel(const TopkParams 
     return;
   }
   const unsigned char* src = p.logits + row * p.ld * Elem<DT>::kBytes;
-  if (warp == kSelWarps) {
+  if (SW == 1 || warp != SW) {
+    RowColumns<DT, SW> cols;
+    cols.row = src;
+    cols.num_tiles = p.num_tiles;
+    cols.chunks = p.chunk_max + row * p.chunk_pitch;
+    cols.units = static_cast<int>(p.chunk_pitch / 16);
+    cols.vocab = static_cast<int>(p.vocab);
+    cols.tile_v = p.tile_v;
+    cols.tile_chunks = p.tile_chunks;
+    cols.warp = SW == 1 ? 0 : warp;
+    cols.lane = lane;
+    cols.queue = sm.queue[SW == 1 ? 0 : warp];
+    cols.queued = &sm.queued[SW == 1 ? 0 : warp];
+    select_columns<DT, SW>(cols, p.k, sm);
+  }
+  if (SW == 1 || warp == SW) {
     const int64_t o = row * p.num_tiles;
     float H = 0.0f;
     const float L = merge_lse<ENT, true>(p.part_max + o, p.part_sum + o, ENT ? p.part_ent + o : nullptr, p.num_tiles,
-                                         lane, &H, scratch);
+                                         lane, &H, sm.scratch);
     if (lane == 0) {
-      row_lse = L;
+      sm.lse = L;
       float z = __int_as_float(0x7fc00000);
       if (t >= 0 && t < p.vocab) {
         z = Elem<DT>::one(src + t * Elem<DT>::kBytes);
@@ -589,26 +797,17 @@ __global__ void __launch_bounds__(kRowThreads) topk_row_kernel(const TopkParams 
       if (lse != nullptr) lse[row] = L;
       if (ENT) entropy[row] = H;
     }
-  } else {
-    RowColumns<DT> cols;
-    cols.row = src;
-    cols.num_chunks = p.num_tiles * p.tile_chunks;
-    cols.chunks = p.chunk_max + row * cols.num_chunks * Elem<DT>::kBytes;
-    cols.vocab = static_cast<int>(p.vocab);
-    cols.tile_v = p.tile_v;
-    cols.tile_chunks = p.tile_chunks;
-    cols.warp = warp;
-    cols.lane = lane;
-    cols.queue = sm.queue[warp];
-    select_columns<DT>(cols, p.k, sm);
   }
-  __syncthreads();
-  for (int j = threadIdx.x; j < p.k; j += kRowThreads) {
+  if constexpr (SW == 1)
+    __syncwarp();
+  else
+    __syncthreads();
+  for (int j = tid; j < p.k; j += kThreads) {
     const u64 e = sm.merged[j];
     float z = key_value(static_cast<uint32_t>(e >> 32));
     if (p.rcp != 1.0f) z = __fmul_rn(z, p.rcp);
     ids[j] = entry_column(e);
-    top[j] = __fsub_rn(z, row_lse);
+    top[j] = __fsub_rn(z, sm.lse);
   }
 }
 
@@ -731,13 +930,14 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 // The workspace: chunk maxima, then the partials.
 struct TopkWorkspace {
   int tile_chunks;
-  size_t chunks, part, total;  // bytes: the chunk maxima, one partial array, all
+  size_t pitch, chunks, part, total;  // bytes: a row of chunk maxima, all rows, one partial array, everything
 };
 
 TopkWorkspace topk_workspace(int dtype, int64_t n_rows, int64_t num_tiles, int tile_v, bool ent) {
   TopkWorkspace w;
-  w.tile_chunks = std::min(kLanes, tile_v / kGroup);
-  w.chunks = round256(static_cast<size_t>(n_rows) * num_tiles * w.tile_chunks * bil_internal::elem_bytes(dtype));
+  w.tile_chunks = (tile_v + kChunk - 1) / kChunk;
+  w.pitch = static_cast<size_t>(align_up(static_cast<size_t>(num_tiles) * w.tile_chunks * bil_internal::elem_bytes(dtype), 16));
+  w.chunks = round256(static_cast<size_t>(n_rows) * w.pitch);
   w.part = round256(static_cast<size_t>(n_rows) * num_tiles * sizeof(float));
   w.total = w.chunks + w.part * (ent ? 3 : 2);
   return w;
@@ -774,10 +974,14 @@ int launch_topk_t(TopkParams p, float* logp, float* lse, float* entropy, int64_t
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return BIL_E_CUDA;
   if (launch_pdl(kernel, grid, warps * kLanes, smem, stream, 1, p) != cudaSuccess) return BIL_E_CUDA;
-  return launch_pdl(topk_row_kernel<DT, ENT>, p.n_rows, kRowThreads, 0, stream, 1, p, logp, lse, entropy, top_ids,
-                    top_logp) == cudaSuccess
-             ? BIL_OK
-             : BIL_E_CUDA;
+  // One warp a row from four rows an SM on.
+  const cudaError_t e =
+      p.n_rows >= 4 * static_cast<int64_t>(sms)
+          ? launch_pdl(topk_row_kernel<DT, ENT, 1>, (p.n_rows + 3) / 4, 4 * kLanes, 0, stream, 1, p, logp, lse, entropy,
+                       top_ids, top_logp)
+          : launch_pdl(topk_row_kernel<DT, ENT, kFewRowWarps>, p.n_rows, (kFewRowWarps + 1) * kLanes, 0, stream, 1, p,
+                       logp, lse, entropy, top_ids, top_logp);
+  return e == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
 template <int DT>
@@ -866,6 +1070,7 @@ int bil_logp_topk_fwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
   p.tile_v = tile_v;
   p.num_tiles = static_cast<int>(num_tiles);
   p.tile_chunks = w.tile_chunks;
+  p.chunk_pitch = static_cast<int64_t>(w.pitch);
   p.targets = target_ids;
   p.ignore_index = ignore_index;
   p.rcp = rcp;
