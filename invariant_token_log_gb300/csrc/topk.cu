@@ -91,26 +91,37 @@ struct TopkParams {
 // The pass over the logits.
 // ---------------------------------------------------------------------------
 
-// Where a warp is in its units: unit u, tile within it.  Units of ignored
-// rows are passed over.
+// Where a warp is in its units: the tile, where the unit's tiles end, and the
+// tile's first column.  Units of ignored rows are passed over.
 struct UnitCursor {
   int64_t unit, row;
+  const unsigned char* src;
   int tile, end;
+  bool more;
 
-  __device__ __forceinline__ bool more(const TopkParams& p) const { return unit < p.n_rows * p.units; }
-  __device__ __forceinline__ void settle(const TopkParams& p, int64_t stride) {
-    for (; more(p); unit += stride) {
-      row = unit / p.units;
+  // the unit itself, or the next one at `stride` that is not of an ignored row
+  __device__ __forceinline__ void settle(const TopkParams& p, int64_t stride, int eb) {
+    for (; unit < p.n_rows * p.units; unit += stride) {
+      row = p.units == 1 ? unit : unit / p.units;
       if (p.targets[row] == p.ignore_index) continue;
       tile = static_cast<int>(unit - row * p.units) * p.unit_tiles;
       end = min(tile + p.unit_tiles, p.num_tiles);
+      src = p.logits + (row * p.ld + static_cast<int64_t>(tile) * p.tile_v) * eb;
+      more = true;
       return;
     }
+    more = false;
   }
-  __device__ __forceinline__ void next(const TopkParams& p, int64_t stride) {
-    if (++tile < end) return;
+  __device__ __forceinline__ void next(const TopkParams& p, int64_t stride, int eb) {
+    if (++tile < end) {
+      src += p.tile_v * eb;
+      return;
+    }
     unit += stride;
-    settle(p, stride);
+    settle(p, stride, eb);
+  }
+  __device__ __forceinline__ int valid(const TopkParams& p) const {
+    return tile < p.num_tiles - 1 ? p.tile_v : static_cast<int>(p.vocab - static_cast<int64_t>(tile) * p.tile_v);
   }
 };
 
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
   __shared__ uint64_t full_bars[kTopkMaxWarps];
   __shared__ int abort_flag;
   constexpr int EB = Elem<DT>::kBytes;
-  const int warp = threadIdx.x / kLanes;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / kLanes), 0);
   const int lane = threadIdx.x % kLanes;
   const int warps = blockDim.x / kLanes;
   volatile int* abort = &abort_flag;
@@ -290,35 +301,32 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
   // Consecutive units go to different blocks.
   const int64_t stride = static_cast<int64_t>(gridDim.x) * warps;
   const uint64_t policy = evict_first_policy();
-  UnitCursor at{static_cast<int64_t>(warp) * gridDim.x + blockIdx.x, 0, 0, 0};
-  at.settle(p, stride);
+  UnitCursor at;
+  at.unit = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  at.settle(p, stride, EB);
 
-  // The copy of the tile at `c` into the warp's stage (its last reader is
+  // The copy of the tile at `at` into the warp's stage (its last reader is
   // done): the 16-byte aligned span that covers the tile, as in the streaming
   // forward.
-  auto issue = [&](const UnitCursor& c) {
-    if (lane != 0 || !c.more(p)) return;
-    const int64_t col0 = static_cast<int64_t>(c.tile) * p.tile_v;
-    const int valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - col0));
-    const unsigned char* src = p.logits + (c.row * p.ld + col0) * EB;
-    const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
-    const unsigned bytes = static_cast<unsigned>(align_up(off + static_cast<size_t>(valid) * EB, 16));
+  auto issue = [&]() {
+    if (lane != 0 || !at.more) return;
+    const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(at.src) & 15u);
+    const unsigned bytes = (off + static_cast<unsigned>(at.valid(p)) * EB + 15u) & ~15u;
     mbar_arrive_expect_tx(full, bytes);
-    bulk_g2s(stage, src - off, bytes, full, policy);
+    bulk_g2s(stage, at.src - off, bytes, full, policy);
   };
-  issue(at);
+  issue();
 
   unsigned parity = 0;
   bool ok = true;
-  while (at.more(p)) {
+  while (at.more) {
     ok = warp_wait(full, parity, abort, kWatchFull);
     if (!ok) break;
     parity ^= 1u;
     const UnitCursor now = at;
-    at.next(p, stride);
-    const int64_t col0 = static_cast<int64_t>(now.tile) * p.tile_v;
-    const int valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - col0));
-    const unsigned char* src = p.logits + (now.row * p.ld + col0) * EB;
+    at.next(p, stride, EB);
+    const int valid = now.valid(p);
+    const unsigned char* src = now.src;
     const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
     const int64_t o = now.row * p.num_tiles + now.tile;
     TilePartial tp;
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
       TileRegs<DT> regs;
       tile_load_regs<DT, !ALIGNED>(stage, valid, lane, regs, off);
       __syncwarp();  // the stage has been read
-      issue(at);
+      issue();
       const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, chunks, p.tile_chunks)
                                           : regs_max<DT, false>(regs, valid, lane, chunks, p.tile_chunks));
       tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
       smem_max<DT, !ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks);
       tp = tile_reduce_smem<DT, ENT, !ALIGNED>(stage, valid, lane, p.rcp, off);
       __syncwarp();
-      issue(at);
+      issue();
     }
     if (now.tile == p.num_tiles - 1) {  // the rest of the row's last 16 bytes
       const int pad = p.num_tiles * p.tile_chunks + lane;
@@ -385,7 +393,6 @@ struct alignas(16) SelShared {
   };
   uint32_t group_max[SW == 1 ? 4 : 8 * kLanes];
   int queue[SW][kQueue];
-  int queued[SW];
   u64 merged[BIL_MAX_TOPK];
   float scratch[kMergeScratch];
   int count;
@@ -414,29 +421,68 @@ struct RowColumns {
   int vocab, tile_v, tile_chunks, num_tiles;
   int warp, lane;
   int* queue;
-  int* queued;
 
   static constexpr int kUnit = 16 / EB;  // maxima of a unit
   __device__ __forceinline__ uint4 unit(int u) const { return reinterpret_cast<const uint4*>(chunks)[u]; }
-  // the unit's maxima, each into its own of 8 (16-bit) or 4 of 8 (float32: the set `half`)
-  __device__ static __forceinline__ void fold(float (&m)[8], uint4 w, int half) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  // running maxima of the units a lane looks at: each of a unit's 8 (16-bit) in its own, or its 4
+  // (float32) in the set `half`
+  struct Maxima {
+    uint32_t r[8];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (EB == 4) {
-        const float v = __uint_as_float(x[j]);
-        if (half == 0)
-          m[j] = fmaxf(m[j], v);
-        else
-          m[4 + j] = fmaxf(m[4 + j], v);
-      } else {
-        float lo, hi;
-        Elem<DT>::pair(x[j], lo, hi);
-        m[2 * j] = fmaxf(m[2 * j], lo);
-        m[2 * j + 1] = fmaxf(m[2 * j + 1], hi);
+      for (int j = 0; j < 8; ++j) r[j] = ChunkMax<DT>::kNone;
+    }
+    __device__ __forceinline__ void add(uint4 w, int half) {
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = EB == 4 ? 4 * half + j : j;
+        r[at] = ChunkMax<DT>::max_of(r[at], x[j]);
       }
     }
+    __device__ __forceinline__ void get(float (&m)[8]) const {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (EB == 4) {
+          m[j] = __uint_as_float(r[j]);
+        } else {
+          float lo, hi;
+          Elem<DT>::pair(r[j / 2], lo, hi);
+          m[j] = j % 2 == 0 ? lo : hi;
+        }
+      }
+    }
+  };
+  // A bound to compare stored words with (the smallest value of the type that is `least` or more), which of
+  // a word's values reach it, and value `bit` of the words: one bit a value, a 16-bit type's upper halves
+  // from bit 16 on.
+  __device__ static __forceinline__ uint32_t bound_word(float least) {
+    if constexpr (DT == BIL_F32) {
+      return __float_as_uint(least);
+    } else if constexpr (DT == BIL_BF16) {
+      return __bfloat16_as_ushort(__float2bfloat16_ru(least)) * 0x10001u;
+    } else {
+      return __half_as_ushort(__float2half_ru(least)) * 0x10001u;
+    }
   }
+  template <int N>
+  __device__ static __forceinline__ unsigned reach(const uint32_t (&w)[N], uint32_t bound) {
+    unsigned t = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (DT == BIL_F32)
+        t |= __uint_as_float(w[j]) >= __uint_as_float(bound) ? 1u << j : 0u;
+      else if constexpr (DT == BIL_BF16)
+        t |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), *reinterpret_cast<const __nv_bfloat162*>(&bound)) &
+             (0x10001u << j);
+      else
+        t |= __hge2_mask(*reinterpret_cast<const __half2*>(&w[j]), *reinterpret_cast<const __half2*>(&bound)) &
+             (0x10001u << j);
+    }
+    return t;
+  }
+  __device__ static __forceinline__ int place(int bit) { return EB == 4 ? bit : 2 * (bit % 16) + bit / 16; }
+
   // whether a chunk of the tile reaches a key (every lane)
   __device__ __forceinline__ bool tile_reaches(int tile, uint32_t least) const {
     bool in = false;
@@ -464,11 +510,12 @@ struct RowColumns {
       }
     }
   }
-  // fn(value, column) for the columns that are `least` or more of the queue's
-  // first n chunks: eight lanes a chunk, a lane a group of 8 columns,
-  // kInFlight chunks at a time.
+  // fn(value, column) for the columns that reach `bound` of the queue's first n
+  // chunks: eight lanes a chunk, a lane a group of 8 columns, kInFlight chunks
+  // at a time.
   template <typename F>
-  __device__ __forceinline__ void read_queue(int n, float least, F fn) const {
+  __device__ __forceinline__ void read_queue(int n, uint32_t bound, F fn) const {
+    const bool even = tile_v % kChunk == 0;  // chunks lie one after the other
     __syncwarp();
     for (int i = lane / 8; i < n; i += 4 * kInFlight) {
       uint32_t w[kInFlight][kW];
@@ -478,80 +525,83 @@ struct RowColumns {
         left[q] = 0;
         if (i + 4 * q < n) {
           const int c = queue[i + 4 * q];
-          const int tile = c / tile_chunks;
-          const int e = (c - tile * tile_chunks) * kChunk + (lane % 8) * kGroup;
-          first[q] = tile * tile_v + e;
-          left[q] = min(kGroup, min(tile_v, vocab - tile * tile_v) - e);
+          if (even) {
+            first[q] = c * kChunk + (lane % 8) * kGroup;
+            left[q] = min(kGroup, vocab - first[q]);
+          } else {
+            const int tile = c / tile_chunks;
+            const int e = (c - tile * tile_chunks) * kChunk + (lane % 8) * kGroup;
+            first[q] = tile * tile_v + e;
+            left[q] = min(kGroup, min(tile_v, vocab - tile * tile_v) - e);
+          }
           if (left[q] > 0) load8(first[q], left[q], w[q]);
         }
       }
 #pragma unroll
       for (int q = 0; q < kInFlight; ++q) {
         if (left[q] <= 0) continue;
-        unsigned take = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t x = Group<DT>::xpair(w[q], j);
-          take |= (lo_of(x) >= least ? 1u << (2 * j) : 0u) | (hi_of(x) >= least ? 2u << (2 * j) : 0u);
-        }
-        take &= (1u << left[q]) - 1u;
+        unsigned take = reach(w[q], bound);
         while (take != 0u) {
-          const int j = __ffs(take) - 1;
+          const int bit = __ffs(take) - 1;
           take &= take - 1;
-          uint64_t x = Group<DT>::xpair(w[q], 0);
+          const int j = place(bit);
+          if (j >= left[q]) continue;
+          uint32_t word = w[q][0];
 #pragma unroll
-          for (int h = 1; h < 4; ++h) x = j / 2 == h ? Group<DT>::xpair(w[q], h) : x;
-          fn((j & 1) ? hi_of(x) : lo_of(x), first[q] + j);
+          for (int h = 1; h < kW; ++h) word = bit % 16 == h ? w[q][h] : word;
+          float x;
+          if constexpr (EB == 4) {
+            x = __uint_as_float(word);
+          } else {
+            float lo, hi;
+            Elem<DT>::pair(word, lo, hi);
+            x = bit < 16 ? lo : hi;
+          }
+          fn(x, first[q] + j);
         }
       }
     }
     __syncwarp();
   }
-  // fn(value, column) for every column that is `least` or more (the row's
-  // warps share the chunks whose maximum is).
+  // fn(value, column) for every column that is `least` (above -inf) or more; the
+  // row's warps share the chunks whose maximum is.
   template <typename F>
   __device__ __forceinline__ void visit(float least, F fn) const {
-    if (lane == 0) *queued = 0;
-    __syncwarp();
+    const uint32_t bound = bound_word(least);
+    int n = 0;
 #pragma unroll 1
     for (int u0 = warp * kLanes; u0 < units; u0 += kStep * SW * kLanes) {
       uint4 w[kStep];
 #pragma unroll
       for (int q = 0; q < kStep; ++q) {
         const int u = u0 + q * SW * kLanes + lane;
-        if (u < units) w[q] = unit(u);
+        w[q] = u < units ? unit(u) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll 1
       for (int q = 0; q < kStep; ++q) {
         const int u = u0 + q * SW * kLanes + lane;
-        uint4 now = w[0];
-        if (q == 1) now = w[1];
-        if (q == 2) now = w[2];
-        if (q == 3) now = w[3];
-        float m[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        fold(m, now, 0);
-        unsigned take = 0;
-        if (u < units) {
-#pragma unroll
-          for (int j = 0; j < kUnit; ++j) take |= m[j] >= least ? 1u << j : 0u;
+        const uint4 now = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
+        const uint32_t x[4] = {now.x, now.y, now.z, now.w};
+        unsigned take = u < units ? reach(x, bound) : 0u;
+        for (;;) {
+          const unsigned vote = __ballot_sync(0xffffffffu, take != 0u);
+          if (vote == 0u) break;
+          if (take != 0u) {
+            queue[n + __popc(vote & ((1u << lane) - 1u))] = u * kUnit + place(__ffs(take) - 1);
+            take &= take - 1;
+          }
+          n += __popc(vote);
         }
-        while (take != 0u) {
-          const int c = u * kUnit + __ffs(take) - 1;
-          take &= take - 1;
-          if (c < num_tiles * tile_chunks) queue[atomicAdd(queued, 1)] = c;  // not the padding
-        }
-        __syncwarp();
-        const int n = __shfl_sync(0xffffffffu, *queued, 0);
         const bool last = q == kStep - 1 && u0 + kStep * SW * kLanes >= units;
         if (n > kQueue - kUnit * kLanes || (last && n != 0)) {
-          read_queue(n, least, fn);
-          if (lane == 0) *queued = 0;
-          __syncwarp();
+          read_queue(n, bound, fn);
+          n = 0;
         }
       }
     }
   }
 };
+static_assert(kStep == 4, "visit picks among four units");
 
 // The row's k best columns, best first, into sm.merged (the row's SW warps).
 template <int DT, int SW>
@@ -561,7 +611,8 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
   constexpr int kSets = 8 / SW;  // groups of a thread
   uint32_t key[8];
   {
-    float m[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    typename RowColumns<DT, SW>::Maxima maxima;
+    maxima.clear();
 #pragma unroll 1
     for (int u0 = tid; u0 < cols.units; u0 += 6 * SW * kLanes) {
       uint4 w[6];
@@ -570,8 +621,10 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
         if (u0 + q * SW * kLanes < cols.units) w[q] = cols.unit(u0 + q * SW * kLanes);
 #pragma unroll
       for (int q = 0; q < 6; ++q)
-        if (u0 + q * SW * kLanes < cols.units) cols.fold(m, w[q], q & 1);
+        if (u0 + q * SW * kLanes < cols.units) maxima.add(w[q], q & 1);
     }
+    float m[8];
+    maxima.get(m);
 #pragma unroll
     for (int q = kSets; q < 8; ++q) m[q % kSets] = fmaxf(m[q % kSets], m[q]);
     if (k <= kLanes) {
@@ -599,7 +652,7 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
       for (int q = 0; q < 8; ++q) key[q] = sm.group_max[q * kLanes + cols.lane];
     }
     uint32_t bound = 0;
-#pragma unroll
+#pragma unroll 1
     for (int bit = 31; bit >= 16; --bit) {
       const uint32_t up = bound | (1u << bit);
       int above = 0;
@@ -610,6 +663,7 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
         for (int q = 4; q < 8; ++q) above += __popc(__ballot_sync(0xffffffffu, key[q] >= up));
       }
       if (above >= k) bound = up;
+      if (above == k) break;  // no tighter bound is needed
     }
     if (cols.lane == 0) sm.bound = bound;
   }
@@ -738,7 +792,7 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
 }
 
 template <int DT, bool ENT, int SW>
-__global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes)
+__global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW == 1 ? 6 : 4)
     topk_row_kernel(const TopkParams p, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp) {
   constexpr int kRows = SW == 1 ? 4 : 1;  // rows of a block
   __shared__ SelShared<SW> shared[kRows];
@@ -778,7 +832,6 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes)
     cols.warp = SW == 1 ? 0 : warp;
     cols.lane = lane;
     cols.queue = sm.queue[SW == 1 ? 0 : warp];
-    cols.queued = &sm.queued[SW == 1 ? 0 : warp];
     select_columns<DT, SW>(cols, p.k, sm);
   }
   if (SW == 1 || warp == SW) {
@@ -895,10 +948,12 @@ __global__ void __launch_bounds__(BIL_MAX_TOPK + kLanes) topk_grad_fix_kernel(co
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // How the stream kernel is laid out: warps of a block, blocks of an SM.  One
-// stage a warp: a tile is in registers (or, past 8 KB, being reduced) while the
-// others' copies are in flight, and 16 warps (at up to 128 registers a thread)
-// keep 128 KB of them on the way, twice what the latency needs.  Two blocks an
-// SM where that leaves them four warps each or more, else one.
+// stage a warp: its copy is on the way while the tile before it is reduced from
+// registers (or, past 8 KB, while the other warps reduce theirs), and 16 warps
+// (at up to 128 registers a thread) have 128 KB of stages.  (Measured at 16384 x
+// 151936 bf16: two stages for 14 warps 843 us, one for 16 warps 792 us: the
+// reduction's latencies want the warps.)  Two blocks an SM where that leaves
+// them four warps each or more, else one.
 constexpr size_t kSmSmemBytes = 228 * 1024;  // an SM's shared memory, 1 KB of it reserved for each block
 void stream_layout(size_t stage_bytes, int* warps, int* blocks) {
   for (*blocks = 2; *blocks >= 1; --*blocks) {
