@@ -1024,9 +1024,12 @@ int launch_topk_t(TopkParams p, float* logp, float* lse, float* entropy, int64_t
   warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps, (units + slots - 1) / slots)));
   const int64_t grid = std::min<int64_t>(slots, (units + warps - 1) / warps);
   const size_t smem = static_cast<size_t>(warps) * p.stage_bytes;
-  if (smem > static_cast<size_t>(smem_optin)) return BIL_E_UNSUPPORTED;
+  if (smem > static_cast<size_t>(smem_optin) - 1024) return BIL_E_UNSUPPORTED;
   auto kernel = topk_stream_kernel<DT, ALIGNED, ENT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+  // past what needs no opt-in (48 KB with the kernel's own variables); always to the same limit, so that host
+  // threads do not undo each other's
+  if (smem > 47 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) != cudaSuccess)
     return BIL_E_CUDA;
   if (launch_pdl(kernel, grid, warps * kLanes, smem, stream, 1, p) != cudaSuccess) return BIL_E_CUDA;
   // One warp a row from four rows an SM on.

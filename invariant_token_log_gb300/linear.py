@@ -16,11 +16,24 @@ as an LM-head ``Linear`` stores it), both bfloat16 or both float16, rows
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
-from .logp import IGNORE_INDEX, _need_cuda, _on_device, _ptr, _stream, _stream_handle, _targets1d, logp_bwd
+from .logp import (
+    _DEVICE_OBJECTS,
+    IGNORE_INDEX,
+    _device_object,
+    _get_device,
+    _need_cuda,
+    _on_device,
+    _ptr,
+    _stream,
+    _stream_handle,
+    _targets1d,
+    logp_bwd,
+)
 
 LINEAR_TILE_V = _lib.LINEAR_TILE_V
 _IN_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
@@ -143,22 +156,28 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target_ids: torch.Te
     return tuple(out)
 
 
-def _matrix8(x: torch.Tensor, what: str) -> torch.Tensor:
-    """[*lead, H] e4m3 -> [N, H] with unit column stride and 16-byte aligned rows (a view when
-    one exists, else a copy whose rows are padded to 16 bytes)."""
+def _matrix8(x: torch.Tensor, what: str) -> tuple[torch.Tensor, int]:
+    """[*lead, H] e4m3 -> ([N, H] with unit column stride and 16-byte aligned rows, its row
+    stride): a view when one exists, else a copy whose rows are padded to 16 bytes."""
     if x.dtype != torch.float8_e4m3fn:
         raise TypeError(f"{what} must be float8_e4m3fn, not {x.dtype}")
     x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    if x2.shape[0] and (x2.stride(-1) != 1 or _ld(x2) % 16 or x2.data_ptr() % 16):
-        buf = torch.empty((x2.shape[0], -(-x2.shape[1] // 16) * 16), dtype=x2.dtype, device=x2.device)
-        x2 = buf[:, :x2.shape[1]].copy_(x2)
-    return x2
+    n, h = x2.shape
+    ld, unit = x2.stride()
+    ld = ld if n > 1 else max(ld, h)
+    if n and (unit != 1 or ld % 16 or ld < h or x2.data_ptr() % 16):
+        ld = -(-h // 16) * 16
+        x2 = torch.empty_strided((n, h), (ld, 1), dtype=x2.dtype, device=x2.device).copy_(x2)
+    return x2, ld
 
 
-def _scales(s: torch.Tensor, n: int, device: torch.device, what: str) -> torch.Tensor:
-    if s.dtype != torch.float32 or s.numel() != n or s.device != device:
+def _scales(s: torch.Tensor, n: int, index: int, what: str) -> torch.Tensor:
+    if s.dtype != torch.float32 or s.numel() != n or s.get_device() != index:
         raise ValueError(f"{what} must be float32, one per row ({n}), on the operands' device")
-    return s.reshape(-1).contiguous()
+    return s if s.dim() == 1 and s.is_contiguous() else s.reshape(-1).contiguous()
+
+
+_workspace_bytes = functools.lru_cache(maxsize=256)(workspace_bytes)
 
 
 def linear_logp_fp8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch.Tensor,
@@ -172,42 +191,56 @@ def linear_logp_fp8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: to
     (``quantize_rows``, once per weight).  z[r, c] = (hidden_r . weight_c) *
     weight_scale[c] * hidden_scale[r], accumulated in float32 on the tensor cores.
     For serving and scoring: it has no backward."""
-    _need_cuda(hidden, hidden_scale, weight, weight_scale, target_ids, workspace)
+    index = hidden.get_device()
+    if (index < 0 or hidden_scale.get_device() < 0 or weight.get_device() < 0 or weight_scale.get_device() < 0 or
+            target_ids.get_device() < 0):
+        _need_cuda(hidden, hidden_scale, weight, weight_scale, target_ids)
     lead = hidden.shape[:-1]
-    if tuple(target_ids.shape) != tuple(lead):
+    if target_ids.shape != lead:
         raise ValueError(f"target_ids shape {tuple(target_ids.shape)} != hidden's leading shape {tuple(lead)}")
-    h2, w2 = _matrix8(hidden, "hidden"), _matrix8(weight, "weight")
-    if h2.shape[1] != w2.shape[1]:
-        raise ValueError(f"hidden size {h2.shape[1]} != weight's {w2.shape[1]}")
-    n, vocab = h2.shape[0], w2.shape[0]
-    dev = h2.device
-    if w2.device != dev:
+    h2, ld_h = _matrix8(hidden, "hidden")
+    w2, ld_w = _matrix8(weight, "weight")
+    n, hs = h2.shape
+    vocab = w2.shape[0]
+    if hs != w2.shape[1]:
+        raise ValueError(f"hidden size {hs} != weight's {w2.shape[1]}")
+    if w2.get_device() != index:
         raise ValueError("hidden and weight must be on one device")
-    hs, ws = _scales(hidden_scale, n, dev, "hidden_scale"), _scales(weight_scale, vocab, dev, "weight_scale")
+    s_h, s_w = _scales(hidden_scale, n, index, "hidden_scale"), _scales(weight_scale, vocab, index, "weight_scale")
+    dev = _DEVICE_OBJECTS.get(index) or _device_object(index)
     t = _targets1d(target_ids, lead, dev)
     logp = torch.empty(n, dtype=torch.float32, device=dev)
     lse = torch.empty(n, dtype=torch.float32, device=dev)
     ent = torch.empty(n, dtype=torch.float32, device=dev) if return_entropy else None
-    logits = None
+    logits, logits_ptr, ld_logits, logits_code = None, None, 0, _lib.F32
     if return_logits:
         if logits_dtype not in _OUT_DTYPES:
             raise TypeError("logits_dtype must be float32 or bfloat16")
-        logits = torch.empty((n, _pad8(vocab)), dtype=logits_dtype, device=dev)[:, :vocab]
-    need = workspace_bytes(n, vocab, return_entropy)
+        ld_logits, logits_code = _pad8(vocab), _OUT_DTYPES[logits_dtype]
+        logits = torch.empty_strided((n, vocab), (ld_logits, 1), dtype=logits_dtype, device=dev)
+        logits_ptr = logits.data_ptr()
+    need = _workspace_bytes(n, vocab, return_entropy)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
-    _lib.check("bil_linear_logp_fp8_fwd", _on_device(
-        dev.index, _lib.load().bil_linear_logp_fp8_fwd, _ptr(h2), _ptr(hs), _ptr(w2), _ptr(ws), n, h2.shape[1],
-        _ld(h2), vocab, _ld(w2), float(temperature), _ptr(t), ignore_index, _ptr(logp), _ptr(lse), _ptr(ent),
-        _ptr(logits), _OUT_DTYPES.get(logits_dtype, _lib.F32), logits.stride(0) if logits is not None else 0,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), int(validate), _stream_handle(dev.index)))
-    out = [logp.reshape(lead), lse.reshape(lead)]
+        workspace, have = torch.empty(need or 1, dtype=torch.uint8, device=dev), need
+    else:
+        _need_cuda(workspace)
+        have = workspace.numel() * workspace.element_size()
+        if have < need:
+            raise ValueError(f"workspace holds {have} bytes, needs {need}")
+    fn = _lib.load().bil_linear_logp_fp8_fwd
+    args = (h2.data_ptr(), s_h.data_ptr(), w2.data_ptr(), s_w.data_ptr(), n, hs, ld_h, vocab, ld_w, float(temperature),
+            t.data_ptr(), ignore_index, logp.data_ptr(), lse.data_ptr(), ent.data_ptr() if return_entropy else None,
+            logits_ptr, logits_code, ld_logits, workspace.data_ptr(), have, 1 if validate else 0, _stream_handle(index))
+    st = fn(*args) if _get_device() == index else _on_device(index, fn, *args)
+    if st:
+        _lib.check("bil_linear_logp_fp8_fwd", st)
+    out = [logp, lse]
     if return_entropy:
-        out.append(ent.reshape(lead))
+        out.append(ent)
     if return_logits:
-        out.append(logits.reshape(*lead, vocab))
+        out.append(logits)
+    if len(lead) != 1:
+        out = [x.reshape(*lead, *x.shape[1:]) for x in out]
     return tuple(out)
 
 

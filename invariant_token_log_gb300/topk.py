@@ -8,15 +8,19 @@ columns of every row with their log-probabilities, in one pass over the logits;
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
 from .logp import (
+    _DEVICE_OBJECTS,
     DEFAULT_TILE_V,
     IGNORE_INDEX,
     _code,
+    _device_object,
     _f32_1d,
+    _get_device,
     _need_cuda,
     _on_device,
     _ptr,
@@ -27,16 +31,19 @@ from .logp import (
 )
 
 
-def workspace_bytes(dtype: torch.dtype, n_rows: int, vocab: int, k: int, tile_v: int = DEFAULT_TILE_V,
-                    entropy: bool = False, device: torch.device | None = None) -> int:
-    """Device scratch bytes ``logp_topk`` needs on ``device`` (default: the current one)."""
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(dtype: int, n_rows: int, vocab: int, tile_v: int, k: int, entropy: bool) -> int:
     out = ctypes.c_int64(0)
-    args = (_code(dtype), n_rows, vocab, tile_v, k, int(entropy), ctypes.byref(out))
-    fn = _lib.load().bil_logp_topk_workspace_bytes
-    st = fn(*args) if device is None else _on_device(device.index, fn, *args)
+    st = _lib.load().bil_logp_topk_workspace_bytes(dtype, n_rows, vocab, tile_v, k, int(entropy), ctypes.byref(out))
     if st:
         _lib.check("bil_logp_topk_workspace_bytes", st)
     return out.value
+
+
+def workspace_bytes(dtype: torch.dtype, n_rows: int, vocab: int, k: int, tile_v: int = DEFAULT_TILE_V,
+                    entropy: bool = False) -> int:
+    """Device scratch bytes ``logp_topk`` needs (host arithmetic)."""
+    return _workspace_bytes(_code(dtype), n_rows, vocab, tile_v, k, entropy)
 
 
 def _logits2d(logits: torch.Tensor, vocab: int | None) -> tuple[torch.Tensor, int]:
@@ -57,32 +64,46 @@ def logp_topk(logits: torch.Tensor, target_ids: torch.Tensor, k: int, ignore_ind
     column, NaN last) and their float32 log-probabilities.  Ignored rows give -1 and 0.
 
     1 <= k <= min(vocab, 128).  Other arguments as for ``logp_fwd``."""
-    _need_cuda(logits, target_ids, workspace)
+    index = logits.get_device()
+    if index < 0 or target_ids.get_device() < 0:
+        _need_cuda(logits, target_ids)
     lead = logits.shape[:-1]
     x2, v = _logits2d(logits, vocab)
-    n = x2.shape[0]
+    n, width = x2.shape
     k = int(k)
     if not 1 <= k <= min(v, _lib.MAX_TOPK):
         raise ValueError(f"k {k} outside [1, {min(v, _lib.MAX_TOPK)}]")
-    dev = x2.device
+    dev = _DEVICE_OBJECTS.get(index) or _device_object(index)
     t1 = _targets1d(target_ids, lead, dev)
-    stats = torch.empty((3 if return_entropy else 2, n), dtype=torch.float32, device=dev)
+    code = _code(x2.dtype)
+    # one allocation a result: on small batches the host's time is what counts, and a view costs more
+    logp = torch.empty(n, dtype=torch.float32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    entropy = torch.empty(n, dtype=torch.float32, device=dev) if return_entropy else None
     top_ids = torch.empty((n, k), dtype=torch.int64, device=dev)
     top_logp = torch.empty((n, k), dtype=torch.float32, device=dev)
-    need = workspace_bytes(x2.dtype, n, v, k, tile_v, return_entropy, dev)
+    need = _workspace_bytes(code, n, v, tile_v, k, return_entropy)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    elif workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
-    base, row = stats.data_ptr(), 4 * n
-    st = _on_device(dev.index, _lib.load().bil_logp_topk_fwd, x2.data_ptr(), _code(x2.dtype), n, v, _row_stride(x2),
-                    t1.data_ptr(), int(ignore_index), int(tile_v), float(temperature), k, base, base + row,
-                    base + 2 * row if return_entropy else None, top_ids.data_ptr(), top_logp.data_ptr(),
-                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(validate),
-                    _stream_handle(dev.index))
+        workspace, have = torch.empty(need or 1, dtype=torch.uint8, device=dev), need
+    else:
+        _need_cuda(workspace)
+        have = workspace.numel() * workspace.element_size()
+        if have < need or not workspace.is_contiguous():
+            raise ValueError(f"workspace holds {have} bytes, needs {need}")
+    fn = _lib.load().bil_logp_topk_fwd
+    args = (x2.data_ptr(), code, n, v, x2.stride(0) if n > 1 else width, t1.data_ptr(), int(ignore_index), tile_v,
+            float(temperature), k, logp.data_ptr(), lse.data_ptr(), entropy.data_ptr() if return_entropy else None,
+            top_ids.data_ptr(), top_logp.data_ptr(), workspace.data_ptr(), have, 1 if validate else 0,
+            _stream_handle(index))
+    st = fn(*args) if _get_device() == index else _on_device(index, fn, *args)
     if st:
         _lib.check("bil_logp_topk_fwd", st)
-    return (*(s.reshape(lead) for s in stats.unbind(0)), top_ids.reshape(*lead, k), top_logp.reshape(*lead, k))
+    if len(lead) != 1:
+        logp, lse = logp.reshape(lead), lse.reshape(lead)
+        top_ids, top_logp = top_ids.reshape(*lead, k), top_logp.reshape(*lead, k)
+        if return_entropy:
+            entropy = entropy.reshape(lead)
+    return (logp, lse, entropy, top_ids, top_logp) if return_entropy else (logp, lse, top_ids, top_logp)
 
 
 def logp_topk_bwd(logits: torch.Tensor, target_ids: torch.Tensor, top_ids: torch.Tensor, lse: torch.Tensor,
