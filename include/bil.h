@@ -516,7 +516,7 @@ int bil_rms_norm_fwd(const void *x, const void *residual, const void *weight, in
 /*
  * bil_rms_norm_quant -- the same norm with an output in 8 bits and a scale per
  * row, as bil_linear_logp_fp8_fwd reads it: with y as above in float32 (not
- * rounded) and a = max(max_c |y_c|, 2^-100),
+ * rounded) and a = max(rstd * max_c |h_c weight_c|, 2^-100),
  *     scale = a / 448,   q_c = e4m3(y_c * (448 / a))   (to nearest even)
  * so that q_c * scale stands for y_c.  A NaN, or an infinity in the row, makes
  * every q_c * scale of the row NaN.
@@ -627,6 +627,7 @@ int bil_linear_logp_fwd_static(const void *hidden, const void *weight, int dtype
  * accumulator, 64 the copy thread's wait for a free stage, 128 the MMA
  * thread's wait for a stage or a free accumulator, 256 a wait of either for
  * its own copies or MMAs to finish.  512: bil_watchdog_selftest.
+ * bil_logp_topk_fwd: 1 and 8.  bil_rms_norm_bwd: 1024, its wait for a row.
  */
 int bil_watchdog_status(unsigned int *flags, int clear);
 

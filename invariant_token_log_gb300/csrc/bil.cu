@@ -647,9 +647,10 @@ int bil_watchdog_status(unsigned int* flags, int clear) {
   unsigned int linear = 0;
   if (int st = bil_internal::linear_watchdog(&linear, clear)) return st;
   *flags |= linear;
-  unsigned int topk = 0;
+  unsigned int topk = 0, norm = 0;
   if (int st = bil_internal::topk_watchdog(&topk, clear)) return st;
-  *flags |= topk;
+  if (int st = bil_internal::norm_watchdog(&norm, clear)) return st;
+  *flags |= topk | norm;
   return BIL_OK;
 }
 

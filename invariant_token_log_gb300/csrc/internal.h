@@ -51,7 +51,8 @@ class BIL_INTERNAL NvtxRange {
 // bil_watchdog_status); cleared when `clear` is non-zero.
 BIL_INTERNAL int linear_watchdog(unsigned int* flags, int clear);
 
-// The same of the kernels in topk.cu.
+// The same of the kernels in topk.cu and in norm.cu.
 BIL_INTERNAL int topk_watchdog(unsigned int* flags, int clear);
+BIL_INTERNAL int norm_watchdog(unsigned int* flags, int clear);
 
 }  // namespace bil_internal

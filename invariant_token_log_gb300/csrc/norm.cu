@@ -5,7 +5,7 @@
 //     h = round_T(x + r)          (r optional: h = x)
 //     rstd = 1 / sqrt(mean_c h_c^2 + eps)
 //     y = (h rstd) w              stored in h's type T, or as
-//     scale = max(max_c |y_c|, 2^-100) / 448,  q = e4m3(y * (448 / max))
+//     a = max(rstd max_c |h_c w_c|, 2^-100),  scale = a / 448,  q = e4m3(y * (448 / a))
 // and the backward of y (and of h, which goes on as the residual stream):
 //     u = h rstd,  v = dy w,  c = mean(v u)
 //     dx = dr = rstd (v - u c) + dh,    dw = sum over rows of dy u
@@ -13,16 +13,22 @@
 // Everything is float32 between the loads and the stores.  h is rounded to T
 // before it is normed: the stream that the next layer and the backward read is
 // the one the norm saw, so the norm of the sum and the norm of the stored sum
-// are the same bits.  q's scale comes from the float32 y, which is then
-// rounded once, to 8 bits; 2^-100 keeps an all-zero row's scale positive.
+// are the same bits.  q is the float32 y rounded once, to 8 bits.  Its scale
+// comes from the products h w, before rstd is known, so that the row's sum of
+// squares and its maximum are one reduction; 2^-100 keeps an all-zero row's
+// scale positive.
 //
 // Bound: HBM.  Every element is read once and written once (16384 x 4096 bf16:
-// 537 MB, 79 us at the measured copy rate).  A row stays in registers
-// between the reductions: thread r of the row's TPR threads holds the 8-element
-// groups r, r + TPR, ... (at most 4), as the 16-byte units they are read in.
-// TPR and the sums' order follow from the width alone, so a row's bits do not
-// depend on the batch.  A row that does not start on a 16-byte boundary is read
-// by the 16-byte units that hold its elements, shifted into place.
+// 537 MB, 79 us at the measured copy rate).  A row is held between its
+// reduction and its output: thread r of the row's TPR threads has the 8-element
+// groups r, r + TPR, ... (at most 4).  TPR and the sums' order follow from the
+// width alone, so a row's bits do not depend on the batch.  The forward keeps
+// the row in registers, packed, four groups a lane: as many bytes in flight for
+// as few registers and barriers as can be.  The backward, whose registers hold
+// the weight's sums, has two groups a lane and streams its rows through shared
+// memory with bulk copies, a few rows ahead.  A row that does not start on a
+// 16-byte boundary is read by the 16-byte units that hold its elements, shifted
+// into place.
 
 #include "../../include/bil.h"
 #include "device_common.cuh"
@@ -42,9 +48,19 @@ namespace {
 constexpr int kVec = 8;             // elements of a group
 constexpr int kMaxGroups = 4;       // groups a thread holds
 constexpr int kMaxRowThreads = 512;
+constexpr int kMaxStages = 4;       // of the backward's ring
+
+__device__ unsigned int g_watchdog_norm;
+constexpr unsigned kWatchNorm = 1024u;  // the backward's wait for a row
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 static_assert(BIL_MAX_NORM_WIDTH == kMaxRowThreads * kMaxGroups * kVec, "the widest row a block holds");
+
+// How a kernel reads its rows: from anywhere, any width, the weight's type looked
+// up; or (the compiled-out tests are half of the instructions) rows of a
+// multiple of 8 elements on 16-byte boundaries, weight and outputs too, with the
+// weight in the rows' type or in float32.
+enum RowPath { kAnyRows = 0, kFullRows = 1, kFullRowsF32Weight = 2 };
 
 template <int DT>
 struct Row {
@@ -101,6 +117,36 @@ struct Row {
     }
   }
 
+  // As load and store where every row starts on a 16-byte boundary and the width
+  // is a multiple of 8 (PATH != kAnyRows): no part of a unit to leave out.
+  template <int PATH>
+  __device__ static __forceinline__ void load_path(const unsigned char* row, int g, int width, uint32_t (&w)[kW]) {
+    if constexpr (PATH == kAnyRows) {
+      load(row, g, min(kVec, width - g * kVec), w);
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(row) + g * kUnits;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const uint4 q = p[u];
+        w[4 * u] = q.x;
+        w[4 * u + 1] = q.y;
+        w[4 * u + 2] = q.z;
+        w[4 * u + 3] = q.w;
+      }
+    }
+  }
+  template <int PATH>
+  __device__ static __forceinline__ void store_path(unsigned char* row, int g, int width, bool vec,
+                                                    const uint32_t (&w)[kW]) {
+    if constexpr (PATH == kAnyRows) {
+      store(row, g, min(kVec, width - g * kVec), vec, w);
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(row) + g * kUnits;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) p[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    }
+  }
+
   __device__ static __forceinline__ float get(const uint32_t (&w)[kW], int j) {
     if constexpr (DT == BIL_F32) {
       return __uint_as_float(w[j]);
@@ -151,21 +197,26 @@ struct Row {
   }
 };
 
-// The weight's 8 values of group g, in the rows' type or float32.
-template <int DT>
-__device__ __forceinline__ void load_weight(const unsigned char* weight, bool f32, int g, int count, float (&w)[kVec]) {
-  if (DT == BIL_F32 || f32) {
-    uint32_t q[Row<BIL_F32>::kW];
-    Row<BIL_F32>::load(weight, g, count, q);
+// The weight's words of group g, and its values.
+template <int DT, int PATH>
+struct Weight {
+  using W = Row<PATH == kFullRows ? DT : BIL_F32>;  // kAnyRows: widened as it is read
+  uint32_t w[W::kW];
+
+  __device__ __forceinline__ void load(const unsigned char* weight, bool f32, int g, int width) {
+    if constexpr (PATH != kAnyRows) {
+      W::template load_path<PATH>(weight, g, width, w);
+    } else if (DT == BIL_F32 || f32) {
+      W::load(weight, g, min(kVec, width - g * kVec), w);
+    } else {
+      uint32_t q[Row<DT>::kW];
+      Row<DT>::load(weight, g, min(kVec, width - g * kVec), q);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) w[j] = Row<BIL_F32>::get(q, j);
-  } else {
-    uint32_t q[Row<DT>::kW];
-    Row<DT>::load(weight, g, count, q);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) w[j] = Row<DT>::get(q, j);
+      for (int j = 0; j < kVec; ++j) w[j] = __float_as_uint(Row<DT>::get(q, j));
+    }
   }
-}
+  __device__ __forceinline__ float get(int j) const { return W::get(w, j); }
+};
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -173,37 +224,47 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// The row's reductions: a butterfly in each warp, then (more than one warp a
-// row) one over the warps' results.  Every thread gets the same value.  Both
-// reductions of a row use a buffer of their own; the barrier of the one keeps
-// a thread from writing the other's before every thread has read it.
+// A row's reductions: a butterfly in each warp, then (more than one warp a row)
+// one over the warps' results.  Every thread gets the same values.  Two rows'
+// reductions in turn use a buffer of their own: the barrier of the one keeps a
+// thread from writing the other's before every thread has read it.
 struct RowReduce {
-  float* red;    // [2][kMaxRowThreads / kLanes]
+  float2* red;   // [2][kMaxRowThreads / kLanes]
   int warps;     // of the row
   int which = 0;
 
-  template <typename Op>
-  __device__ __forceinline__ float run(float v, Op op, float none) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (warps == 1) return v;
-    float* buf = red + which * (kMaxRowThreads / kLanes);
+  // the sum of s and the maximum (a NaN wins) of m, which is >= 0
+  template <bool SUM, bool MAX>
+  __device__ __forceinline__ void run(float& s, float& m) {
+    butterfly<SUM, MAX>(s, m);
+    if (warps == 1) return;
+    float2* buf = red + which * (kMaxRowThreads / kLanes);
     which ^= 1;
     const int lane = threadIdx.x % kLanes;
-    if (lane == 0) buf[threadIdx.x / kLanes] = v;
+    if (lane == 0) buf[threadIdx.x / kLanes] = make_float2(s, m);
     __syncthreads();
-    v = lane < warps ? buf[lane] : none;
+    const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+    s = v.x;
+    m = v.y;
+    butterfly<SUM, MAX>(s, m);
+  }
+  template <bool SUM, bool MAX>
+  __device__ static __forceinline__ void butterfly(float& s, float& m) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-  }
-  __device__ __forceinline__ float sum(float v) {
-    return run(v, [](float a, float b) { return __fadd_rn(a, b); }, 0.0f);
-  }
-  __device__ __forceinline__ float max_abs(float v) {
-    return run(v, [](float a, float b) { return max_nan(a, b); }, 0.0f);
+    for (int o = 16; o > 0; o >>= 1) {
+      if (SUM) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      if (MAX) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
   }
 };
+
+// 1-D bulk copy global -> shared, completion counted on `bar` in bytes (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, unsigned bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
 struct NormParams {
   const unsigned char* x;
@@ -227,7 +288,11 @@ struct NormParams {
   unsigned char* dx;
   int vec_dx;
   float* dw_part;  // [parts, width]
+  int stages;      // of the ring
 };
+
+// Shared memory of a row that may start anywhere in a 16-byte unit.
+__host__ __device__ inline unsigned slot_bytes(int row_bytes) { return static_cast<unsigned>((row_bytes + 15 + 15) & ~15); }
 
 enum NormMode { kNormPlain = 0, kNormQuant = 1, kQuantOnly = 2 };
 
@@ -238,10 +303,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
-template <int DT, int NG, int MODE>
+template <int DT, int NG, int MODE, int PATH>
 __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormParams p) {
   using R = Row<DT>;
-  __shared__ float red[2 * (kMaxRowThreads / kLanes)];
+  __shared__ float2 red[2 * (kMaxRowThreads / kLanes)];
   griddep_wait();
   griddep_launch_dependents();
   const int tpr = p.row_threads;
@@ -252,11 +317,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   const unsigned char* x = p.x + row * p.ld_x * R::EB;
 
   uint32_t w[NG][R::kW];  // the row's h
-  float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const int g = r + i * tpr;
-    if (g < p.groups) R::load(x, g, min(kVec, p.width - g * kVec), w[i]);
+    if (g < p.groups) R::template load_path<PATH>(x, g, p.width, w[i]);
   }
   if (MODE != kQuantOnly && p.residual != nullptr) {
     const unsigned char* res = p.residual + row * p.ld_r * R::EB;
@@ -264,7 +328,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
-      if (g < p.groups) R::load(res, g, min(kVec, p.width - g * kVec), q[i]);
+      if (g < p.groups) R::template load_path<PATH>(res, g, p.width, q[i]);
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -275,21 +339,27 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(R::get(w[i], j), R::get(q[i], j));
       R::pack(v, w[i]);
       if (p.h != nullptr)
-        R::store(p.h + row * p.ld_h * R::EB, g, min(kVec, p.width - g * kVec), p.vec_h != 0, w[i]);
+        R::template store_path<PATH>(p.h + row * p.ld_h * R::EB, g, p.width, p.vec_h != 0, w[i]);
     }
   }
+  float ss = 0.0f, amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const int g = r + i * tpr;
+    if (g >= p.groups) continue;
+    Weight<DT, PATH> wt;
+    if (MODE == kNormQuant) wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {  // missing elements are zero, and so are their weights
+      const float v = R::get(w[i], j);
+      if (MODE != kQuantOnly) ss = __fmaf_rn(v, v, ss);
+      if (MODE == kNormQuant) amax = max_nan(amax, fabsf(__fmul_rn(v, wt.get(j))));
+      if (MODE == kQuantOnly) amax = max_nan(amax, fabsf(v));
+    }
+  }
+  reduce.run<MODE != kQuantOnly, MODE != kNormPlain>(ss, amax);
   float rstd = 1.0f;
   if (MODE != kQuantOnly) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      if (r + i * tpr >= p.groups) continue;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float v = R::get(w[i], j);
-        ss = __fmaf_rn(v, v, ss);
-      }
-    }
-    ss = reduce.sum(ss);
     const float ms = __fdiv_rn(ss, static_cast<float>(p.width));
     rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ms, p.eps)));
     if (r == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
@@ -299,42 +369,18 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
-      const int count = min(kVec, p.width - g * kVec);
-      float wt[kVec], v[kVec];
-      load_weight<DT>(p.weight, p.weight_f32 != 0, g, count, wt);
+      Weight<DT, PATH> wt;
+      wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+      float v[kVec];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt[j]);
+      for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt.get(j));
       uint32_t o[R::kW];
       R::pack(v, o);
-      R::store(p.y + row * p.ld_y * R::EB, g, count, p.vec_y != 0, o);
+      R::template store_path<PATH>(p.y + row * p.ld_y * R::EB, g, p.width, p.vec_y != 0, o);
     }
   } else {
-    float y[NG][kVec];
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int g = r + i * tpr;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) y[i][j] = 0.0f;
-      if (g >= p.groups) continue;
-      if (MODE == kNormQuant) {
-        float wt[kVec];
-        load_weight<DT>(p.weight, p.weight_f32 != 0, g, min(kVec, p.width - g * kVec), wt);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) y[i][j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt[j]);
-        if (p.width - g * kVec < kVec) {  // a missing element is no part of the maximum (0 * inf would be)
-#pragma unroll
-          for (int j = 0; j < kVec; ++j)
-            if (j >= p.width - g * kVec) y[i][j] = 0.0f;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) y[i][j] = R::get(w[i], j);
-      }
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) amax = max_nan(amax, fabsf(y[i][j]));
-    }
-    amax = max_nan(reduce.max_abs(amax), kMinAmax);
+    if (MODE == kNormQuant) amax = __fmul_rn(amax, rstd);
+    amax = max_nan(amax, kMinAmax);
     const float inv = __fdiv_rn(kE4m3Max, amax);
     if (r == 0) p.scale[row] = __fdiv_rn(amax, kE4m3Max);
     unsigned char* out = p.y + row * p.ld_y;
@@ -343,12 +389,22 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
       const int count = min(kVec, p.width - g * kVec);
+      float y[kVec];
+      if (MODE == kNormQuant) {
+        Weight<DT, PATH> wt;
+        wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) y[j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt.get(j));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) y[j] = R::get(w[i], j);
+      }
       uint32_t q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        q[j] = e4m3x2(__fmul_rn(y[i][2 * j], inv), __fmul_rn(y[i][2 * j + 1], inv));
+        q[j] = e4m3x2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv));
       unsigned char* o = out + static_cast<int64_t>(g) * kVec;
-      if (p.vec_y != 0 && count == kVec) {
+      if (PATH != kAnyRows || (p.vec_y != 0 && count == kVec)) {
         *reinterpret_cast<uint2*>(o) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       } else {
 #pragma unroll
@@ -359,91 +415,207 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   }
 }
 
-// Backward.  A block takes the rows b, b + blocks, ... and keeps its columns'
-// sums of dy u in registers; they go to dw_part as one row a block (a row a
-// warp where a warp takes a row), which norm_dw_kernel adds up in order.
-template <int DT, int NG>
+// Backward.  A block takes the rows b, b + blocks, ... (a warp takes its
+// block's rows in turn where a warp has a row) and keeps its columns' sums of
+// dy u in registers; they go to dw_part as one row a block (the warps' added up
+// in order), which norm_dw_kernel adds up in order.
+// BULK (one row a block): the rows of h, dy and dh come through p.stages stages
+// of shared memory, each operand's 16-byte aligned span in a slot of its own; a
+// stage is refilled once every thread has passed the next row's reduction, when
+// all are done with it.
+template <int DT, int NG, bool BULK, int PATH>
 __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormParams p) {
   using R = Row<DT>;
-  __shared__ float red[2 * (kMaxRowThreads / kLanes)];
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ float2 red[2 * (kMaxRowThreads / kLanes)];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int abort_flag;
   const int tpr = p.row_threads;
   const int r = static_cast<int>(threadIdx.x) % tpr;
   const int64_t part = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const int64_t parts = static_cast<int64_t>(gridDim.x) * (blockDim.x / tpr);
   RowReduce reduce{red, tpr / kLanes};
+  volatile int* abort = &abort_flag;
+  if (BULK) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+      *abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const unsigned slot = slot_bytes(p.width * R::EB);
+  const unsigned stage_bytes = slot * (p.dh != nullptr ? 3u : 2u);
+  // the rows of one stage, by one thread: each from the 16-byte boundary below its first element
+  auto fill = [&](int64_t row, int s) {
+    const unsigned char* src[3] = {p.x + row * p.ld_x * R::EB, p.dy + row * p.ld_dy * R::EB,
+                                   p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr};
+    unsigned bytes[3], total = 0;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(src[q]) & 15u);
+      src[q] -= off;
+      bytes[q] = (off + static_cast<unsigned>(p.width * R::EB) + 15u) & ~15u;
+      if (q < 2 || p.dh != nullptr) total += bytes[q];
+    }
+    mbar_arrive_expect_tx(&full[s], total);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (q < 2 || p.dh != nullptr)
+        bulk_copy(ring + static_cast<size_t>(s) * stage_bytes + q * slot, src[q], bytes[q], &full[s]);
+  };
+  if (BULK && threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s)
+      if (part + s * parts < p.n_rows) fill(part + s * parts, s);
+  }
+  // the weight: in registers, packed, or (kAnyRows) read again each time
+  Weight<DT, PATH> wt[PATH == kAnyRows ? 1 : NG];
+  if (PATH != kAnyRows) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (r + i * tpr < p.groups) wt[PATH == kAnyRows ? 0 : i].load(p.weight, false, r + i * tpr, p.width);
+  }
   float dw[NG][kVec];
 #pragma unroll
   for (int i = 0; i < NG; ++i)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) dw[i][j] = 0.0f;
+  int stage = 0;
+  unsigned parity = 0;
   for (int64_t row = part; row < p.n_rows; row += parts) {
-    const unsigned char* h = p.x + row * p.ld_x * R::EB;
-    const unsigned char* dy = p.dy + row * p.ld_dy * R::EB;
+    const unsigned char* h;
+    const unsigned char* dy;
+    const unsigned char* dh = nullptr;
     const float rstd = p.rstd[row];
-    uint32_t wh[NG][R::kW], wd[NG][R::kW];
+    if (BULK) {
+      // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
+      // barriers still met by every thread, and fills no further stage.)
+      warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm);
+      // a row lies as far past a 16-byte boundary in its slot as in memory
+      const unsigned char* at = ring + static_cast<size_t>(stage) * stage_bytes;
+      h = at;
+      dy = at + slot;
+      if (p.dh != nullptr) dh = at + 2 * slot;
+      if (PATH == kAnyRows) {
+        h += reinterpret_cast<uintptr_t>(p.x + row * p.ld_x * R::EB) & 15u;
+        dy += reinterpret_cast<uintptr_t>(p.dy + row * p.ld_dy * R::EB) & 15u;
+        if (p.dh != nullptr) dh += reinterpret_cast<uintptr_t>(p.dh + row * p.ld_dh * R::EB) & 15u;
+      }
+    } else {
+      h = p.x + row * p.ld_x * R::EB;
+      dy = p.dy + row * p.ld_dy * R::EB;
+      if (p.dh != nullptr) dh = p.dh + row * p.ld_dh * R::EB;
+    }
+    // The row in registers between the two passes, or (BULK) in its stage: then a group at a time.
+    constexpr int kHeld = BULK ? 1 : NG;
+    uint32_t wh[kHeld][R::kW], wd[kHeld][R::kW];
     float dot = 0.0f;
+    if (!BULK) {
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int g = r + i * tpr;
-      if (g >= p.groups) continue;
-      const int count = min(kVec, p.width - g * kVec);
-      R::load(h, g, count, wh[i]);
-      R::load(dy, g, count, wd[i]);
+      for (int i = 0; i < NG; ++i) {
+        const int g = r + i * tpr;
+        if (g >= p.groups) continue;
+        R::template load_path<PATH>(h, g, p.width, wh[i % kHeld]);
+        R::template load_path<PATH>(dy, g, p.width, wd[i % kHeld]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
-      float wt[kVec];
-      load_weight<DT>(p.weight, p.weight_f32 != 0, g, min(kVec, p.width - g * kVec), wt);
+      if (BULK) {
+        R::template load_path<PATH>(h, g, p.width, wh[0]);
+        R::template load_path<PATH>(dy, g, p.width, wd[0]);
+      }
+      Weight<DT, PATH>& now = wt[PATH == kAnyRows ? 0 : i];
+      if (PATH == kAnyRows) now.load(p.weight, p.weight_f32 != 0, g, p.width);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float u = __fmul_rn(R::get(wh[i], j), rstd), d = R::get(wd[i], j);
-        dot = __fmaf_rn(__fmul_rn(d, wt[j]), u, dot);
+        const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd), d = R::get(wd[i % kHeld], j);
+        dot = __fmaf_rn(__fmul_rn(d, now.get(j)), u, dot);
         dw[i][j] = __fmaf_rn(d, u, dw[i][j]);
       }
     }
-    const float c = __fdiv_rn(reduce.sum(dot), static_cast<float>(p.width));
+    float none = 0.0f;
+    reduce.run<true, false>(dot, none);
+    const float c = __fdiv_rn(dot, static_cast<float>(p.width));
+    if (BULK) {
+      // every thread is done with the stage of the row before this one
+      const int64_t refill = row + static_cast<int64_t>(p.stages - 1) * parts;
+      if (threadIdx.x == 0 && row != part && refill < p.n_rows && *abort == 0)
+        fill(refill, stage == 0 ? p.stages - 1 : stage - 1);
+    }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
-      const int count = min(kVec, p.width - g * kVec);
-      float wt[kVec], v[kVec];
-      load_weight<DT>(p.weight, p.weight_f32 != 0, g, count, wt);
+      Weight<DT, PATH>& now = wt[PATH == kAnyRows ? 0 : i];
+      if (PATH == kAnyRows) now.load(p.weight, p.weight_f32 != 0, g, p.width);
+      float v[kVec];
+      if (BULK) {
+        R::template load_path<PATH>(h, g, p.width, wh[0]);
+        R::template load_path<PATH>(dy, g, p.width, wd[0]);
+      }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float u = __fmul_rn(R::get(wh[i], j), rstd);
-        v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i], j), wt[j])));
+        const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd);
+        v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i % kHeld], j), now.get(j))));
       }
-      if (p.dh != nullptr) {
+      if (dh != nullptr) {
         uint32_t q[R::kW];
-        R::load(p.dh + row * p.ld_dh * R::EB, g, count, q);
+        R::template load_path<PATH>(dh, g, p.width, q);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(q, j));
       }
       uint32_t o[R::kW];
       R::pack(v, o);
-      R::store(p.dx + row * p.ld_dx * R::EB, g, count, p.vec_dx != 0, o);
+      R::template store_path<PATH>(p.dx + row * p.ld_dx * R::EB, g, p.width, p.vec_dx != 0, o);
+    }
+    if (++stage == p.stages) {
+      stage = 0;
+      parity ^= 1u;
     }
   }
+  float* out = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width;
+  if (BULK || tpr == static_cast<int>(blockDim.x)) {
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const int g = r + i * tpr;
-    if (g >= p.groups) continue;
+    for (int i = 0; i < NG; ++i) {
+      const int g = r + i * tpr;
+      if (g >= p.groups) continue;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      if (g * kVec + j < p.width) p.dw_part[part * p.width + g * kVec + j] = dw[i][j];
+      for (int j = 0; j < kVec; ++j)
+        if (g * kVec + j < p.width) out[g * kVec + j] = dw[i][j];
+    }
+  } else {  // the block's warps: each row of `ring` is one warp's sums
+    float* sums = reinterpret_cast<float*>(ring);
+    const int pitch = p.groups * kVec, warps = blockDim.x / tpr;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int g = r + i * tpr;
+      if (g >= p.groups) continue;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) sums[static_cast<int>(threadIdx.x) / tpr * pitch + g * kVec + j] = dw[i][j];
+    }
+    __syncthreads();
+    for (int col = threadIdx.x; col < p.width; col += blockDim.x) {
+      float v = sums[col];
+      for (int q = 1; q < warps; ++q) v = __fadd_rn(v, sums[q * pitch + col]);
+      out[col] = v;
+    }
   }
 }
 
 // dw[c] = the parts' sum in a fixed order: warp w of the block adds parts w,
-// w + 8, ... of its 32 columns in order, and the eight sums are added in order.
-constexpr int kDwWarps = 8;
+// w + 16, ... of its 32 columns in order, and the sums are added in order.
+constexpr int kDwWarps = 16;
 
 __global__ void __launch_bounds__(kDwWarps * kLanes) norm_dw_kernel(const float* __restrict__ part, int64_t parts,
                                                                     int width, float* __restrict__ dw) {
   __shared__ float sums[kDwWarps][kLanes];
+  griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
   const int c = static_cast<int>(blockIdx.x) * kLanes + lane;
   float s = 0.0f;
@@ -469,53 +641,64 @@ bool rows_start_on(const void* p, int64_t n_rows, int64_t ld_bytes, size_t a) {
   return aligned_to(p, a) && (n_rows <= 1 || ld_bytes % static_cast<int64_t>(a) == 0);
 }
 
-// A row's threads and the groups each holds, by the width alone: a warp up to
-// 1024 elements (four groups a lane), then the fewest threads, in powers of
-// two up to 512, that hold the row in two groups each; past 8192 elements 512
-// threads hold up to four.
-void row_shape(int width, int* threads, int* per_thread) {
+// A row's threads and the groups each holds (rounded up to what is compiled), by
+// the width alone: as few warps as hold the row in `most` groups a lane (four in
+// the forward, two in the backward, whose rows past 8192 elements take four).
+void row_shape(int width, int most, int* threads, int* per_thread) {
   const int groups = (width + kVec - 1) / kVec;
-  if (groups <= kLanes * kMaxGroups) {
-    *threads = kLanes;
-  } else {
-    int t = 2 * kLanes;
-    while (t < kMaxRowThreads && t * 2 < groups) t *= 2;
-    *threads = t;
-  }
+  if (groups > kMaxRowThreads * most) most = kMaxGroups;
+  *threads = (groups + kLanes * most - 1) / (kLanes * most) * kLanes;
   const int need = (groups + *threads - 1) / *threads;
   *per_thread = need <= 1 ? 1 : need <= 2 ? 2 : 4;
 }
+constexpr int kFwdGroups = 4, kBwdGroups = 2;
 
 // Threads of a block: one row, or eight rows of one warp each.
 int block_threads(int row_threads) { return row_threads == kLanes ? 8 * kLanes : row_threads; }
 
 typedef void (*NormKernel)(NormParams);
 
-template <int MODE>
-NormKernel fwd_kernel(int dtype, int ng) {
-  switch (dtype) {
-    case BIL_F32:
-      return ng == 1 ? norm_fwd_kernel<BIL_F32, 1, MODE> : ng == 2 ? norm_fwd_kernel<BIL_F32, 2, MODE>
-                                                                  : norm_fwd_kernel<BIL_F32, 4, MODE>;
-    case BIL_BF16:
-      return ng == 1 ? norm_fwd_kernel<BIL_BF16, 1, MODE> : ng == 2 ? norm_fwd_kernel<BIL_BF16, 2, MODE>
-                                                                    : norm_fwd_kernel<BIL_BF16, 4, MODE>;
-    default:
-      return ng == 1 ? norm_fwd_kernel<BIL_F16, 1, MODE> : ng == 2 ? norm_fwd_kernel<BIL_F16, 2, MODE>
-                                                                   : norm_fwd_kernel<BIL_F16, 4, MODE>;
-  }
+template <int DT, int MODE, int PATH>
+NormKernel fwd_kernel_ng(int ng) {
+  return ng == 1 ? norm_fwd_kernel<DT, 1, MODE, PATH>
+                 : ng == 2 ? norm_fwd_kernel<DT, 2, MODE, PATH> : norm_fwd_kernel<DT, 4, MODE, PATH>;
 }
 
-NormKernel bwd_kernel_of(int dtype, int ng) {
-  switch (dtype) {
-    case BIL_F32:
-      return ng == 1 ? norm_bwd_kernel<BIL_F32, 1> : ng == 2 ? norm_bwd_kernel<BIL_F32, 2> : norm_bwd_kernel<BIL_F32, 4>;
-    case BIL_BF16:
-      return ng == 1 ? norm_bwd_kernel<BIL_BF16, 1>
-                     : ng == 2 ? norm_bwd_kernel<BIL_BF16, 2> : norm_bwd_kernel<BIL_BF16, 4>;
-    default:
-      return ng == 1 ? norm_bwd_kernel<BIL_F16, 1> : ng == 2 ? norm_bwd_kernel<BIL_F16, 2> : norm_bwd_kernel<BIL_F16, 4>;
-  }
+template <int DT, int MODE>
+NormKernel fwd_kernel_dt(int ng, int path) {
+  if (path == kFullRows) return fwd_kernel_ng<DT, MODE, kFullRows>(ng);
+  if constexpr (DT != BIL_F32 && MODE != kQuantOnly)
+    if (path == kFullRowsF32Weight) return fwd_kernel_ng<DT, MODE, kFullRowsF32Weight>(ng);
+  return fwd_kernel_ng<DT, MODE, kAnyRows>(ng);
+}
+
+template <int MODE>
+NormKernel fwd_kernel(int dtype, int ng, int path) {
+  return dtype == BIL_F32    ? fwd_kernel_dt<BIL_F32, MODE>(ng, path)
+         : dtype == BIL_BF16 ? fwd_kernel_dt<BIL_BF16, MODE>(ng, path)
+                             : fwd_kernel_dt<BIL_F16, MODE>(ng, path);
+}
+
+template <int DT, int PATH>
+NormKernel bwd_kernel_ng(int ng, bool bulk) {
+  if (bulk) return ng <= 2 ? norm_bwd_kernel<DT, 2, true, PATH> : norm_bwd_kernel<DT, 4, true, PATH>;
+  if constexpr (DT == BIL_F32)  // rows too wide for the ring (with dh, past 9472 elements)
+    if (ng == 4) return norm_bwd_kernel<DT, 4, false, PATH>;
+  return ng == 1 ? norm_bwd_kernel<DT, 1, false, PATH> : norm_bwd_kernel<DT, 2, false, PATH>;
+}
+
+template <int DT>
+NormKernel bwd_kernel_dt(int ng, bool bulk, int path) {
+  if (path == kFullRows) return bwd_kernel_ng<DT, kFullRows>(ng, bulk);
+  if constexpr (DT != BIL_F32)
+    if (path == kFullRowsF32Weight) return bwd_kernel_ng<DT, kFullRowsF32Weight>(ng, bulk);
+  return bwd_kernel_ng<DT, kAnyRows>(ng, bulk);
+}
+
+// The rows' path: `full` says that every row starts on a 16-byte boundary.
+int row_path(int64_t width, bool full, const void* weight, bool same_type) {
+  if (!full || width % kVec != 0 || !aligned_to(weight, 16)) return kAnyRows;
+  return same_type ? kFullRows : kFullRowsF32Weight;
 }
 
 // Rows' extent and alignment of one [n_rows, ld] operand of eb-byte elements.
@@ -548,25 +731,52 @@ int launch_fwd(NormKernel kernel, NormParams& p, cudaStream_t s) {
   return launch_pdl(kernel, grid, threads, 0, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
-// Blocks of the backward: four a multiprocessor, at most one a row (eight rows
-// a block where a warp takes a row).
-int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms) {
+// Blocks of the backward: per_sm a multiprocessor, at most one a row (eight
+// rows a block where a warp takes a row).
+constexpr int kBwdPerSm = 4;
+int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms, int per_sm) {
   const int64_t rows_per_block = block_threads(row_threads) / row_threads;
   return std::max<int64_t>(1, std::min<int64_t>((n_rows + rows_per_block - 1) / rows_per_block,
-                                                static_cast<int64_t>(sms) * 4));
+                                                static_cast<int64_t>(sms) * per_sm));
 }
 
-// The backward's partial sums: one row of `width` a block, or a warp.
+// The ring of the backward: the most blocks an SM (up to four, of up to 88
+// registers a thread, or 128 in blocks of more than 256) that leave each three
+// stages, or one block with two.  0 stages: the rows are too wide for that.
+void ring_shape(size_t stage_bytes, int threads, int* per_sm, int* stages) {
+  const int resident = 65536 / (threads * (threads > 256 ? 128 : 88));
+  for (*per_sm = std::max(1, std::min(kBwdPerSm, resident)); *per_sm >= 1; --*per_sm) {
+    const size_t room = static_cast<size_t>(228 * 1024) / *per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
+    *stages = static_cast<int>(std::min<size_t>(kMaxStages, room / stage_bytes));
+    if (*stages >= 3 || (*per_sm == 1 && *stages == 2)) return;
+  }
+  *stages = 0;
+}
+
+// The backward's partial sums, at most: one row of `width` a block.
 int bwd_parts(int64_t n_rows, int64_t width, int64_t* parts) {
   int sms = 0, smem = 0;
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   int threads = 0, ng = 0;
-  row_shape(static_cast<int>(width), &threads, &ng);
-  *parts = bwd_blocks(n_rows, threads, sms) * (block_threads(threads) / threads);
+  row_shape(static_cast<int>(width), kBwdGroups, &threads, &ng);
+  *parts = bwd_blocks(n_rows, threads, sms, kBwdPerSm);
   return BIL_OK;
 }
 
 }  // namespace
+
+namespace bil_internal {
+
+int norm_watchdog(unsigned int* flags, int clear) {
+  if (cudaMemcpyFromSymbol(flags, g_watchdog_norm, sizeof(unsigned int)) != cudaSuccess) return BIL_E_CUDA;
+  if (clear) {
+    const unsigned int zero = 0;
+    if (cudaMemcpyToSymbol(g_watchdog_norm, &zero, sizeof(unsigned int)) != cudaSuccess) return BIL_E_CUDA;
+  }
+  return BIL_OK;
+}
+
+}  // namespace bil_internal
 
 extern "C" {
 
@@ -606,8 +816,11 @@ int bil_rms_norm_fwd(const void* x, const void* residual, const void* weight, in
   p.vec_y = rows_start_on(y, n_rows, ld_y * eb, 16);
   p.vec_h = rows_start_on(h, n_rows, ld_h * eb, 16);
   int ng = 0;
-  row_shape(p.width, &p.row_threads, &ng);
-  return launch_fwd(fwd_kernel<kNormPlain>(dtype, ng), p, reinterpret_cast<cudaStream_t>(stream));
+  row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
+  const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y &&
+                    (residual == nullptr || (rows_start_on(residual, n_rows, ld_residual * eb, 16) && p.vec_h));
+  return launch_fwd(fwd_kernel<kNormPlain>(dtype, ng, row_path(width, full, weight, weight_dtype == dtype)), p,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_rms_norm_quant(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype,
@@ -647,8 +860,11 @@ int bil_rms_norm_quant(const void* x, const void* residual, const void* weight, 
   p.vec_y = rows_start_on(q, n_rows, ld_q, 8);
   p.vec_h = rows_start_on(h, n_rows, ld_h * eb, 16);
   int ng = 0;
-  row_shape(p.width, &p.row_threads, &ng);
-  return launch_fwd(fwd_kernel<kNormQuant>(dtype, ng), p, reinterpret_cast<cudaStream_t>(stream));
+  row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
+  const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y &&
+                    (residual == nullptr || (rows_start_on(residual, n_rows, ld_residual * eb, 16) && p.vec_h));
+  return launch_fwd(fwd_kernel<kNormQuant>(dtype, ng, row_path(width, full, weight, weight_dtype == dtype)), p,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_quantize_rows(const void* x, int dtype, int64_t n_rows, int64_t width, int64_t ld_x, void* q, int64_t ld_q,
@@ -672,8 +888,10 @@ int bil_quantize_rows(const void* x, int dtype, int64_t n_rows, int64_t width, i
   p.scale = scale;
   p.vec_y = rows_start_on(q, n_rows, ld_q, 8);
   int ng = 0;
-  row_shape(p.width, &p.row_threads, &ng);
-  return launch_fwd(fwd_kernel<kQuantOnly>(dtype, ng), p, reinterpret_cast<cudaStream_t>(stream));
+  row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
+  const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y;
+  return launch_fwd(fwd_kernel<kQuantOnly>(dtype, ng, row_path(width, full, nullptr, true)), p,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_rms_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int64_t* bytes) {
@@ -728,13 +946,35 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   p.vec_dx = rows_start_on(dx, n_rows, ld_dx * eb, 16);
   p.dw_part = static_cast<float*>(workspace);
   int ng = 0;
-  row_shape(p.width, &p.row_threads, &ng);
+  row_shape(p.width, kBwdGroups, &p.row_threads, &ng);
   const int threads = block_threads(p.row_threads);
-  bwd_kernel_of(dtype, ng)<<<static_cast<unsigned>(parts / (threads / p.row_threads)), threads, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return BIL_E_CUDA;
-  norm_dw_kernel<<<static_cast<unsigned>((width + kLanes - 1) / kLanes), kDwWarps * kLanes, 0, s>>>(
-      p.dw_part, parts, p.width, dweight);
-  return cudaGetLastError() == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+  // Rows of more than one warp come through the ring.
+  const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (dh != nullptr ? 3 : 2);
+  int per_sm = kBwdPerSm;
+  if (p.row_threads > kLanes) ring_shape(stage_bytes, p.row_threads, &per_sm, &p.stages);
+  const bool bulk = p.stages != 0;
+  if (!bulk) per_sm = kBwdPerSm;
+  int sms = 0, smem_optin = 0;
+  if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  const int64_t grid = bwd_blocks(n_rows, p.row_threads, sms, per_sm);
+  parts = grid;
+  const bool full = rows_start_on(h, n_rows, ld_h * eb, 16) && rows_start_on(dy, n_rows, ld_dy * eb, 16) && p.vec_dx &&
+                    (dh == nullptr || rows_start_on(dh, n_rows, ld_dh * eb, 16));
+  const int path = row_path(width, full, weight, weight_dtype == dtype);
+  NormKernel kernel = dtype == BIL_F32    ? bwd_kernel_dt<BIL_F32>(ng, bulk, path)
+                      : dtype == BIL_BF16 ? bwd_kernel_dt<BIL_BF16>(ng, bulk, path)
+                                          : bwd_kernel_dt<BIL_F16>(ng, bulk, path);
+  const size_t smem = bulk                            ? stage_bytes * p.stages
+                      : threads == p.row_threads ? 0  // the warps' sums
+                                                 : static_cast<size_t>(threads / kLanes) * p.groups * kVec * sizeof(float);
+  if (bulk && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) !=
+                      cudaSuccess)
+    return BIL_E_CUDA;
+  if (launch_pdl(kernel, grid, threads, smem, s, 1, p) != cudaSuccess) return BIL_E_CUDA;
+  return launch_pdl(norm_dw_kernel, (width + kLanes - 1) / kLanes, kDwWarps * kLanes, 0, s, 1,
+                    static_cast<const float*>(p.dw_part), parts, p.width, dweight) == cudaSuccess
+             ? BIL_OK
+             : BIL_E_CUDA;
 }
 
 }  // extern "C"
