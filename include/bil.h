@@ -501,7 +501,7 @@ int bil_linear_logp_fp8_fwd(const void *hidden, const float *hidden_scale, const
  *  residual      NULL, or [n_rows, ld_residual] of dtype; then h, [n_rows, ld_h]
  *                of dtype, receives the sum (it may be the residual's own
  *                buffer, or x's).
- *  weight        [width] of weight_dtype: dtype or BIL_F32.
+ *  weight        [width] of weight_dtype: dtype or BIL_F32; 16-byte aligned.
  *  eps           finite, >= 0.
  *  y             [n_rows, ld_y] of dtype.
  *  rstd          [n_rows] float32 for the backward, or NULL.

@@ -56,11 +56,10 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 static_assert(BIL_MAX_NORM_WIDTH == kMaxRowThreads * kMaxGroups * kVec, "the widest row a block holds");
 
-// How a kernel reads its rows: from anywhere, any width, the weight's type looked
-// up; or (the compiled-out tests are half of the instructions) rows of a
-// multiple of 8 elements on 16-byte boundaries, weight and outputs too, with the
-// weight in the rows' type or in float32.
-enum RowPath { kAnyRows = 0, kFullRows = 1, kFullRowsF32Weight = 2 };
+// How a kernel reads its rows: from anywhere, of any width, or (without the tests
+// that takes, half of the instructions) rows of a multiple of 8 elements on
+// 16-byte boundaries, outputs too; the weight in the rows' type or in float32.
+enum RowPath { kAnyRows = 0, kAnyRowsF32Weight = 1, kFullRows = 2, kFullRowsF32Weight = 3 };
 
 template <int DT>
 struct Row {
@@ -68,42 +67,18 @@ struct Row {
   static constexpr int kW = kVec * EB / 4;    // 32-bit words of a group
   static constexpr int kUnits = kW / 4;       // 16-byte units of an aligned group
 
-  // Group g of the row at `row`: `count` of its 8 elements exist (the others
-  // come out as +0).  Reads only 16-byte units that hold one of them.
-  __device__ static __forceinline__ void load(const unsigned char* row, int g, int count, uint32_t (&w)[kW]) {
-    const unsigned char* p = row + static_cast<int64_t>(g) * kVec * EB;
-    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u);
-    if (off == 0) {
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (count * EB > 16 * u) q = *reinterpret_cast<const uint4*>(p + 16 * u);
-        w[4 * u] = q.x;
-        w[4 * u + 1] = q.y;
-        w[4 * u + 2] = q.z;
-        w[4 * u + 3] = q.w;
-      }
-    } else {
-      uint32_t v[kW + 4];
-#pragma unroll
-      for (int u = 0; u <= kUnits; ++u) {
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (static_cast<int>(off) + count * EB > 16 * u) q = *reinterpret_cast<const uint4*>(p - off + 16 * u);
-        v[4 * u] = q.x;
-        v[4 * u + 1] = q.y;
-        v[4 * u + 2] = q.z;
-        v[4 * u + 3] = q.w;
-      }
-      // the group's first word sits off / 4 words in, then off % 4 bytes down
-#pragma unroll
-      for (int i = 0; i + 2 < kW + 4; ++i)
-        if (off & 8u) v[i] = v[i + 2];
-#pragma unroll
-      for (int i = 0; i + 1 < kW + 2; ++i)
-        if (off & 4u) v[i] = v[i + 1];
-      const unsigned sh = 8u * (off & 3u);
-#pragma unroll
-      for (int j = 0; j < kW; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], sh);
+  // Group g of a row that starts `off` bytes past the 16-byte boundary `base`:
+  // `count` of its 8 elements exist (the others come out as +0).  Reads only
+  // 16-byte units that hold one of them.  The offset is the row's: the branch on
+  // it is uniform.
+  __device__ static __forceinline__ void load(const unsigned char* base, unsigned off, int g, int count,
+                                              uint32_t (&w)[kW]) {
+    const unsigned char* p = base + static_cast<int64_t>(g) * kVec * EB;
+    switch (off >> 2) {
+      case 0: load_from<0>(p, off, count, w); break;
+      case 1: load_from<1>(p, off, count, w); break;
+      case 2: load_from<2>(p, off, count, w); break;
+      default: load_from<3>(p, off, count, w); break;
     }
     if (count < kVec) {
 #pragma unroll
@@ -116,15 +91,39 @@ struct Row {
       }
     }
   }
-
-  // As load and store where every row starts on a 16-byte boundary and the width
-  // is a multiple of 8 (PATH != kAnyRows): no part of a unit to leave out.
-  template <int PATH>
-  __device__ static __forceinline__ void load_path(const unsigned char* row, int g, int width, uint32_t (&w)[kW]) {
-    if constexpr (PATH == kAnyRows) {
-      load(row, g, min(kVec, width - g * kVec), w);
+  // the group's words, WOFF words and off % 4 bytes into the units from p on
+  template <int WOFF>
+  __device__ static __forceinline__ void load_from(const unsigned char* p, unsigned off, int count, uint32_t (&w)[kW]) {
+    uint32_t v[4 * (kUnits + 1)];
+    const int units = (static_cast<int>(off) + count * EB + 15) / 16;
+#pragma unroll
+    for (int u = 0; u <= kUnits; ++u) {
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (u < units) q = *reinterpret_cast<const uint4*>(p + 16 * u);
+      v[4 * u] = q.x;
+      v[4 * u + 1] = q.y;
+      v[4 * u + 2] = q.z;
+      v[4 * u + 3] = q.w;
+    }
+    if constexpr (EB == 4) {
+#pragma unroll
+      for (int j = 0; j < kW; ++j) w[j] = v[j + WOFF];
     } else {
-      const uint4* p = reinterpret_cast<const uint4*>(row) + g * kUnits;
+      const unsigned sh = 8u * (off & 3u);
+#pragma unroll
+      for (int j = 0; j < kW; ++j) w[j] = __funnelshift_r(v[j + WOFF], v[j + WOFF + 1], sh);
+    }
+  }
+
+  // As load and store; no part of a unit to leave out where every row starts on a
+  // 16-byte boundary and the width is a multiple of 8.
+  template <int PATH>
+  __device__ static __forceinline__ void load_path(const unsigned char* base, unsigned off, int g, int width,
+                                                   uint32_t (&w)[kW]) {
+    if constexpr (PATH == kAnyRows || PATH == kAnyRowsF32Weight) {
+      load(base, off, g, min(kVec, width - g * kVec), w);
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(base) + g * kUnits;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const uint4 q = p[u];
@@ -138,7 +137,7 @@ struct Row {
   template <int PATH>
   __device__ static __forceinline__ void store_path(unsigned char* row, int g, int width, bool vec,
                                                     const uint32_t (&w)[kW]) {
-    if constexpr (PATH == kAnyRows) {
+    if constexpr (PATH == kAnyRows || PATH == kAnyRowsF32Weight) {
       store(row, g, min(kVec, width - g * kVec), vec, w);
     } else {
       uint4* p = reinterpret_cast<uint4*>(row) + g * kUnits;
@@ -200,22 +199,23 @@ struct Row {
 // The weight's words of group g, and its values.
 template <int DT, int PATH>
 struct Weight {
-  using W = Row<PATH == kFullRows ? DT : BIL_F32>;  // kAnyRows: widened as it is read
+  using W = Row<PATH == kFullRows || PATH == kAnyRows ? DT : BIL_F32>;
   uint32_t w[W::kW];
 
-  __device__ __forceinline__ void load(const unsigned char* weight, bool f32, int g, int width) {
-    if constexpr (PATH != kAnyRows) {
-      W::template load_path<PATH>(weight, g, width, w);
-    } else if (DT == BIL_F32 || f32) {
-      W::load(weight, g, min(kVec, width - g * kVec), w);
-    } else {
-      uint32_t q[Row<DT>::kW];
-      Row<DT>::load(weight, g, min(kVec, width - g * kVec), q);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) w[j] = __float_as_uint(Row<DT>::get(q, j));
-    }
+  __device__ __forceinline__ void load(const unsigned char* weight, int g, int width) {
+    W::template load_path<PATH>(weight, 0, g, width, w);
   }
   __device__ __forceinline__ float get(int j) const { return W::get(w, j); }
+};
+
+// A row's 16-byte boundary and how far past it the row starts.
+struct RowStart {
+  const unsigned char* base;
+  unsigned off;
+  __device__ __forceinline__ RowStart(const unsigned char* row)
+      : off(static_cast<unsigned>(reinterpret_cast<uintptr_t>(row) & 15u)) {
+    base = row - off;
+  }
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -270,7 +270,6 @@ struct NormParams {
   const unsigned char* x;
   const unsigned char* residual;  // NULL: none
   const unsigned char* weight;    // NULL: the quantisation alone, y = x
-  int weight_f32;
   int64_t n_rows;
   int width, groups;
   int64_t ld_x, ld_r, ld_y, ld_h;  // elements (ld_y of an 8-bit output: bytes)
@@ -288,11 +287,43 @@ struct NormParams {
   unsigned char* dx;
   int vec_dx;
   float* dw_part;  // [parts, width]
-  int stages;      // of the ring
+  int stages;      // of the ring, where there is one
 };
 
 // Shared memory of a row that may start anywhere in a 16-byte unit.
 __host__ __device__ inline unsigned slot_bytes(int row_bytes) { return static_cast<unsigned>((row_bytes + 15 + 15) & ~15); }
+
+// A block's ring of stages, each the rows of up to three operands in slots of
+// their own, which one thread fills with bulk copies of the 16-byte aligned spans
+// that hold them.
+struct RowRing {
+  unsigned char* smem;
+  uint64_t* full;
+  unsigned slot, stage_bytes;
+  int row_bytes;
+
+  __device__ __forceinline__ void fill(int s, const unsigned char* a, const unsigned char* b, const unsigned char* c) {
+    const unsigned char* src[3] = {a, b, c};
+    unsigned bytes[3], total = 0;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(src[q]) & 15u);
+      bytes[q] = (off + static_cast<unsigned>(row_bytes) + 15u) & ~15u;
+      if (src[q] != nullptr) {
+        src[q] -= off;
+        total += bytes[q];
+      }
+    }
+    mbar_arrive_expect_tx(&full[s], total);
+    unsigned at = 0;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      if (src[q] == nullptr) continue;
+      bulk_copy(smem + static_cast<size_t>(s) * stage_bytes + at, src[q], bytes[q], &full[s]);
+      at += slot;
+    }
+  }
+};
 
 enum NormMode { kNormPlain = 0, kNormQuant = 1, kQuantOnly = 2 };
 
@@ -303,32 +334,67 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
+// Rows of whole units: a block takes its rows (eight of one warp each, or one)
+// and is done.  Any rows: one row a block at a time through the ring, a stage
+// refilled as soon as its row is in registers (the registers could not hold
+// the two units a group lies in until they are shifted).
 template <int DT, int NG, int MODE, int PATH>
 __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormParams p) {
   using R = Row<DT>;
+  constexpr bool BULK = PATH < kFullRows;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ float2 red[2 * (kMaxRowThreads / kLanes)];
-  griddep_wait();
-  griddep_launch_dependents();
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
   const int tpr = p.row_threads;
   const int r = static_cast<int>(threadIdx.x) % tpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-  if (row >= p.n_rows) return;  // one warp a row: no barrier follows
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   RowReduce reduce{red, tpr / kLanes};
-  const unsigned char* x = p.x + row * p.ld_x * R::EB;
-
+  RowRing ring{ring_smem, full, slot_bytes(p.width * R::EB), 0, p.width * R::EB};
+  ring.stage_bytes = ring.slot * (p.residual != nullptr ? 2u : 1u);
+  auto fill = [&](int64_t of, int s) {
+    ring.fill(s, p.x + of * p.ld_x * R::EB, p.residual != nullptr ? p.residual + of * p.ld_r * R::EB : nullptr, nullptr);
+  };
+  if (BULK) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+      *abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (row >= p.n_rows) return;  // whole units, one warp a row: no barrier follows
+  if (BULK && threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s)
+      if (row + static_cast<int64_t>(s) * gridDim.x < p.n_rows) fill(row + static_cast<int64_t>(s) * gridDim.x, s);
+  }
+  int stage = 0;
+  unsigned parity = 0;
+  do {
+  RowStart x(p.x + row * p.ld_x * R::EB);
+  RowStart res(p.residual != nullptr ? p.residual + row * p.ld_r * R::EB : nullptr);
+  if (BULK) {
+    // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
+    // barriers still met by every thread, and fills no further stage.)
+    warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm);
+    x.base = ring_smem + static_cast<size_t>(stage) * ring.stage_bytes;
+    res.base = x.base + ring.slot;
+  }
   uint32_t w[NG][R::kW];  // the row's h
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const int g = r + i * tpr;
-    if (g < p.groups) R::template load_path<PATH>(x, g, p.width, w[i]);
+    if (g < p.groups) R::template load_path<PATH>(x.base, x.off, g, p.width, w[i]);
   }
   if (MODE != kQuantOnly && p.residual != nullptr) {
-    const unsigned char* res = p.residual + row * p.ld_r * R::EB;
     uint32_t q[NG][R::kW];
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
-      if (g < p.groups) R::template load_path<PATH>(res, g, p.width, q[i]);
+      if (g < p.groups) R::template load_path<PATH>(res.base, res.off, g, p.width, q[i]);
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
@@ -348,7 +414,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
     const int g = r + i * tpr;
     if (g >= p.groups) continue;
     Weight<DT, PATH> wt;
-    if (MODE == kNormQuant) wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+    if (MODE == kNormQuant) wt.load(p.weight, g, p.width);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {  // missing elements are zero, and so are their weights
       const float v = R::get(w[i], j);
@@ -358,6 +424,15 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
     }
   }
   reduce.run<MODE != kQuantOnly, MODE != kNormPlain>(ss, amax);
+  if (BULK) {  // every thread has the row: its stage takes another
+    if (reduce.warps == 1) __syncwarp();
+    const int64_t refill = row + static_cast<int64_t>(p.stages) * gridDim.x;
+    if (threadIdx.x == 0 && refill < p.n_rows && *abort == 0) fill(refill, stage);
+    if (++stage == p.stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
   float rstd = 1.0f;
   if (MODE != kQuantOnly) {
     const float ms = __fdiv_rn(ss, static_cast<float>(p.width));
@@ -370,7 +445,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
       Weight<DT, PATH> wt;
-      wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+      wt.load(p.weight, g, p.width);
       float v[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt.get(j));
@@ -392,7 +467,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       float y[kVec];
       if (MODE == kNormQuant) {
         Weight<DT, PATH> wt;
-        wt.load(p.weight, p.weight_f32 != 0, g, p.width);
+        wt.load(p.weight, g, p.width);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) y[j] = __fmul_rn(__fmul_rn(R::get(w[i], j), rstd), wt.get(j));
       } else {
@@ -404,7 +479,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       for (int j = 0; j < 4; ++j)
         q[j] = e4m3x2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv));
       unsigned char* o = out + static_cast<int64_t>(g) * kVec;
-      if (PATH != kAnyRows || (p.vec_y != 0 && count == kVec)) {
+      if (PATH >= kFullRows || (p.vec_y != 0 && count == kVec)) {
         *reinterpret_cast<uint2*>(o) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       } else {
 #pragma unroll
@@ -413,6 +488,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       }
     }
   }
+  row += gridDim.x;
+  } while (BULK && row < p.n_rows);
 }
 
 // Backward.  A block takes the rows b, b + blocks, ... (a warp takes its
@@ -446,37 +523,20 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
   }
   griddep_wait();
   griddep_launch_dependents();
-  const unsigned slot = slot_bytes(p.width * R::EB);
-  const unsigned stage_bytes = slot * (p.dh != nullptr ? 3u : 2u);
-  // the rows of one stage, by one thread: each from the 16-byte boundary below its first element
+  RowRing rows{ring, full, slot_bytes(p.width * R::EB), 0, p.width * R::EB};
+  rows.stage_bytes = rows.slot * (p.dh != nullptr ? 3u : 2u);
   auto fill = [&](int64_t row, int s) {
-    const unsigned char* src[3] = {p.x + row * p.ld_x * R::EB, p.dy + row * p.ld_dy * R::EB,
-                                   p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr};
-    unsigned bytes[3], total = 0;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(src[q]) & 15u);
-      src[q] -= off;
-      bytes[q] = (off + static_cast<unsigned>(p.width * R::EB) + 15u) & ~15u;
-      if (q < 2 || p.dh != nullptr) total += bytes[q];
-    }
-    mbar_arrive_expect_tx(&full[s], total);
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      if (q < 2 || p.dh != nullptr)
-        bulk_copy(ring + static_cast<size_t>(s) * stage_bytes + q * slot, src[q], bytes[q], &full[s]);
+    rows.fill(s, p.x + row * p.ld_x * R::EB, p.dy + row * p.ld_dy * R::EB,
+              p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr);
   };
   if (BULK && threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s)
       if (part + s * parts < p.n_rows) fill(part + s * parts, s);
   }
-  // the weight: in registers, packed, or (kAnyRows) read again each time
-  Weight<DT, PATH> wt[PATH == kAnyRows ? 1 : NG];
-  if (PATH != kAnyRows) {
+  Weight<DT, PATH> wt[NG];  // stays in registers, packed
 #pragma unroll
-    for (int i = 0; i < NG; ++i)
-      if (r + i * tpr < p.groups) wt[PATH == kAnyRows ? 0 : i].load(p.weight, false, r + i * tpr, p.width);
-  }
+  for (int i = 0; i < NG; ++i)
+    if (r + i * tpr < p.groups) wt[i].load(p.weight, r + i * tpr, p.width);
   float dw[NG][kVec];
 #pragma unroll
   for (int i = 0; i < NG; ++i)
@@ -485,28 +545,17 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
   int stage = 0;
   unsigned parity = 0;
   for (int64_t row = part; row < p.n_rows; row += parts) {
-    const unsigned char* h;
-    const unsigned char* dy;
-    const unsigned char* dh = nullptr;
+    // where the rows lie in memory and (BULK, as far past a 16-byte boundary) in the stage
+    RowStart h(p.x + row * p.ld_x * R::EB), dy(p.dy + row * p.ld_dy * R::EB);
+    RowStart dh(p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr);
     const float rstd = p.rstd[row];
     if (BULK) {
       // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
       // barriers still met by every thread, and fills no further stage.)
       warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm);
-      // a row lies as far past a 16-byte boundary in its slot as in memory
-      const unsigned char* at = ring + static_cast<size_t>(stage) * stage_bytes;
-      h = at;
-      dy = at + slot;
-      if (p.dh != nullptr) dh = at + 2 * slot;
-      if (PATH == kAnyRows) {
-        h += reinterpret_cast<uintptr_t>(p.x + row * p.ld_x * R::EB) & 15u;
-        dy += reinterpret_cast<uintptr_t>(p.dy + row * p.ld_dy * R::EB) & 15u;
-        if (p.dh != nullptr) dh += reinterpret_cast<uintptr_t>(p.dh + row * p.ld_dh * R::EB) & 15u;
-      }
-    } else {
-      h = p.x + row * p.ld_x * R::EB;
-      dy = p.dy + row * p.ld_dy * R::EB;
-      if (p.dh != nullptr) dh = p.dh + row * p.ld_dh * R::EB;
+      h.base = ring + static_cast<size_t>(stage) * rows.stage_bytes;
+      dy.base = h.base + rows.slot;
+      dh.base = h.base + 2 * rows.slot;
     }
     // The row in registers between the two passes, or (BULK) in its stage: then a group at a time.
     constexpr int kHeld = BULK ? 1 : NG;
@@ -517,8 +566,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
       for (int i = 0; i < NG; ++i) {
         const int g = r + i * tpr;
         if (g >= p.groups) continue;
-        R::template load_path<PATH>(h, g, p.width, wh[i % kHeld]);
-        R::template load_path<PATH>(dy, g, p.width, wd[i % kHeld]);
+        R::template load_path<PATH>(h.base, h.off, g, p.width, wh[i % kHeld]);
+        R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[i % kHeld]);
       }
     }
 #pragma unroll
@@ -526,15 +575,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
       if (BULK) {
-        R::template load_path<PATH>(h, g, p.width, wh[0]);
-        R::template load_path<PATH>(dy, g, p.width, wd[0]);
+        R::template load_path<PATH>(h.base, h.off, g, p.width, wh[0]);
+        R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[0]);
       }
-      Weight<DT, PATH>& now = wt[PATH == kAnyRows ? 0 : i];
-      if (PATH == kAnyRows) now.load(p.weight, p.weight_f32 != 0, g, p.width);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd), d = R::get(wd[i % kHeld], j);
-        dot = __fmaf_rn(__fmul_rn(d, now.get(j)), u, dot);
+        dot = __fmaf_rn(__fmul_rn(d, wt[i].get(j)), u, dot);
         dw[i][j] = __fmaf_rn(d, u, dw[i][j]);
       }
     }
@@ -551,21 +598,19 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
-      Weight<DT, PATH>& now = wt[PATH == kAnyRows ? 0 : i];
-      if (PATH == kAnyRows) now.load(p.weight, p.weight_f32 != 0, g, p.width);
       float v[kVec];
       if (BULK) {
-        R::template load_path<PATH>(h, g, p.width, wh[0]);
-        R::template load_path<PATH>(dy, g, p.width, wd[0]);
+        R::template load_path<PATH>(h.base, h.off, g, p.width, wh[0]);
+        R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[0]);
       }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd);
-        v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i % kHeld], j), now.get(j))));
+        v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i % kHeld], j), wt[i].get(j))));
       }
-      if (dh != nullptr) {
+      if (p.dh != nullptr) {
         uint32_t q[R::kW];
-        R::template load_path<PATH>(dh, g, p.width, q);
+        R::template load_path<PATH>(dh.base, dh.off, g, p.width, q);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(q, j));
       }
@@ -667,8 +712,10 @@ NormKernel fwd_kernel_ng(int ng) {
 template <int DT, int MODE>
 NormKernel fwd_kernel_dt(int ng, int path) {
   if (path == kFullRows) return fwd_kernel_ng<DT, MODE, kFullRows>(ng);
-  if constexpr (DT != BIL_F32 && MODE != kQuantOnly)
+  if constexpr (DT != BIL_F32 && MODE != kQuantOnly) {
     if (path == kFullRowsF32Weight) return fwd_kernel_ng<DT, MODE, kFullRowsF32Weight>(ng);
+    if (path == kAnyRowsF32Weight) return fwd_kernel_ng<DT, MODE, kAnyRowsF32Weight>(ng);
+  }
   return fwd_kernel_ng<DT, MODE, kAnyRows>(ng);
 }
 
@@ -690,14 +737,16 @@ NormKernel bwd_kernel_ng(int ng, bool bulk) {
 template <int DT>
 NormKernel bwd_kernel_dt(int ng, bool bulk, int path) {
   if (path == kFullRows) return bwd_kernel_ng<DT, kFullRows>(ng, bulk);
-  if constexpr (DT != BIL_F32)
+  if constexpr (DT != BIL_F32) {
     if (path == kFullRowsF32Weight) return bwd_kernel_ng<DT, kFullRowsF32Weight>(ng, bulk);
+    if (path == kAnyRowsF32Weight) return bwd_kernel_ng<DT, kAnyRowsF32Weight>(ng, bulk);
+  }
   return bwd_kernel_ng<DT, kAnyRows>(ng, bulk);
 }
 
 // The rows' path: `full` says that every row starts on a 16-byte boundary.
-int row_path(int64_t width, bool full, const void* weight, bool same_type) {
-  if (!full || width % kVec != 0 || !aligned_to(weight, 16)) return kAnyRows;
+int row_path(int64_t width, bool full, bool same_type) {
+  if (!full || width % kVec != 0) return same_type ? kAnyRows : kAnyRowsF32Weight;
   return same_type ? kFullRows : kFullRowsF32Weight;
 }
 
@@ -720,15 +769,33 @@ int check_common(int dtype, int64_t n_rows, int64_t width) {
 int check_weight(const void* weight, int dtype, int weight_dtype) {
   if (weight_dtype != dtype && weight_dtype != BIL_F32) return BIL_E_DTYPE;
   if (weight == nullptr) return BIL_E_INVALID_ARG;
-  return aligned_to(weight, static_cast<size_t>(bil_internal::elem_bytes(weight_dtype))) ? BIL_OK : BIL_E_ALIGN;
+  return aligned_to(weight, 16) ? BIL_OK : BIL_E_ALIGN;
 }
 
-int launch_fwd(NormKernel kernel, NormParams& p, cudaStream_t s) {
-  const int threads = block_threads(p.row_threads);
-  const int64_t rows_per_block = threads / p.row_threads;
-  const int64_t grid = (p.n_rows + rows_per_block - 1) / rows_per_block;
-  if (grid > INT32_MAX) return BIL_E_UNSUPPORTED;
-  return launch_pdl(kernel, grid, threads, 0, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+int launch_fwd(NormKernel kernel, NormParams& p, int path, int eb, cudaStream_t s) {
+  if (path >= kFullRows) {
+    const int threads = block_threads(p.row_threads);
+    const int64_t rows_per_block = threads / p.row_threads;
+    const int64_t grid = (p.n_rows + rows_per_block - 1) / rows_per_block;
+    if (grid > INT32_MAX) return BIL_E_UNSUPPORTED;
+    return launch_pdl(kernel, grid, threads, 0, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+  }
+  // Through the ring: as many blocks as hold 1024 threads an SM, or 640 of float32 (at up to 64, 96 registers
+  // a thread) with two stages each; fewer blocks, then one stage, for the widest rows.
+  int sms = 0, smem_optin = 0;
+  if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (p.residual != nullptr ? 2 : 1);
+  int per_sm = std::max(1, std::min(32, (eb == 4 ? 640 : 1024) / p.row_threads));
+  for (;; --per_sm) {
+    const size_t room = static_cast<size_t>(228 * 1024) / per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
+    p.stages = static_cast<int>(std::min<size_t>(3, room / stage_bytes));
+    if (p.stages >= 2 || per_sm == 1) break;
+  }
+  if (p.stages < 1) return BIL_E_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) != cudaSuccess)
+    return BIL_E_CUDA;
+  const int64_t grid = std::min<int64_t>(p.n_rows, static_cast<int64_t>(sms) * per_sm);
+  return launch_pdl(kernel, grid, p.row_threads, stage_bytes * p.stages, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
 // Blocks of the backward: per_sm a multiprocessor, at most one a row (eight
@@ -741,10 +808,10 @@ int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms, int per_sm) {
 }
 
 // The ring of the backward: the most blocks an SM (up to four, of up to 88
-// registers a thread, or 128 in blocks of more than 256) that leave each three
+// registers a thread, or 128 with four groups a lane) that leave each three
 // stages, or one block with two.  0 stages: the rows are too wide for that.
-void ring_shape(size_t stage_bytes, int threads, int* per_sm, int* stages) {
-  const int resident = 65536 / (threads * (threads > 256 ? 128 : 88));
+void ring_shape(size_t stage_bytes, int threads, int per_thread, int* per_sm, int* stages) {
+  const int resident = 65536 / (threads * (per_thread == 4 ? 128 : 88));
   for (*per_sm = std::max(1, std::min(kBwdPerSm, resident)); *per_sm >= 1; --*per_sm) {
     const size_t room = static_cast<size_t>(228 * 1024) / *per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
     *stages = static_cast<int>(std::min<size_t>(kMaxStages, room / stage_bytes));
@@ -801,7 +868,6 @@ int bil_rms_norm_fwd(const void* x, const void* residual, const void* weight, in
   p.x = static_cast<const unsigned char*>(x);
   p.residual = static_cast<const unsigned char*>(residual);
   p.weight = static_cast<const unsigned char*>(weight);
-  p.weight_f32 = weight_dtype == BIL_F32;
   p.n_rows = n_rows;
   p.width = static_cast<int>(width);
   p.groups = (p.width + kVec - 1) / kVec;
@@ -819,8 +885,8 @@ int bil_rms_norm_fwd(const void* x, const void* residual, const void* weight, in
   row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
   const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y &&
                     (residual == nullptr || (rows_start_on(residual, n_rows, ld_residual * eb, 16) && p.vec_h));
-  return launch_fwd(fwd_kernel<kNormPlain>(dtype, ng, row_path(width, full, weight, weight_dtype == dtype)), p,
-                    reinterpret_cast<cudaStream_t>(stream));
+  const int path = row_path(width, full, weight_dtype == dtype);
+  return launch_fwd(fwd_kernel<kNormPlain>(dtype, ng, path), p, path, eb, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_rms_norm_quant(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype,
@@ -845,7 +911,6 @@ int bil_rms_norm_quant(const void* x, const void* residual, const void* weight, 
   p.x = static_cast<const unsigned char*>(x);
   p.residual = static_cast<const unsigned char*>(residual);
   p.weight = static_cast<const unsigned char*>(weight);
-  p.weight_f32 = weight_dtype == BIL_F32;
   p.n_rows = n_rows;
   p.width = static_cast<int>(width);
   p.groups = (p.width + kVec - 1) / kVec;
@@ -863,8 +928,8 @@ int bil_rms_norm_quant(const void* x, const void* residual, const void* weight, 
   row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
   const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y &&
                     (residual == nullptr || (rows_start_on(residual, n_rows, ld_residual * eb, 16) && p.vec_h));
-  return launch_fwd(fwd_kernel<kNormQuant>(dtype, ng, row_path(width, full, weight, weight_dtype == dtype)), p,
-                    reinterpret_cast<cudaStream_t>(stream));
+  const int path = row_path(width, full, weight_dtype == dtype);
+  return launch_fwd(fwd_kernel<kNormQuant>(dtype, ng, path), p, path, eb, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_quantize_rows(const void* x, int dtype, int64_t n_rows, int64_t width, int64_t ld_x, void* q, int64_t ld_q,
@@ -890,8 +955,8 @@ int bil_quantize_rows(const void* x, int dtype, int64_t n_rows, int64_t width, i
   int ng = 0;
   row_shape(p.width, kFwdGroups, &p.row_threads, &ng);
   const bool full = rows_start_on(x, n_rows, ld_x * eb, 16) && p.vec_y;
-  return launch_fwd(fwd_kernel<kQuantOnly>(dtype, ng, row_path(width, full, nullptr, true)), p,
-                    reinterpret_cast<cudaStream_t>(stream));
+  const int path = row_path(width, full, true);
+  return launch_fwd(fwd_kernel<kQuantOnly>(dtype, ng, path), p, path, eb, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int bil_rms_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int64_t* bytes) {
@@ -931,7 +996,6 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   NormParams p{};
   p.x = static_cast<const unsigned char*>(h);
   p.weight = static_cast<const unsigned char*>(weight);
-  p.weight_f32 = weight_dtype == BIL_F32;
   p.n_rows = n_rows;
   p.width = static_cast<int>(width);
   p.groups = (p.width + kVec - 1) / kVec;
@@ -951,7 +1015,7 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   // Rows of more than one warp come through the ring.
   const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (dh != nullptr ? 3 : 2);
   int per_sm = kBwdPerSm;
-  if (p.row_threads > kLanes) ring_shape(stage_bytes, p.row_threads, &per_sm, &p.stages);
+  if (p.row_threads > kLanes) ring_shape(stage_bytes, p.row_threads, ng, &per_sm, &p.stages);
   const bool bulk = p.stages != 0;
   if (!bulk) per_sm = kBwdPerSm;
   int sms = 0, smem_optin = 0;
@@ -960,7 +1024,7 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   parts = grid;
   const bool full = rows_start_on(h, n_rows, ld_h * eb, 16) && rows_start_on(dy, n_rows, ld_dy * eb, 16) && p.vec_dx &&
                     (dh == nullptr || rows_start_on(dh, n_rows, ld_dh * eb, 16));
-  const int path = row_path(width, full, weight, weight_dtype == dtype);
+  const int path = row_path(width, full, weight_dtype == dtype);
   NormKernel kernel = dtype == BIL_F32    ? bwd_kernel_dt<BIL_F32>(ng, bulk, path)
                       : dtype == BIL_BF16 ? bwd_kernel_dt<BIL_BF16>(ng, bulk, path)
                                           : bwd_kernel_dt<BIL_F16>(ng, bulk, path);

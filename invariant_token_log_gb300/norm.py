@@ -66,7 +66,8 @@ def _weight(weight: torch.Tensor, x: torch.Tensor, width: int) -> torch.Tensor:
         raise ValueError("weight must be on the rows' device")
     if weight.dtype != x.dtype and weight.dtype != torch.float32:
         raise TypeError("weight must have the rows' type or float32")
-    return weight.contiguous()
+    weight = weight.contiguous()
+    return weight if weight.data_ptr() % 16 == 0 else weight.clone()
 
 
 def _check_width(width: int) -> None:
