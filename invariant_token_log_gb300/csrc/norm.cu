@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
     }
     // The row in registers between the two passes, or (BULK) in its stage: then a group at a time.
     constexpr int kHeld = BULK ? 1 : NG;
-    uint32_t wh[kHeld][R::kW], wd[kHeld][R::kW];
+    uint32_t wh[kHeld][R::kW], wd[kHeld][R::kW], wg[kHeld][R::kW];
     float dot = 0.0f;
     if (!BULK) {
 #pragma unroll
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
         if (g >= p.groups) continue;
         R::template load_path<PATH>(h.base, h.off, g, p.width, wh[i % kHeld]);
         R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[i % kHeld]);
+        if (p.dh != nullptr) R::template load_path<PATH>(dh.base, dh.off, g, p.width, wg[i % kHeld]);
       }
     }
 #pragma unroll
@@ -609,10 +610,9 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
         v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i % kHeld], j), wt[i].get(j))));
       }
       if (p.dh != nullptr) {
-        uint32_t q[R::kW];
-        R::template load_path<PATH>(dh.base, dh.off, g, p.width, q);
+        if (BULK) R::template load_path<PATH>(dh.base, dh.off, g, p.width, wg[0]);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(q, j));
+        for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(wg[i % kHeld], j));
       }
       uint32_t o[R::kW];
       R::pack(v, o);
@@ -799,20 +799,22 @@ int launch_fwd(NormKernel kernel, NormParams& p, int path, int eb, cudaStream_t 
 }
 
 // Blocks of the backward: per_sm a multiprocessor, at most one a row (eight
-// rows a block where a warp takes a row).
-constexpr int kBwdPerSm = 4;
+// rows a block where a warp takes a row): 768 threads an SM at up to 88
+// registers, or 512 at 128 with four groups a lane; 1024 where a warp takes a row.
+int bwd_per_sm(int row_threads, int per_thread) {
+  if (row_threads == kLanes) return 4;
+  return std::max(1, (per_thread == 4 ? 512 : 768) / row_threads);
+}
 int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms, int per_sm) {
   const int64_t rows_per_block = block_threads(row_threads) / row_threads;
   return std::max<int64_t>(1, std::min<int64_t>((n_rows + rows_per_block - 1) / rows_per_block,
                                                 static_cast<int64_t>(sms) * per_sm));
 }
 
-// The ring of the backward: the most blocks an SM (up to four, of up to 88
-// registers a thread, or 128 with four groups a lane) that leave each three
-// stages, or one block with two.  0 stages: the rows are too wide for that.
-void ring_shape(size_t stage_bytes, int threads, int per_thread, int* per_sm, int* stages) {
-  const int resident = 65536 / (threads * (per_thread == 4 ? 128 : 88));
-  for (*per_sm = std::max(1, std::min(kBwdPerSm, resident)); *per_sm >= 1; --*per_sm) {
+// The ring of the backward: of up to *per_sm blocks an SM the most that leave each
+// three stages, or one block with two.  0 stages: the rows are too wide for that.
+void ring_shape(size_t stage_bytes, int* per_sm, int* stages) {
+  for (; *per_sm >= 1; --*per_sm) {
     const size_t room = static_cast<size_t>(228 * 1024) / *per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
     *stages = static_cast<int>(std::min<size_t>(kMaxStages, room / stage_bytes));
     if (*stages >= 3 || (*per_sm == 1 && *stages == 2)) return;
@@ -826,7 +828,7 @@ int bwd_parts(int64_t n_rows, int64_t width, int64_t* parts) {
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   int threads = 0, ng = 0;
   row_shape(static_cast<int>(width), kBwdGroups, &threads, &ng);
-  *parts = bwd_blocks(n_rows, threads, sms, kBwdPerSm);
+  *parts = bwd_blocks(n_rows, threads, sms, bwd_per_sm(threads, ng));
   return BIL_OK;
 }
 
@@ -1014,10 +1016,10 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   const int threads = block_threads(p.row_threads);
   // Rows of more than one warp come through the ring.
   const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (dh != nullptr ? 3 : 2);
-  int per_sm = kBwdPerSm;
-  if (p.row_threads > kLanes) ring_shape(stage_bytes, p.row_threads, ng, &per_sm, &p.stages);
+  int per_sm = bwd_per_sm(p.row_threads, ng);
+  if (p.row_threads > kLanes) ring_shape(stage_bytes, &per_sm, &p.stages);
   const bool bulk = p.stages != 0;
-  if (!bulk) per_sm = kBwdPerSm;
+  if (!bulk) per_sm = bwd_per_sm(p.row_threads, ng);
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   const int64_t grid = bwd_blocks(n_rows, p.row_threads, sms, per_sm);
