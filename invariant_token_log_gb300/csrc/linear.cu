@@ -288,6 +288,34 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[kChunk])
       : "memory");
 }
 
+// The same load without the wait, and the wait for every load issued so far
+// (which hands out the registers of one of them, so that no use of these can be
+// scheduled before it): what comes between the two runs while the data is on
+// its way.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[kChunk]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[kChunk]) {
+  __syncwarp();
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 // Row tile m and column tile n of work unit u: groups of `group` row tiles;
 // within a group the row tile varies fastest, so the blocks working at one
 // time share a few B tiles (and their A tiles) through L2.
@@ -479,83 +507,121 @@ __device__ __forceinline__ void row_partial(uint32_t taddr, int vcols, float rcp
 // (sw: the column's scale, sh >= 0: the row's); the partial takes the row's
 // scale out of the maximum and into the exponent's constant:
 //   mx = max over valid c of v_c (exact);  m = (mx *rn sh) *rn rcp
-//   t_c = (v_c -rn mx) *rn c,  c = (sh *rn rcp) *rn log2e
-// with e_c, the eight slots, the tree and the entropy sum of row_partial; the
-// target logit is (v_t *rn sh) *rn rcp.  `sw` is the warp's copy of the tile's
-// column scales in shared memory (every lane reads the same word: a
-// broadcast).  With `box_map` the logits z_c go out through the warp's staging
-// boxes.  Both passes run on packed float32 pairs.
-template <bool ENT>
+//   t_c = fma(v_c, c, -(mx *rn c)),  c = (sh *rn rcp) *rn log2e
+// with e_c = 2^t_c, the eight slots, the tree and the entropy sum of row_partial
+// (no clamp: an accumulator is never infinite); the target logit is (v_t *rn sh)
+// *rn rcp.  `sw` is the warp's copy of the tile's column scales in shared memory
+// (every lane reads the same word: a broadcast).  With `box_map` the logits z_c
+// go out through the warp's staging boxes.
+//
+// A tile's MMAs take 16384 cycles at K = 4096, half of the 16-bit kernel's, and
+// this, one warp per scheduler, has to keep below that: packed float32 pairs, the
+// column tests only in a tile that is cut off (FULL: none is), the target looked
+// for only in a chunk of 32 columns that holds one of the warp's, each chunk
+// loaded from tensor memory while the one before it is worked on.  (Before, at
+// 2048 x 38912 x 4096: 5.6 k instructions a warp and tile, tensor pipe 78%
+// active, the epilogue the bound.)
+template <bool ENT, bool FULL>
 __device__ __forceinline__ void row_partial8(uint32_t taddr, int vcols, float rcp, float sh, const float* sw,
                                              int64_t tloc, int out_dtype, float& m_out, float& s_out, float& u_out,
                                              float& tl_out, const CUtensorMap* box_map, unsigned char* staging,
                                              int box_x, int box_y, int lane, uint32_t* issued) {
-  uint32_t r[kChunk];
+  uint32_t ra[kChunk], rb[kChunk];
   float mx = -INFINITY;
   float tl = 0.0f;
+  const int target_chunk = tloc >= 0 && tloc < kBN ? static_cast<int>(tloc) / kChunk : -1;
   const uint64_t sh2 = pk(sh, sh);
-#pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += kChunk) {
-    tmem_ld32(taddr + c0, r);
+  auto pair = [](const uint32_t (&r)[kChunk], int k) {
+    return static_cast<uint64_t>(r[k]) | (static_cast<uint64_t>(r[k + 1]) << 32);
+  };
+  auto first_pass = [&](uint32_t (&r)[kChunk], int c0) {
+    uint64_t v[kChunk / 2];
 #pragma unroll
     for (int k = 0; k < kChunk; k += 4) {
       const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
-      const uint64_t v0 = mul2(static_cast<uint64_t>(r[k]) | (static_cast<uint64_t>(r[k + 1]) << 32), w.x);
-      const uint64_t v1 = mul2(static_cast<uint64_t>(r[k + 2]) | (static_cast<uint64_t>(r[k + 3]) << 32), w.y);
-      const float v[4] = {lo_of(v0), hi_of(v0), lo_of(v1), hi_of(v1)};
+      v[k / 2] = mul2(pair(r, k), w.x);
+      v[k / 2 + 1] = mul2(pair(r, k + 2), w.y);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (c0 + k + j < vcols) mx = fmaxf(mx, v[j]);
-        if (c0 + k + j == tloc) tl = v[j];
-      }
-      if (box_map != nullptr) {
-        const uint64_t z0 = mul2(v0, sh2), z1 = mul2(v1, sh2);
-        r[k] = __float_as_uint(lo_of(z0));
-        r[k + 1] = __float_as_uint(hi_of(z0));
-        r[k + 2] = __float_as_uint(lo_of(z1));
-        r[k + 3] = __float_as_uint(hi_of(z1));
+    for (int k = 0; k < kChunk; k += 2) {
+      if (FULL || c0 + k < vcols) mx = fmaxf(mx, lo_of(v[k / 2]));
+      if (FULL || c0 + k + 1 < vcols) mx = fmaxf(mx, hi_of(v[k / 2]));
+    }
+    if (__any_sync(0xffffffffu, target_chunk == c0 / kChunk)) {
+#pragma unroll
+      for (int k = 0; k < kChunk; k += 2) {
+        if (c0 + k == tloc) tl = lo_of(v[k / 2]);
+        if (c0 + k + 1 == tloc) tl = hi_of(v[k / 2]);
       }
     }
-    if (box_map != nullptr && c0 < vcols) {
+    if (box_map != nullptr && (FULL || c0 < vcols)) {
+#pragma unroll
+      for (int k = 0; k < kChunk / 2; ++k) v[k] = mul2(v[k], sh2);
       if (out_dtype == BIL_F32) {  // two boxes of 16 columns
         uint32_t w0[16], w1[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          w0[j] = r[j];
-          w1[j] = r[16 + j];
+        for (int j = 0; j < 8; ++j) {
+          w0[2 * j] = __float_as_uint(lo_of(v[j]));
+          w0[2 * j + 1] = __float_as_uint(hi_of(v[j]));
+          w1[2 * j] = __float_as_uint(lo_of(v[8 + j]));
+          w1[2 * j + 1] = __float_as_uint(hi_of(v[8 + j]));
         }
         store_box(staging, box_map, box_x + c0, box_y, lane, *issued, w0);
         store_box(staging, box_map, box_x + c0 + 16, box_y, lane, *issued, w1);
       } else {
         uint32_t pk16[kChunk / 2];
 #pragma unroll
-        for (int j = 0; j < kChunk; j += 2) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-          pk16[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int j = 0; j < kChunk / 2; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(v[j]), hi_of(v[j]));
+          pk16[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
         store_box(staging, box_map, box_x + c0, box_y, lane, *issued, pk16);
       }
     }
+  };
+  uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
+  uint64_t c2 = 0, shift2 = 0;
+  auto second_pass = [&](uint32_t (&r)[kChunk], int c0) {
+#pragma unroll
+    for (int k = 0; k < kChunk; k += 4) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t t = fma2(mul2(pair(r, k + 2 * h), h == 0 ? w.x : w.y), c2, shift2);
+        float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
+        if (!FULL) {  // columns past the vocabulary add nothing
+          if (c0 + k + 2 * h >= vcols) e0 = 0.0f;
+          if (c0 + k + 2 * h + 1 >= vcols) e1 = 0.0f;
+        }
+        const uint64_t e = pk(e0, e1);
+        const int slot = (k / 2 + h) % 4;
+        a2[slot] = add2(a2[slot], e);
+        if (ENT) u2[slot] = fma2(e, t, u2[slot]);
+      }
+    }
+  };
+  tmem_ld32_issue(taddr, ra);
+#pragma unroll 1
+  for (int c0 = 0; c0 < kBN; c0 += 2 * kChunk) {
+    tmem_ld_wait(ra);
+    tmem_ld32_issue(taddr + c0 + kChunk, rb);
+    first_pass(ra, c0);
+    tmem_ld_wait(rb);
+    tmem_ld32_issue(taddr + (c0 + 2 * kChunk) % kBN, ra);  // the last one: the second pass's first
+    first_pass(rb, c0 + kChunk);
   }
   const float shift = (mx == -INFINITY) ? 0.0f : mx;
   const float c = __fmul_rn(__fmul_rn(sh, rcp), kLog2e);
-  uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
-  const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
+  c2 = pk(c, c);
+  shift2 = pk(-__fmul_rn(shift, c), -__fmul_rn(shift, c));
 #pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += kChunk) {
-    tmem_ld32(taddr + c0, r);
-#pragma unroll
-    for (int k = 0; k < kChunk / 2; ++k) {
-      const uint64_t w = *reinterpret_cast<const uint64_t*>(sw + c0 + 2 * k);
-      const uint64_t v = mul2(static_cast<uint64_t>(r[2 * k]) | (static_cast<uint64_t>(r[2 * k + 1]) << 32), w);
-      const uint64_t t = mul2(sub2(v, shift2), c2);
-      float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
-      if (c0 + 2 * k >= vcols) e0 = 0.0f;  // columns past the vocabulary add nothing
-      if (c0 + 2 * k + 1 >= vcols) e1 = 0.0f;
-      const uint64_t e = pk(e0, e1);
-      a2[k % 4] = add2(a2[k % 4], e);
-      if (ENT) u2[k % 4] = fma2(e, pk(fmaxf(lo_of(t), kNegMax), fmaxf(hi_of(t), kNegMax)), u2[k % 4]);
-    }
+  for (int c0 = 0; c0 < kBN; c0 += 2 * kChunk) {
+    tmem_ld_wait(ra);
+    tmem_ld32_issue(taddr + c0 + kChunk, rb);
+    second_pass(ra, c0);
+    tmem_ld_wait(rb);
+    if (c0 + 2 * kChunk < kBN) tmem_ld32_issue(taddr + c0 + 2 * kChunk, ra);
+    second_pass(rb, c0 + kChunk);
   }
   m_out = __fmul_rn(__fmul_rn(mx, sh), rcp);
   s_out = __fadd_rn(__fadd_rn(__fadd_rn(lo_of(a2[0]), hi_of(a2[0])), __fadd_rn(lo_of(a2[1]), hi_of(a2[1]))),
@@ -1020,9 +1086,15 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
         if (!warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear)) break;
         tc_fence_after();
         float mt, st, ut = 0.0f, tl;
-        row_partial8<ENT>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl,
-                          p.logits != nullptr ? &tmap_out : nullptr, staging_all + q * 2 * kStoreBoxBytes,
-                          static_cast<int>(col0), static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
+        const CUtensorMap* boxes = p.logits != nullptr ? &tmap_out : nullptr;
+        if (vcols == kBN)
+          row_partial8<ENT, true>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes,
+                                  staging_all + q * 2 * kStoreBoxBytes, static_cast<int>(col0),
+                                  static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
+        else
+          row_partial8<ENT, false>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes,
+                                   staging_all + q * 2 * kStoreBoxBytes, static_cast<int>(col0),
+                                   static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
