@@ -43,6 +43,8 @@
 //                            tcgen05.mma kind::f8f6f4 over 128-element K
 //                            blocks (the same 128-byte lines), the partial
 //                            of the accumulator scaled by row and column.
+// For more than 128 rows that forward has a kernel of its own on pairs of blocks,
+// linear_partials8_pair_kernel.
 //
 // What fixes the bits of z[r, c] is the K order (K blocks in order, four
 // K=16 steps each, from a zeroed accumulator), the same for every row and
@@ -54,6 +56,7 @@
 #include "../../include/bil.h"
 #include "device_common.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 #include <cuda.h>  // CUtensorMap and its enums (types only; the encoder is fetched at run time)
 #include <cuda_bf16.h>
@@ -743,6 +746,53 @@ __device__ __forceinline__ void row_store(uint32_t taddr, int vcols, bool valid,
   }
 }
 
+// The 8-bit forward's epilogue of column tile n for one warp: row `row` (of the
+// lane; the warp's are 32 consecutive ones) of the accumulator at `taddr`.
+// `wait` waits for the accumulator, `release` (one lane) hands it back.  False: the
+// wait ran out.
+template <bool ENT, typename Wait, typename Release>
+__device__ __forceinline__ bool epilogue8(const LinearParams& p, const CUtensorMap& tmap_out, uint32_t taddr,
+                                          unsigned char* staging, float* sw, int64_t row, int n, int lane,
+                                          uint32_t& store_boxes, Wait wait, Release release) {
+  const bool valid = row < p.n_rows;
+  const int64_t col0 = static_cast<int64_t>(n) * kBN;
+  const int vcols = static_cast<int>(p.shard_cols - col0 < kBN ? p.shard_cols - col0 : kBN);
+  const int64_t t = valid ? p.targets[row] : p.ignore_index;
+  const bool active = valid && t != p.ignore_index;
+  const int64_t tloc = active ? t - col0 : -1;
+  const float sh = valid ? p.row_scale[row] : 0.0f;
+  // the tile's column scales, while its MMAs run (the warp's reads of the last tile's are done)
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < kBN / kLanes; ++j) {
+    const int c = j * kLanes + lane;
+    sw[c] = c < vcols ? p.col_scale[col0 + c] : 0.0f;
+  }
+  __syncwarp();
+  if (!wait()) return false;
+  tc_fence_after();
+  float mt, st, ut = 0.0f, tl;
+  const CUtensorMap* boxes = p.logits != nullptr ? &tmap_out : nullptr;
+  const int box_y = static_cast<int>(row - lane);
+  if (vcols == kBN)
+    row_partial8<ENT, true>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes, staging,
+                            static_cast<int>(col0), box_y, lane, &store_boxes);
+  else
+    row_partial8<ENT, false>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes, staging,
+                             static_cast<int>(col0), box_y, lane, &store_boxes);
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) release();
+  if (valid) {
+    const int64_t at = row * p.ld_part + n;
+    p.part_max[at] = active ? mt : -INFINITY;
+    p.part_sum[at] = active ? st : 0.0f;
+    if (ENT) p.part_ent[at] = active ? ut : 0.0f;
+    if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------------------
 // Soft lockstep of the store GEMMs' copy threads.  Their K is long (the
 // vocabulary for dhidden), and the blocks of one wave read the same A and B
@@ -914,6 +964,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
+  if (kOp8) {  // launched while its predecessor finishes
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   const int64_t total = static_cast<int64_t>(p.num_m) * p.num_n;
 
@@ -1070,41 +1124,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
       } else if constexpr (MODE == kModePartials8) {
         unsigned char* staging_all = reinterpret_cast<unsigned char*>(
             (reinterpret_cast<uintptr_t>(&sm + 1) + 1023) & ~static_cast<uintptr_t>(1023));
-        float* sw = reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN;
-        const int64_t t = valid ? p.targets[row] : p.ignore_index;
-        const bool active = valid && t != p.ignore_index;
-        const int64_t tloc = active ? t - static_cast<int64_t>(p.tile_begin + n) * kBN : -1;
-        const float sh = valid ? p.row_scale[row] : 0.0f;
-        // the tile's column scales, while its MMAs run (the warp's reads of the last tile's are done)
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < kBN / kLanes; ++j) {
-          const int c = j * kLanes + lane;
-          sw[c] = c < vcols ? __ldg(p.col_scale + col0 + c) : 0.0f;
-        }
-        __syncwarp();
-        if (!warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear)) break;
-        tc_fence_after();
-        float mt, st, ut = 0.0f, tl;
-        const CUtensorMap* boxes = p.logits != nullptr ? &tmap_out : nullptr;
-        if (vcols == kBN)
-          row_partial8<ENT, true>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes,
-                                  staging_all + q * 2 * kStoreBoxBytes, static_cast<int>(col0),
-                                  static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
-        else
-          row_partial8<ENT, false>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes,
-                                   staging_all + q * 2 * kStoreBoxBytes, static_cast<int>(col0),
-                                   static_cast<int>(m * kBM + q * 32), lane, &store_boxes);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
-        if (valid) {
-          const int64_t at = row * p.ld_part + p.tile_begin + n;
-          p.part_max[at] = active ? mt : -INFINITY;
-          p.part_sum[at] = active ? st : 0.0f;
-          if (ENT) p.part_ent[at] = active ? ut : 0.0f;
-          if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
-        }
+        const bool ok = epilogue8<ENT>(
+            p, tmap_out, taddr, staging_all + q * 2 * kStoreBoxBytes,
+            reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN, row, n, lane, store_boxes,
+            [&] { return warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear); },
+            [&] { mbar_arrive(&sm.acc_empty[b]); });
+        if (!ok) break;
       } else if constexpr (MODE == kModeGrad) {
         RowMeta meta{p.ignore_index, 0.0f, 0.0f, 0.0f, 0.0f};
         if (valid) {
@@ -1161,6 +1186,253 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit forward on pairs of blocks (cta_group::2), for more than one row
+// tile.  One tcgen05.mma of 256 x 256 x 32 runs on both SMs of a pair: each
+// block holds its own 128 rows of A and half of the B tile (128 of the 256
+// vocabulary columns), and gets the accumulator of its own 128 rows.  A K block of
+// 128 takes 32 KB of copies a block instead of 48 KB, and the ring has six stages
+// instead of four: e4m3's MMAs take a stage in 512 cycles, and with one block a
+// tile the copies' latency showed (tensor pipe 79% active at 2048 x 38912 x 4096).
+//
+// Both blocks' copies count on the leader's (rank 0's) `full` barrier, which the
+// leader arms for the bytes of both; its MMA thread's commits arrive at both
+// blocks' `empty` and `acc_full`; the epilogue warps of both release an
+// accumulator at the leader's `acc_empty`.  K order and epilogue are those of the
+// one-block kernel, and so are the bits.
+// ---------------------------------------------------------------------------
+
+constexpr int kPairStages = 6;
+constexpr unsigned kPairStageBytes = 2 * kStageABytes;  // 128 rows of A, 128 of B
+constexpr int kPairThreads = 32 * (2 + kEpiWarps);
+static_assert(kPairStages * size_t(kPairStageBytes) <= kStages * size_t(kStageBytes), "the one-block kernel's ring");
+
+struct alignas(8) PairSmem {
+  uint64_t full[kPairStages];
+  uint64_t empty[kPairStages];
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The shared::cluster address of `p` (a shared variable of this block) in the block of rank `rank`.
+__device__ __forceinline__ uint32_t cluster_smem(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// One box into this block's shared memory, completion counted on a barrier of either block of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive once on `bar` in both blocks when every tcgen05 operation this thread issued so far has completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// The MMA thread's wait for an accumulator that both blocks' epilogues release: as thread_wait_watch, acquiring
+// at cluster scope.
+__device__ __forceinline__ bool thread_wait_cluster(uint64_t* bar, unsigned parity, volatile int* abort, unsigned code) {
+  long long start = 0;
+  for (unsigned spin = 0;; ++spin) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    if (ok) return true;
+    if ((spin & 15u) == 15u) {
+      const long long now = global_ns();
+      if (start == 0) {
+        start = now;
+      } else if (*abort) {
+        return false;
+      } else if (now - start > kWaitLimitNs) {
+        atomicOr(&g_watchdog_linear, code);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+template <bool ENT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_partials8_pair_kernel(const __grid_constant__ CUtensorMap tmap_hidden,
+                                 const __grid_constant__ CUtensorMap tmap_weight,
+                                 const __grid_constant__ CUtensorMap tmap_logits, const LinearParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + kPairStages * size_t(kPairStageBytes));
+  volatile int* abort = &sm.abort;
+  const int warp = threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes;
+  const int rank = static_cast<int>(cluster_rank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(&sm.mma_done, 1);
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // both blocks' barriers and tensor memory are there
+  tc_fence_after();
+  const uint32_t tmem_base = sm.tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int64_t total = static_cast<int64_t>(p.num_m) * p.num_n;  // units of 256 rows x 256 columns
+  const int64_t pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- producer: this block's half of the pair's copies ----
+      int64_t it = 0;
+      bool ok = true;
+      for (int64_t u = pair0; u < total && ok; u += pairs) {
+        int m, n;
+        unit_coords(u, p.num_m, p.num_n, p.m_group, m, n);
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const int s = static_cast<int>(it % kPairStages);
+          const unsigned ph = static_cast<unsigned>((it / kPairStages) & 1);
+          if (!thread_wait_watch(&sm.empty[s], ph ^ 1u, abort, kWatchStageFree, &g_watchdog_linear, true)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = cluster_smem(&sm.full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kPairStageBytes);
+          unsigned char* a_dst = base + s * size_t(kPairStageBytes);
+          tma_load_2d_pair(a_dst, &tmap_hidden, kb * kBK8, (2 * m + rank) * kBM, bar);
+          tma_load_2d_pair(a_dst + kStageABytes, &tmap_weight, kb * kBK8, n * kBN + rank * (kBN / 2), bar);
+        }
+      }
+      // The leader waits (bounded, whatever happened) for the pair's copies still in flight; the other block
+      // waits for the leader at the end.
+      if (rank == 0) {
+        for (int64_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i) {
+          if (!thread_wait_watch(&sm.full[i % kPairStages], static_cast<unsigned>((i / kPairStages) & 1), abort,
+                                 kWatchOwnDrain, &g_watchdog_linear, false))
+            break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---- MMA issuer of the pair ----
+      int64_t it = 0;
+      int local = 0;
+      bool ok = true;
+      for (int64_t u = pair0; u < total && ok; u += pairs, ++local) {
+        const int b = local & 1;
+        const unsigned use = static_cast<unsigned>(local >> 1);
+        if (!thread_wait_cluster(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kAccCols);
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
+          const int s = static_cast<int>(it % kPairStages);
+          const unsigned ph = static_cast<unsigned>((it / kPairStages) & 1);
+          if (!thread_wait_watch(&sm.full[s], ph, abort, kWatchMma, &g_watchdog_linear, true)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(base + s * size_t(kPairStageBytes));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // K steps of 32 elements = 32 bytes of a line
+            umma_f8_pair(d_tmem, smem_desc(a_addr + k * 32), smem_desc(a_addr + kStageABytes + k * 32), p.idesc,
+                         (kb | k) != 0 ? 1u : 0u);
+          umma_commit_pair(&sm.empty[s]);
+        }
+        if (!ok) break;
+        umma_commit_pair(&sm.acc_full[b]);
+      }
+      // Every MMA this thread issued completes before the blocks free tensor memory.
+      umma_commit_pair(&sm.mma_done);
+      thread_wait_watch(&sm.mma_done, 0u, abort, kWatchOwnDrain, &g_watchdog_linear, false);
+    }
+  } else {
+    // ---- epilogue: this block's 128 rows ----
+    const int q = warp & 3;
+    unsigned char* staging_all = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(&sm + 1) + 1023) & ~static_cast<uintptr_t>(1023));
+    int local = 0;
+    uint32_t store_boxes = 0;
+    for (int64_t u = pair0; u < total; u += pairs, ++local) {
+      int m, n;
+      unit_coords(u, p.num_m, p.num_n, p.m_group, m, n);
+      const int b = local & 1;
+      const unsigned use = static_cast<unsigned>(local >> 1);
+      const int64_t row = (static_cast<int64_t>(2) * m + rank) * kBM + q * 32 + lane;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kAccCols);
+      const bool ok = epilogue8<ENT>(
+          p, tmap_logits, taddr, staging_all + q * 2 * kStoreBoxBytes,
+          reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN, row, n, lane, store_boxes,
+          [&] { return warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear); },
+          [&] {
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             cluster_smem(&sm.acc_empty[b], 0))
+                         : "memory");
+          });
+      if (!ok) break;
+    }
+    if (lane == 0 && store_boxes != 0) bulk_wait_all();  // the staging boxes stay in use until then
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // neither block leaves while the other may still reach into it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
                  : "memory");
   }
 }
@@ -1300,16 +1572,16 @@ typedef void (*GemmKernel)(CUtensorMap, CUtensorMap, CUtensorMap, LinearParams);
 // mo: the output's tensor map for an epilogue that stores with TMA (the
 // gradient pass's dZ), else any valid map (unused).
 int launch_gemm(GemmKernel kernel, const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mo,
-                const LinearParams& p, cudaStream_t stream, size_t smem_bytes = kSmemBytes) {
+                const LinearParams& p, cudaStream_t stream) {
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
-  if (static_cast<size_t>(smem_optin) < smem_bytes) return BIL_E_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes)) !=
+  if (static_cast<size_t>(smem_optin) < kSmemBytes) return BIL_E_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
       cudaSuccess)
     return BIL_E_CUDA;
   const int64_t total = static_cast<int64_t>(p.num_m) * p.num_n;
   const int grid = static_cast<int>(std::min<int64_t>(total, sms));
-  kernel<<<grid, kThreads, smem_bytes, stream>>>(mh, mw, mo, p);
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(mh, mw, mo, p);
   return cudaGetLastError() == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
@@ -1719,10 +1991,20 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
   }
-  const int a_rows = static_cast<int>(n_rows < kBM ? n_rows : kBM);  // as in bil_linear_logp_partials
+  // Pairs of blocks where their rounds of 256-row units, at 7/8 of the time of a round of 128-row tiles (the
+  // measured ratio: 173 to 190 us for sixteen rounds at K = 4096), come to less: 4096 rows of 151936 columns do (126
+  // rounds either way: 1.54 against 1.61 ms), 333 rows of 32003 do not (4 against 3: 54 against 42 us), nor does
+  // one row tile.  A batch of fewer rows than a tile goes in a box of exactly its rows, as in
+  // bil_linear_logp_partials.
+  int sms = 0, smem_optin = 0;
+  if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  if (static_cast<size_t>(smem_optin) < kSmemBytes8) return BIL_E_UNSUPPORTED;
+  const int64_t tiles = (n_rows + kBM - 1) / kBM * num_tiles, units = (n_rows + 2 * kBM - 1) / (2 * kBM) * num_tiles;
+  const bool pair = n_rows > kBM && 7 * ((units + sms / 2 - 1) / (sms / 2)) < 8 * ((tiles + sms - 1) / sms);
+  const int a_rows = static_cast<int>(n_rows < kBM ? n_rows : kBM);
   CUtensorMap mh, mw;
   if (int st = make_map8(&mh, hidden, n_rows, hidden_size, ld_hidden, a_rows)) return st;
-  if (int st = make_map8(&mw, weight, vocab, hidden_size, ld_weight, kBN)) return st;
+  if (int st = make_map8(&mw, weight, vocab, hidden_size, ld_weight, pair ? kBN / 2 : kBN)) return st;
   CUtensorMap mo = mw;
   if (logits != nullptr) {
     if (int st = make_store_map(&mo, logits, logits_dtype, n_rows, vocab, ld_logits)) return st;
@@ -1733,7 +2015,7 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   p.n_rows = n_rows;
   p.shard_cols = vocab;
   p.num_n = static_cast<int>(num_tiles);
-  p.num_m = static_cast<int>((n_rows + kBM - 1) / kBM);
+  p.num_m = static_cast<int>((pair ? units : tiles) / num_tiles);
   p.k_blocks = static_cast<int>((hidden_size + kBK8 - 1) / kBK8);
   p.targets = target_ids;
   p.ignore_index = ignore_index;
@@ -1747,13 +2029,20 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   p.logits_dtype = logits_dtype;
   p.ld_logits = ld_logits;
   p.idesc = make_idesc(false);  // type code 0: e4m3 for kind::f8f6f4
+  if (pair) p.idesc += static_cast<uint32_t>(kBM >> 4) << 24;  // M = 256
   p.a_box_bytes = static_cast<unsigned>(a_rows) * kBK8;
-  p.m_group = kMGroup;
+  p.m_group = pair ? kMGroup / 2 : kMGroup;
   p.row_scale = hidden_scale;
   p.col_scale = weight_scale;
-  if (int st = launch_gemm(ent ? linear_partials8_kernel<true> : linear_partials8_kernel<false>, mh, mw, mo, p, s,
-                           kSmemBytes8))
-    return st;
+  GemmKernel kernel = pair ? (ent ? linear_partials8_pair_kernel<true> : linear_partials8_pair_kernel<false>)
+                           : (ent ? linear_partials8_kernel<true> : linear_partials8_kernel<false>);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes8)) !=
+      cudaSuccess)
+    return BIL_E_CUDA;
+  const int blocks = pair ? 2 : 1;  // of a unit
+  const int64_t grid = std::min<int64_t>(static_cast<int64_t>(p.num_m) * p.num_n, sms / blocks) * blocks;
+  if (launch_pdl(kernel, grid, pair ? kPairThreads : kThreads, kSmemBytes8, s, blocks, mh, mw, mo, p) != cudaSuccess)
+    return BIL_E_CUDA;
   return bil_logp_merge(p.part_max, p.part_sum, p.part_ent, n_rows, static_cast<int32_t>(num_tiles), num_tiles,
                         p.target_logit, target_ids, ignore_index, vocab, logp, lse, entropy, 0, stream);
 }
