@@ -277,6 +277,52 @@ __device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, 
   }
 }
 
+// The sums of a tile in shared memory for its maximum (the operations of
+// tile_reduce_smem_t, in its order).
+template <int DT, bool ENT, int WOFF>
+__device__ __forceinline__ TilePartial smem_sums_t(const unsigned char* tile, int valid, int lane, float mx_all, float rcp,
+                                                   unsigned sh) {
+  const int groups = (valid + kGroup - 1) / kGroup;
+  const int rem = valid % kGroup;
+  const float m = rcp == 1.0f ? mx_all : __fmul_rn(mx_all, rcp);
+  const float shift = (mx_all == -INFINITY) ? 0.0f : mx_all;
+  const float c = __fmul_rn(rcp, kLog2e);
+  const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
+  uint64_t a[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll 2
+  for (int g = lane; g < groups; g += kLanes) {
+    uint32_t w[Group<DT>::kW];
+    load_group<DT, WOFF>(tile, g, sh, w);
+    if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+    Group<DT>::template sum_acc<ENT, false>(a, u, w, shift2, c2);
+  }
+  TilePartial tp = finish_tile<ENT>(m, a, u);
+  if (ENT && tp.u != tp.u) {  // NaN (warp-uniform): the entropy terms again, with the clamp
+    uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
+    for (int g = lane; g < groups; g += kLanes) {
+      uint32_t w[Group<DT>::kW];
+      load_group<DT, WOFF>(tile, g, sh, w);
+      if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+      Group<DT>::template sum_acc<ENT, true>(a2, u2, w, shift2, c2);
+    }
+    tp.u = finish_tile<ENT>(m, a2, u2).u;
+  }
+  return tp;
+}
+
+template <int DT, bool ENT, bool SHIFTED>
+__device__ __forceinline__ TilePartial smem_sums(const unsigned char* tile, int valid, int lane, float mx_all, float rcp,
+                                                 unsigned off) {
+  const unsigned sh = 8u * (off & 3u);
+  if (!SHIFTED || off == 0) return smem_sums_t<DT, ENT, -1>(tile, valid, lane, mx_all, rcp, 0);
+  switch (off >> 2) {
+    case 0: return smem_sums_t<DT, ENT, 0>(tile, valid, lane, mx_all, rcp, sh);
+    case 1: return smem_sums_t<DT, ENT, 1>(tile, valid, lane, mx_all, rcp, sh);
+    case 2: return smem_sums_t<DT, ENT, 2>(tile, valid, lane, mx_all, rcp, sh);
+    default: return smem_sums_t<DT, ENT, 3>(tile, valid, lane, mx_all, rcp, sh);
+  }
+}
+
 template <int DT, bool ALIGNED, bool ENT>
 __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(const TopkParams p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -350,8 +396,8 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
         tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
       }
     } else {
-      smem_max<DT, !ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks);
-      tp = tile_reduce_smem<DT, ENT, !ALIGNED>(stage, valid, lane, p.rcp, off);
+      const float mx_all = warp_max(smem_max<DT, !ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks));
+      tp = smem_sums<DT, ENT, !ALIGNED>(stage, valid, lane, mx_all, p.rcp, off);
       __syncwarp();
       issue();
     }
@@ -546,17 +592,7 @@ struct RowColumns {
           take &= take - 1;
           const int j = place(bit);
           if (j >= left[q]) continue;
-          uint32_t word = w[q][0];
-#pragma unroll
-          for (int h = 1; h < kW; ++h) word = bit % 16 == h ? w[q][h] : word;
-          float x;
-          if constexpr (EB == 4) {
-            x = __uint_as_float(word);
-          } else {
-            float lo, hi;
-            Elem<DT>::pair(word, lo, hi);
-            x = bit < 16 ? lo : hi;
-          }
+          const float x = Elem<DT>::one(row + (static_cast<int64_t>(first[q]) + j) * EB);  // a line just read
           fn(x, first[q] + j);
         }
       }
