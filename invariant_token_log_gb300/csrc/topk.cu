@@ -194,7 +194,70 @@ struct ChunkMax {
   }
 };
 
-// A tile in registers: its chunk maxima, to `out`, and the lane's part of the tile's.
+// Group g of a tile whose first element lies `off` bytes past the 16-byte
+// aligned `tile`.  Of a 16-bit type: 8-byte words from the boundary at or below
+// the group, one selection and a funnel shift by what is left of the offset (one
+// code for all eight offsets, which differ from row to row).  Of float32: the
+// 16-byte units, a case an offset (8-byte reads 32 bytes apart would take the
+// banks nearly twice as long).  LIMIT (16-bit): only 8-byte words below `limit`
+// bytes are read (global memory).
+template <int DT, bool LIMIT>
+__device__ __forceinline__ void load_group_at(const unsigned char* tile, unsigned off, int g, uint32_t (&w)[Group<DT>::kW],
+                                              int limit) {
+  constexpr int kW = Group<DT>::kW;
+  if constexpr (Elem<DT>::kBytes == 4) {
+    static_assert(!LIMIT, "float32 tiles are read from their stage alone");
+    switch (off >> 2) {
+      case 0: load_group<DT, 0>(tile, g, 0, w); break;
+      case 1: load_group<DT, 1>(tile, g, 0, w); break;
+      case 2: load_group<DT, 2>(tile, g, 0, w); break;
+      default: load_group<DT, 3>(tile, g, 0, w); break;
+    }
+  } else {
+    const int at = static_cast<int>(off & 8u) + g * kGroup * Elem<DT>::kBytes;
+    uint32_t v[kW + 2];
+#pragma unroll
+    for (int q = 0; q < kW / 2 + 1; ++q) {
+      uint2 x = make_uint2(0u, 0u);
+      if (!LIMIT || at + 8 * q < limit) x = *reinterpret_cast<const uint2*>(tile + at + 8 * q);
+      v[2 * q] = x.x;
+      v[2 * q + 1] = x.y;
+    }
+    const bool word = (off & 4u) != 0;
+#pragma unroll
+    for (int j = 0; j < kW + 1; ++j) v[j] = word ? v[j + 1] : v[j];
+#pragma unroll
+    for (int j = 0; j < kW; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], 8u * (off & 3u));
+  }
+}
+
+// As load_group_at with the columns past the tile's `valid` as -inf; ALIGNED: off is 0.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void stage_group(const unsigned char* tile, unsigned off, int g, int valid,
+                                            uint32_t (&w)[Group<DT>::kW]) {
+  if constexpr (ALIGNED)
+    load_group<DT, -1>(tile, g, 0, w);
+  else
+    load_group_at<DT, false>(tile, off, g, w, 0);
+  if (valid - g * kGroup < kGroup) Group<DT>::mask_tail(w, valid - g * kGroup);
+}
+
+// The lane's groups of a tile off 16-byte boundaries, as tile_load_regs gives those of one on them.
+template <int DT, bool LIMIT>
+__device__ __forceinline__ void load_regs_at(const unsigned char* tile, unsigned off, int valid, int lane, TileRegs<DT>& r) {
+  const int limit = (static_cast<int>(off) + valid * Elem<DT>::kBytes + 15) & ~15;
+#pragma unroll
+  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i) {
+    const int g = lane + kLanes * i;
+    if (g * kGroup < valid) {
+      load_group_at<DT, LIMIT>(tile, off, g, r.w[i], limit);
+      if (valid - g * kGroup < kGroup) Group<DT>::mask_tail(r.w[i], valid - g * kGroup);
+    }
+  }
+}
+
+// A tile of a 16-bit type in registers: its chunk maxima, to `out`, and the
+// lane's part of the tile's.
 template <int DT, bool FULL>
 __device__ __forceinline__ float regs_max(const TileRegs<DT>& t, int valid, int lane, unsigned char* out, int chunks) {
   using C = ChunkMax<DT>;
@@ -202,55 +265,74 @@ __device__ __forceinline__ float regs_max(const TileRegs<DT>& t, int valid, int 
   C c;
 #pragma unroll
   for (int a = 0; a < 8; ++a) {
-    if constexpr (C::EB == 4) {
-      c.r[a] = FULL || a < ng ? C::group(t.w[a]) : C::kNone;
-    } else {
-      const uint32_t even = FULL || 2 * a < ng ? C::group(t.w[2 * a]) : C::kNone;
-      const uint32_t odd = FULL || 2 * a + 1 < ng ? C::group(t.w[2 * a + 1]) : C::kNone;
-      c.pair(a, even, odd);
-    }
+    const uint32_t even = FULL || 2 * a < ng ? C::group(t.w[2 * a]) : C::kNone;
+    const uint32_t odd = FULL || 2 * a + 1 < ng ? C::group(t.w[2 * a + 1]) : C::kNone;
+    c.pair(a, even, odd);
   }
   return c.finish(out, 0, chunks, lane);
+}
+
+// A tile's last group where it is a part of one, for the lane that has it (of
+// the lane's groups it is the last too): Group::sum_acc with nothing added for
+// the columns that are not there.  As -inf, which they are in the maximum, they
+// would make the entropy sum 0 * inf, and the tile would be summed again with
+// the clamp (4096 x 32003 bf16: a row's last tile of eight, and 114 us where
+// whole groups take 71).
+template <int DT, bool ENT>
+__device__ __forceinline__ void sum_tail(uint64_t (&a)[4], uint64_t (&u)[4], const uint32_t (&w)[Group<DT>::kW], int valid,
+                                         int lane, uint64_t shift2, uint64_t c2) {
+  const int rem = valid % kGroup;
+  if (rem == 0 || (valid / kGroup) % kLanes != lane) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t t = mul2(sub2(Group<DT>::xpair(w, k), shift2), c2);
+    const float t0 = 2 * k < rem ? lo_of(t) : 0.0f, t1 = 2 * k + 1 < rem ? hi_of(t) : 0.0f;
+    const uint64_t e = pk(2 * k < rem ? ex2_approx(t0) : 0.0f, 2 * k + 1 < rem ? ex2_approx(t1) : 0.0f);
+    a[k] = add2(a[k], e);
+    if (ENT) u[k] = fma2(e, pk(t0, t1), u[k]);
+  }
 }
 
 // The sums for the tile's maximum (the operations of tile_reduce_regs_t, in its order).
 template <int DT, bool FULL, bool ENT>
 __device__ __forceinline__ TilePartial regs_sums(const TileRegs<DT>& r, int valid, int lane, float mx_all, float rcp) {
-  const int ng = FULL ? TileRegs<DT>::kMaxGroups : lane_groups(valid, lane);
   const float m = rcp == 1.0f ? mx_all : __fmul_rn(mx_all, rcp);
   const float shift = (mx_all == -INFINITY) ? 0.0f : mx_all;
   const float c = __fmul_rn(rcp, kLog2e);
   const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
   uint64_t a[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+  uint32_t tail[Group<DT>::kW];
 #pragma unroll
-  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i)
-    if (FULL || i < ng) Group<DT>::template sum_acc<ENT, false>(a, u, r.w[i], shift2, c2);
+  for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i) {
+    const int left = valid - (lane + kLanes * i) * kGroup;
+    if (FULL || left >= kGroup) {
+      Group<DT>::template sum_acc<ENT, false>(a, u, r.w[i], shift2, c2);
+    } else if (left > 0) {
+#pragma unroll
+      for (int j = 0; j < Group<DT>::kW; ++j) tail[j] = r.w[i][j];
+    }
+  }
+  if (!FULL) sum_tail<DT, ENT>(a, u, tail, valid, lane, shift2, c2);
   return finish_tile<ENT>(m, a, u);
 }
 
 // The same of a tile in shared memory (tiles past what registers hold).
-// groups of the columns of a tile's chunks
-__device__ __forceinline__ int tile_groups(int chunks) { return chunks * (kChunk / kGroup); }
-
-template <int DT, int WOFF>
-__device__ __forceinline__ float smem_max_t(const unsigned char* tile, int valid, int lane, unsigned sh,
-                                            unsigned char* out, int chunks) {
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, int lane, unsigned off,
+                                          unsigned char* out, int chunks) {
   using C = ChunkMax<DT>;
-  const int groups = (valid + kGroup - 1) / kGroup;
-  const int rem = valid % kGroup;
   float m = -INFINITY;
 #pragma unroll 1
-  for (int g0 = 0; g0 < tile_groups(chunks); g0 += C::kGroups * kLanes) {
+  for (int g0 = 0; g0 < chunks * (kChunk / kGroup); g0 += C::kGroups * kLanes) {
     C c;
     uint32_t last = 0;
 #pragma unroll
     for (int i = 0; i < C::kGroups; ++i) {
       const int g = g0 + i * kLanes + lane;
       uint32_t now = C::kNone;
-      if (g < groups) {
+      if (g * kGroup < valid) {
         uint32_t w[Group<DT>::kW];
-        load_group<DT, WOFF>(tile, g, sh, w);
-        if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+        stage_group<DT, ALIGNED>(tile, off, g, valid, w);
         now = C::group(w);
       }
       if constexpr (C::EB == 4)
@@ -259,68 +341,45 @@ __device__ __forceinline__ float smem_max_t(const unsigned char* tile, int valid
         c.pair(i / 2, last, now);
       last = now;
     }
-    m = fmaxf(m, c.finish(out, g0 / 8, chunks, lane));
+    m = fmaxf(m, c.finish(out, g0 / (kChunk / kGroup), chunks, lane));
   }
   return m;
 }
 
-template <int DT, bool SHIFTED>
-__device__ __forceinline__ float smem_max(const unsigned char* tile, int valid, int lane, unsigned off,
-                                          unsigned char* out, int chunks) {
-  const unsigned sh = 8u * (off & 3u);
-  if (!SHIFTED || off == 0) return smem_max_t<DT, -1>(tile, valid, lane, 0, out, chunks);
-  switch (off >> 2) {
-    case 0: return smem_max_t<DT, 0>(tile, valid, lane, sh, out, chunks);
-    case 1: return smem_max_t<DT, 1>(tile, valid, lane, sh, out, chunks);
-    case 2: return smem_max_t<DT, 2>(tile, valid, lane, sh, out, chunks);
-    default: return smem_max_t<DT, 3>(tile, valid, lane, sh, out, chunks);
-  }
-}
-
 // The sums of a tile in shared memory for its maximum (the operations of
 // tile_reduce_smem_t, in its order).
-template <int DT, bool ENT, int WOFF>
-__device__ __forceinline__ TilePartial smem_sums_t(const unsigned char* tile, int valid, int lane, float mx_all, float rcp,
-                                                   unsigned sh) {
+template <int DT, bool ENT, bool ALIGNED>
+__device__ __forceinline__ TilePartial smem_sums(const unsigned char* tile, int valid, int lane, float mx_all, float rcp,
+                                                 unsigned off) {
   const int groups = (valid + kGroup - 1) / kGroup;
-  const int rem = valid % kGroup;
   const float m = rcp == 1.0f ? mx_all : __fmul_rn(mx_all, rcp);
   const float shift = (mx_all == -INFINITY) ? 0.0f : mx_all;
   const float c = __fmul_rn(rcp, kLog2e);
   const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
   uint64_t a[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
-#pragma unroll 2
-  for (int g = lane; g < groups; g += kLanes) {
+#pragma unroll 4
+  for (int g = lane; g < valid / kGroup; g += kLanes) {
     uint32_t w[Group<DT>::kW];
-    load_group<DT, WOFF>(tile, g, sh, w);
-    if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+    stage_group<DT, ALIGNED>(tile, off, g, valid, w);
     Group<DT>::template sum_acc<ENT, false>(a, u, w, shift2, c2);
+  }
+  if (groups != valid / kGroup) {
+    uint32_t w[Group<DT>::kW];
+    stage_group<DT, ALIGNED>(tile, off, groups - 1, valid, w);
+    sum_tail<DT, ENT>(a, u, w, valid, lane, shift2, c2);
   }
   TilePartial tp = finish_tile<ENT>(m, a, u);
   if (ENT && tp.u != tp.u) {  // NaN (warp-uniform): the entropy terms again, with the clamp
     uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
+#pragma unroll 1
     for (int g = lane; g < groups; g += kLanes) {
       uint32_t w[Group<DT>::kW];
-      load_group<DT, WOFF>(tile, g, sh, w);
-      if (rem != 0 && g == groups - 1) Group<DT>::mask_tail(w, rem);
+      stage_group<DT, ALIGNED>(tile, off, g, valid, w);
       Group<DT>::template sum_acc<ENT, true>(a2, u2, w, shift2, c2);
     }
     tp.u = finish_tile<ENT>(m, a2, u2).u;
   }
   return tp;
-}
-
-template <int DT, bool ENT, bool SHIFTED>
-__device__ __forceinline__ TilePartial smem_sums(const unsigned char* tile, int valid, int lane, float mx_all, float rcp,
-                                                 unsigned off) {
-  const unsigned sh = 8u * (off & 3u);
-  if (!SHIFTED || off == 0) return smem_sums_t<DT, ENT, -1>(tile, valid, lane, mx_all, rcp, 0);
-  switch (off >> 2) {
-    case 0: return smem_sums_t<DT, ENT, 0>(tile, valid, lane, mx_all, rcp, sh);
-    case 1: return smem_sums_t<DT, ENT, 1>(tile, valid, lane, mx_all, rcp, sh);
-    case 2: return smem_sums_t<DT, ENT, 2>(tile, valid, lane, mx_all, rcp, sh);
-    default: return smem_sums_t<DT, ENT, 3>(tile, valid, lane, mx_all, rcp, sh);
-  }
 }
 
 template <int DT, bool ALIGNED, bool ENT>
@@ -377,27 +436,37 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
     const int64_t o = now.row * p.num_tiles + now.tile;
     TilePartial tp;
     unsigned char* chunks = p.chunk_max + now.row * p.chunk_pitch + static_cast<int64_t>(now.tile) * p.tile_chunks * EB;
-    if (p.tile_v <= TileRegs<DT>::kMaxTile) {
-      const bool whole = valid == TileRegs<DT>::kMaxTile;
-      TileRegs<DT> regs;
-      tile_load_regs<DT, !ALIGNED>(stage, valid, lane, regs, off);
-      __syncwarp();  // the stage has been read
-      issue();
-      const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, chunks, p.tile_chunks)
-                                          : regs_max<DT, false>(regs, valid, lane, chunks, p.tile_chunks));
-      tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
-                 : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
-      if (ENT && tp.u != tp.u) {  // as in the streaming forward: u from a clamped pass
-        if (ALIGNED) {
-          tile_load_regs<DT>(src, valid, lane, regs);
-        } else {
-          tile_load_regs<DT, true, true>(src - off, valid, lane, regs, off);
+    bool done = false;
+    // A 16-bit type's tile of up to 4096 columns in registers; any other in its stage, twice.  (Float32 has no
+    // register form: half of its default tile would fit, and the code of both slowed either.)
+    if constexpr (EB == 2) {
+      if (p.tile_v <= TileRegs<DT>::kMaxTile) {
+        const bool whole = valid == TileRegs<DT>::kMaxTile;
+        TileRegs<DT> regs;
+        if (ALIGNED)
+          tile_load_regs<DT>(stage, valid, lane, regs);
+        else
+          load_regs_at<DT, false>(stage, off, valid, lane, regs);
+        __syncwarp();  // the stage has been read
+        issue();
+        const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, chunks, p.tile_chunks)
+                                            : regs_max<DT, false>(regs, valid, lane, chunks, p.tile_chunks));
+        tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
+                   : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
+        if (ENT && tp.u != tp.u) {  // as in the streaming forward: u from a clamped pass
+          if (ALIGNED) {
+            tile_load_regs<DT>(src, valid, lane, regs);
+          } else {
+            load_regs_at<DT, true>(src - off, off, valid, lane, regs);
+          }
+          tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
         }
-        tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
+        done = true;
       }
-    } else {
-      const float mx_all = warp_max(smem_max<DT, !ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks));
-      tp = smem_sums<DT, ENT, !ALIGNED>(stage, valid, lane, mx_all, p.rcp, off);
+    }
+    if (!done) {
+      const float mx_all = warp_max(smem_max<DT, ALIGNED>(stage, valid, lane, off, chunks, p.tile_chunks));
+      tp = smem_sums<DT, ENT, ALIGNED>(stage, valid, lane, mx_all, p.rcp, off);
       __syncwarp();
       issue();
     }
