@@ -202,6 +202,39 @@ __device__ __forceinline__ bool thread_wait_watch(uint64_t* bar, unsigned parity
   }
 }
 
+// One thread's wait for arrivals from the other blocks of its cluster too: as
+// thread_wait_watch with check_abort, acquiring at cluster scope.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool thread_wait_cluster_watch(uint64_t* bar, unsigned parity, volatile int* abort,
+                                                          unsigned code, unsigned int* watch) {
+  long long start = 0;
+  for (unsigned spin = 0;; ++spin) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((spin & 15u) == 15u) {
+      const long long now = global_ns();
+      if (start == 0) {
+        start = now;
+      } else if (*abort) {
+        return false;
+      } else if (now - start > kWaitLimitNs) {
+        atomicOr(watch, code);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }

@@ -1260,35 +1260,6 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// The MMA thread's wait for an accumulator that both blocks' epilogues release: as thread_wait_watch, acquiring
-// at cluster scope.
-__device__ __forceinline__ bool thread_wait_cluster(uint64_t* bar, unsigned parity, volatile int* abort, unsigned code) {
-  long long start = 0;
-  for (unsigned spin = 0;; ++spin) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
-        : "memory");
-    if (ok) return true;
-    if ((spin & 15u) == 15u) {
-      const long long now = global_ns();
-      if (start == 0) {
-        start = now;
-      } else if (*abort) {
-        return false;
-      } else if (now - start > kWaitLimitNs) {
-        atomicOr(&g_watchdog_linear, code);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
 template <bool ENT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_partials8_pair_kernel(const __grid_constant__ CUtensorMap tmap_hidden,
@@ -1374,7 +1345,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int64_t u = pair0; u < total && ok; u += pairs, ++local) {
         const int b = local & 1;
         const unsigned use = static_cast<unsigned>(local >> 1);
-        if (!thread_wait_cluster(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma)) break;
+        if (!thread_wait_cluster_watch(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma, &g_watchdog_linear)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kAccCols);
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
@@ -1971,6 +1942,8 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   }
   if (!bil_internal::extent_ok(n_rows, ld_hidden, 1) || !bil_internal::extent_ok(vocab, ld_weight, 1))
     return BIL_E_UNSUPPORTED;
+  if (n_rows > INT32_MAX - kBM || vocab > INT32_MAX - kBN || hidden_size > INT32_MAX - kBK8)
+    return BIL_E_UNSUPPORTED;
   float rcp = 1.0f;
   if (int st = bil_internal::temperature_rcp(temperature, &rcp)) return st;
   if (n_rows == 0) return BIL_OK;
@@ -1985,8 +1958,6 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
       !aligned_to(logp, 4) || (lse && !aligned_to(lse, 4)) || (entropy && !aligned_to(entropy, 4)))
     return BIL_E_ALIGN;
   if (logits != nullptr && !rows16(logits, ld_logits, el)) return BIL_E_ALIGN;
-  if (n_rows > INT32_MAX - kBM || vocab > INT32_MAX - kBN || hidden_size > INT32_MAX - kBK8)
-    return BIL_E_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
