@@ -122,10 +122,21 @@ constexpr uint32_t kStoreBoxBytes = kStoreBox * kStoreBox * 2;           // 2 KB
 constexpr size_t kStagingBytes = BIL_EPILOGUE_TMA_STORE ? 4 * 2 * kStoreBoxBytes : 0;  // 4 warps x 2 buffers
 constexpr size_t kSmemBytes = 1024 /* alignment slack */ + kStages * size_t(kStageBytes) + sizeof(LinearSmem) +
                               (BIL_EPILOGUE_TMA_STORE ? 1024 + kStagingBytes : 0);
-// The 8-bit forward keeps, past the staging boxes, each epilogue warp's copy of its tile's column scales.
-constexpr size_t kStagingBytes8 = kEpiWarps * 2 * kStoreBoxBytes;
-constexpr size_t kSmemBytes8 = 1024 + kStages * size_t(kStageBytes) + sizeof(LinearSmem) + 1024 + kStagingBytes8 +
-                               kEpiWarps * kBN * sizeof(float);
+// The 8-bit forward: eight epilogue warps, two to a quarter of the rows, each
+// half of the tile's columns.  Where the logits are stored, the last stage of the
+// ring is the warps' staging boxes instead.  Past the barriers lie each warp's
+// copy of its columns' scales and what the two warps of a quarter tell each other.
+constexpr int kEpiWarps8 = 8;
+constexpr int kHalfCols = kBN / 2;
+constexpr int kThreads8 = 32 * (2 + kEpiWarps8);
+struct Exchange8 {
+  float scale[kEpiWarps8][kHalfCols];
+  float max[kEpiWarps8][kLanes];
+  float sum[4][kLanes], ent[4][kLanes];  // the upper half's, by quarter
+  int ok[kEpiWarps8];
+};
+static_assert(kEpiWarps8 * 2 * kStoreBoxBytes <= 2 * kStageABytes, "the staging boxes fit the last stage of either ring");
+constexpr size_t kSmemBytes8 = 1024 + kStages * size_t(kStageBytes) + 1024 + sizeof(Exchange8);
 
 // What the epilogue warps do with a finished accumulator tile.
 enum EpilogueMode {
@@ -511,53 +522,72 @@ __device__ __forceinline__ void row_partial(uint32_t taddr, int vcols, float rcp
 // scale out of the maximum and into the exponent's constant:
 //   mx = max over valid c of v_c (exact);  m = (mx *rn sh) *rn rcp
 //   t_c = fma(v_c, c, -(mx *rn c)),  c = (sh *rn rcp) *rn log2e
-// with e_c = 2^t_c, the eight slots, the tree and the entropy sum of row_partial
-// (no clamp: an accumulator is never infinite); the target logit is (v_t *rn sh)
-// *rn rcp.  `sw` is the warp's copy of the tile's column scales in shared memory
-// (every lane reads the same word: a broadcast).  With `box_map` the logits z_c
-// go out through the warp's staging boxes.
+// with e_c = 2^t_c, summed over each half of 128 columns in eight slots and by the
+// tree of row_partial, the two halves' sums added; the entropy sum alike (no
+// clamp: an accumulator is never infinite); the target logit is (v_t *rn sh) *rn
+// rcp.  A thread has one half; `sw` is its warp's copy of the half's column
+// scales in shared memory (every lane reads the same word: a broadcast).
 //
-// A tile's MMAs take 16384 cycles at K = 4096, half of the 16-bit kernel's, and
-// this, one warp per scheduler, has to keep below that: packed float32 pairs, the
-// column tests only in a tile that is cut off (FULL: none is), the target looked
-// for only in a chunk of 32 columns that holds one of the warp's, each chunk
-// loaded from tensor memory while the one before it is worked on.  (Before, at
-// 2048 x 38912 x 4096: 5.6 k instructions a warp and tile, tensor pipe 78%
-// active, the epilogue the bound.)
-template <bool ENT, bool FULL>
-__device__ __forceinline__ void row_partial8(uint32_t taddr, int vcols, float rcp, float sh, const float* sw,
-                                             int64_t tloc, int out_dtype, float& m_out, float& s_out, float& u_out,
-                                             float& tl_out, const CUtensorMap* box_map, unsigned char* staging,
-                                             int box_x, int box_y, int lane, uint32_t* issued) {
+// At K = 4096 a tile's MMAs take 16384 cycles, half of the 16-bit kernel's, and
+// at a small K the epilogue is what bounds the kernel.  So: packed float32 pairs,
+// the column tests only in a tile that is cut off (FULL: none is), the target
+// looked for only in a chunk of 32 columns that holds one of the warp's, each chunk
+// loaded from tensor memory while the one before it is worked on, and two warps a
+// scheduler.  Against four warps with whole rows: 4096 x 152064 x 1024 589 us for
+// 784, x 2048 758 for 822, 2048 x 38912 x 512 92 for 114, 333 x 32003 x 1104 38 for
+// 42; at 2048 x 38912 x 4096 198 for 195.
+template <bool FULL>
+struct HalfRow {
   uint32_t ra[kChunk], rb[kChunk];
-  float mx = -INFINITY;
-  float tl = 0.0f;
-  const int target_chunk = tloc >= 0 && tloc < kBN ? static_cast<int>(tloc) / kChunk : -1;
-  const uint64_t sh2 = pk(sh, sh);
-  auto pair = [](const uint32_t (&r)[kChunk], int k) {
+  uint32_t taddr;   // the half's first column
+  int vcols;        // valid columns of the half, may be <= 0
+  const float* sw;
+
+  __device__ static __forceinline__ uint64_t pair(const uint32_t (&r)[kChunk], int k) {
     return static_cast<uint64_t>(r[k]) | (static_cast<uint64_t>(r[k + 1]) << 32);
-  };
-  auto first_pass = [&](uint32_t (&r)[kChunk], int c0) {
-    uint64_t v[kChunk / 2];
-#pragma unroll
-    for (int k = 0; k < kChunk; k += 4) {
-      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
-      v[k / 2] = mul2(pair(r, k), w.x);
-      v[k / 2 + 1] = mul2(pair(r, k + 2), w.y);
+  }
+  // fn(registers, first column) for the half's four chunks, each loaded a chunk ahead
+  template <typename F>
+  __device__ __forceinline__ void chunks(F fn) {
+    tmem_ld32_issue(taddr, ra);
+#pragma unroll 1
+    for (int c0 = 0; c0 < kHalfCols; c0 += 2 * kChunk) {
+      tmem_ld_wait(ra);
+      tmem_ld32_issue(taddr + c0 + kChunk, rb);
+      fn(ra, c0);
+      tmem_ld_wait(rb);
+      if (c0 + 2 * kChunk < kHalfCols) tmem_ld32_issue(taddr + c0 + 2 * kChunk, ra);
+      fn(rb, c0 + kChunk);
     }
+  }
+  // the half's maximum; the target's v where the half has it (tcol: its column here); with box_map the logits
+  // z_c through the warp's staging boxes
+  __device__ __forceinline__ float maximum(int tcol, float& tl, float sh, const CUtensorMap* box_map, int out_dtype,
+                                           unsigned char* staging, int box_x, int box_y, int lane, uint32_t* issued) {
+    float mx = -INFINITY;
+    const int target_chunk = tcol >= 0 && tcol < kHalfCols ? tcol / kChunk : -1;
+    const uint64_t sh2 = pk(sh, sh);
+    chunks([&](uint32_t (&r)[kChunk], int c0) {
+      uint64_t v[kChunk / 2];
 #pragma unroll
-    for (int k = 0; k < kChunk; k += 2) {
-      if (FULL || c0 + k < vcols) mx = fmaxf(mx, lo_of(v[k / 2]));
-      if (FULL || c0 + k + 1 < vcols) mx = fmaxf(mx, hi_of(v[k / 2]));
-    }
-    if (__any_sync(0xffffffffu, target_chunk == c0 / kChunk)) {
+      for (int k = 0; k < kChunk; k += 4) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
+        v[k / 2] = mul2(pair(r, k), w.x);
+        v[k / 2 + 1] = mul2(pair(r, k + 2), w.y);
+      }
 #pragma unroll
       for (int k = 0; k < kChunk; k += 2) {
-        if (c0 + k == tloc) tl = lo_of(v[k / 2]);
-        if (c0 + k + 1 == tloc) tl = hi_of(v[k / 2]);
+        if (FULL || c0 + k < vcols) mx = fmaxf(mx, lo_of(v[k / 2]));
+        if (FULL || c0 + k + 1 < vcols) mx = fmaxf(mx, hi_of(v[k / 2]));
       }
-    }
-    if (box_map != nullptr && (FULL || c0 < vcols)) {
+      if (__any_sync(0xffffffffu, target_chunk == c0 / kChunk)) {
+#pragma unroll
+        for (int k = 0; k < kChunk; k += 2) {
+          if (c0 + k == tcol) tl = lo_of(v[k / 2]);
+          if (c0 + k + 1 == tcol) tl = hi_of(v[k / 2]);
+        }
+      }
+      if (box_map == nullptr || !(FULL || c0 < vcols)) return;
 #pragma unroll
       for (int k = 0; k < kChunk / 2; ++k) v[k] = mul2(v[k], sh2);
       if (out_dtype == BIL_F32) {  // two boxes of 16 columns
@@ -580,62 +610,40 @@ __device__ __forceinline__ void row_partial8(uint32_t taddr, int vcols, float rc
         }
         store_box(staging, box_map, box_x + c0, box_y, lane, *issued, pk16);
       }
-    }
-  };
-  uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
-  uint64_t c2 = 0, shift2 = 0;
-  auto second_pass = [&](uint32_t (&r)[kChunk], int c0) {
+    });
+    return mx;
+  }
+  // the half's sums for t = fma(v, c, -shift)
+  template <bool ENT>
+  __device__ __forceinline__ void sums(float c, float shift, float& sum, float& ent) {
+    uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
+    const uint64_t c2 = pk(c, c), shift2 = pk(-shift, -shift);
+    chunks([&](uint32_t (&r)[kChunk], int c0) {
 #pragma unroll
-    for (int k = 0; k < kChunk; k += 4) {
-      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
+      for (int k = 0; k < kChunk; k += 4) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint64_t t = fma2(mul2(pair(r, k + 2 * h), h == 0 ? w.x : w.y), c2, shift2);
-        float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
-        if (!FULL) {  // columns past the vocabulary add nothing
-          if (c0 + k + 2 * h >= vcols) e0 = 0.0f;
-          if (c0 + k + 2 * h + 1 >= vcols) e1 = 0.0f;
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t t = fma2(mul2(pair(r, k + 2 * h), h == 0 ? w.x : w.y), c2, shift2);
+          float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
+          if (!FULL) {  // columns past the vocabulary add nothing
+            if (c0 + k + 2 * h >= vcols) e0 = 0.0f;
+            if (c0 + k + 2 * h + 1 >= vcols) e1 = 0.0f;
+          }
+          const uint64_t e = pk(e0, e1);
+          const int slot = (k / 2 + h) % 4;
+          a2[slot] = add2(a2[slot], e);
+          if (ENT) u2[slot] = fma2(e, t, u2[slot]);
         }
-        const uint64_t e = pk(e0, e1);
-        const int slot = (k / 2 + h) % 4;
-        a2[slot] = add2(a2[slot], e);
-        if (ENT) u2[slot] = fma2(e, t, u2[slot]);
       }
-    }
-  };
-  tmem_ld32_issue(taddr, ra);
-#pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 2 * kChunk) {
-    tmem_ld_wait(ra);
-    tmem_ld32_issue(taddr + c0 + kChunk, rb);
-    first_pass(ra, c0);
-    tmem_ld_wait(rb);
-    tmem_ld32_issue(taddr + (c0 + 2 * kChunk) % kBN, ra);  // the last one: the second pass's first
-    first_pass(rb, c0 + kChunk);
-  }
-  const float shift = (mx == -INFINITY) ? 0.0f : mx;
-  const float c = __fmul_rn(__fmul_rn(sh, rcp), kLog2e);
-  c2 = pk(c, c);
-  shift2 = pk(-__fmul_rn(shift, c), -__fmul_rn(shift, c));
-#pragma unroll 1
-  for (int c0 = 0; c0 < kBN; c0 += 2 * kChunk) {
-    tmem_ld_wait(ra);
-    tmem_ld32_issue(taddr + c0 + kChunk, rb);
-    second_pass(ra, c0);
-    tmem_ld_wait(rb);
-    if (c0 + 2 * kChunk < kBN) tmem_ld32_issue(taddr + c0 + 2 * kChunk, ra);
-    second_pass(rb, c0 + kChunk);
-  }
-  m_out = __fmul_rn(__fmul_rn(mx, sh), rcp);
-  s_out = __fadd_rn(__fadd_rn(__fadd_rn(lo_of(a2[0]), hi_of(a2[0])), __fadd_rn(lo_of(a2[1]), hi_of(a2[1]))),
+    });
+    sum = __fadd_rn(__fadd_rn(__fadd_rn(lo_of(a2[0]), hi_of(a2[0])), __fadd_rn(lo_of(a2[1]), hi_of(a2[1]))),
                     __fadd_rn(__fadd_rn(lo_of(a2[2]), hi_of(a2[2])), __fadd_rn(lo_of(a2[3]), hi_of(a2[3]))));
-  if (ENT)
-    u_out = __fmul_rn(
-        __fadd_rn(__fadd_rn(__fadd_rn(lo_of(u2[0]), hi_of(u2[0])), __fadd_rn(lo_of(u2[1]), hi_of(u2[1]))),
-                  __fadd_rn(__fadd_rn(lo_of(u2[2]), hi_of(u2[2])), __fadd_rn(lo_of(u2[3]), hi_of(u2[3])))),
-        kLn2);
-  tl_out = __fmul_rn(__fmul_rn(tl, sh), rcp);
-}
+    if (ENT)
+      ent = __fadd_rn(__fadd_rn(__fadd_rn(lo_of(u2[0]), hi_of(u2[0])), __fadd_rn(lo_of(u2[1]), hi_of(u2[1]))),
+                      __fadd_rn(__fadd_rn(lo_of(u2[2]), hi_of(u2[2])), __fadd_rn(lo_of(u2[3]), hi_of(u2[3]))));
+  }
+};
 
 // float -> 16-bit storage, round to nearest even.
 template <int DT>
@@ -746,49 +754,96 @@ __device__ __forceinline__ void row_store(uint32_t taddr, int vcols, bool valid,
   }
 }
 
-// The 8-bit forward's epilogue of column tile n for one warp: row `row` (of the
-// lane; the warp's are 32 consecutive ones) of the accumulator at `taddr`.
-// `wait` waits for the accumulator, `release` (one lane) hands it back.  False: the
-// wait ran out.
+// The epilogue number of a warp (2 to 9): a warp reads the quarter of the tensor
+// memory's lanes that its number modulo 4 names.
+__device__ __forceinline__ int epi8(int warp) { return warp % 4 + 4 * ((warp - 2) / 4); }
+
+// The two warps of a quarter wait for each other.
+__device__ __forceinline__ void quarter_sync(int q) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + q), "n"(2 * kLanes) : "memory");
+}
+
+// The 8-bit forward's epilogue of column tile n for warp e (of eight: quarter e
+// % 4 of the tile's rows, half e / 4 of its columns): row `row` (of the lane) of
+// the accumulator at `taddr` (the tile's first column).  `wait` waits for the
+// accumulator, `release` (one lane) hands it back.  False: a wait ran out, of
+// this warp or of the quarter's other (which says so at the first barrier, so
+// that neither is left waiting at one).
 template <bool ENT, typename Wait, typename Release>
 __device__ __forceinline__ bool epilogue8(const LinearParams& p, const CUtensorMap& tmap_out, uint32_t taddr,
-                                          unsigned char* staging, float* sw, int64_t row, int n, int lane,
+                                          unsigned char* staging, Exchange8& x, int e, int64_t row, int n, int lane,
                                           uint32_t& store_boxes, Wait wait, Release release) {
+  const int q = e % 4, half = e / 4;
+  if (row - lane >= p.n_rows) {  // no row of the quarter exists (the other warp finds the same)
+    if (!wait()) return false;
+    if (lane == 0) release();
+    return true;
+  }
   const bool valid = row < p.n_rows;
-  const int64_t col0 = static_cast<int64_t>(n) * kBN;
-  const int vcols = static_cast<int>(p.shard_cols - col0 < kBN ? p.shard_cols - col0 : kBN);
+  const int64_t col0 = static_cast<int64_t>(n) * kBN + half * kHalfCols;
+  const int vcols = static_cast<int>(p.shard_cols - col0 < kHalfCols ? p.shard_cols - col0 : kHalfCols);
   const int64_t t = valid ? p.targets[row] : p.ignore_index;
   const bool active = valid && t != p.ignore_index;
-  const int64_t tloc = active ? t - col0 : -1;
+  const int64_t tcol = active ? t - col0 : -1;
+  const int tloc = tcol >= 0 && tcol < vcols ? static_cast<int>(tcol) : -1;
   const float sh = valid ? p.row_scale[row] : 0.0f;
-  // the tile's column scales, while its MMAs run (the warp's reads of the last tile's are done)
+  // the half's column scales, while the tile's MMAs run (the warp's reads of the last tile's are done)
+  float* sw = x.scale[e];
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < kBN / kLanes; ++j) {
+  for (int j = 0; j < kHalfCols / kLanes; ++j) {
     const int c = j * kLanes + lane;
     sw[c] = c < vcols ? p.col_scale[col0 + c] : 0.0f;
   }
   __syncwarp();
-  if (!wait()) return false;
-  tc_fence_after();
-  float mt, st, ut = 0.0f, tl;
+  const bool ok = wait();
+  const uint32_t at = taddr + static_cast<uint32_t>(half * kHalfCols);
   const CUtensorMap* boxes = p.logits != nullptr ? &tmap_out : nullptr;
-  const int box_y = static_cast<int>(row - lane);
-  if (vcols == kBN)
-    row_partial8<ENT, true>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes, staging,
-                            static_cast<int>(col0), box_y, lane, &store_boxes);
-  else
-    row_partial8<ENT, false>(taddr, vcols, p.rcp, sh, sw, tloc, p.logits_dtype, mt, st, ut, tl, boxes, staging,
-                             static_cast<int>(col0), box_y, lane, &store_boxes);
+  const int box_x = static_cast<int>(col0), box_y = static_cast<int>(row - lane);
+  float mx = -INFINITY, tl = 0.0f;
+  if (ok) {
+    tc_fence_after();
+    if (vcols == kHalfCols) {
+      HalfRow<true> h;
+      h.taddr = at, h.vcols = vcols, h.sw = sw;
+      mx = h.maximum(tloc, tl, sh, boxes, p.logits_dtype, staging, box_x, box_y, lane, &store_boxes);
+    } else {
+      HalfRow<false> h;
+      h.taddr = at, h.vcols = vcols, h.sw = sw;
+      mx = h.maximum(tloc, tl, sh, boxes, p.logits_dtype, staging, box_x, box_y, lane, &store_boxes);
+    }
+  }
+  x.max[e][lane] = mx;
+  if (lane == 0) x.ok[e] = ok ? 1 : 0;
+  quarter_sync(q);
+  if (x.ok[q] == 0 || x.ok[q + 4] == 0) return false;
+  mx = fmaxf(mx, x.max[e ^ 4][lane]);
+  const float c = __fmul_rn(__fmul_rn(sh, p.rcp), kLog2e);
+  const float shift = __fmul_rn(mx == -INFINITY ? 0.0f : mx, c);
+  float sum, ent = 0.0f;
+  if (vcols == kHalfCols) {
+    HalfRow<true> h;
+    h.taddr = at, h.vcols = vcols, h.sw = sw;
+    h.template sums<ENT>(c, shift, sum, ent);
+  } else {
+    HalfRow<false> h;
+    h.taddr = at, h.vcols = vcols, h.sw = sw;
+    h.template sums<ENT>(c, shift, sum, ent);
+  }
   tc_fence_before();
   __syncwarp();
   if (lane == 0) release();
-  if (valid) {
-    const int64_t at = row * p.ld_part + n;
-    p.part_max[at] = active ? mt : -INFINITY;
-    p.part_sum[at] = active ? st : 0.0f;
-    if (ENT) p.part_ent[at] = active ? ut : 0.0f;
-    if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
+  if (half == 1) {
+    x.sum[q][lane] = sum;
+    if (ENT) x.ent[q][lane] = ent;
+  }
+  quarter_sync(q);
+  if (tloc >= 0) p.target_logit[row] = __fmul_rn(__fmul_rn(tl, sh), p.rcp);  // the half that has it
+  if (half == 0 && valid) {
+    const int64_t o = row * p.ld_part + n;
+    p.part_max[o] = active ? __fmul_rn(__fmul_rn(mx, sh), p.rcp) : -INFINITY;
+    p.part_sum[o] = active ? __fadd_rn(sum, x.sum[q][lane]) : 0.0f;
+    if (ENT) p.part_ent[o] = active ? __fmul_rn(__fadd_rn(ent, x.ent[q][lane]), kLn2) : 0.0f;
   }
   return true;
 }
@@ -921,12 +976,13 @@ template <int MODE, bool ENT, int DT, int HALVES = 1>
 __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const CUtensorMap& tmap_weight,
                                           const CUtensorMap& tmap_out, const LinearParams& p) {
   static_assert(HALVES == 1 || (HALVES == 2 && MODE == kModeStore), "two-half units are for the store epilogue");
+  constexpr bool kOp8 = MODE == kModePartials8;
   constexpr unsigned kStageBytesH = HALVES * kStageABytes + kStageBBytes;
-  constexpr int kStagesH = static_cast<int>(kStages * size_t(kStageBytes) / kStageBytesH);  // 4, or 3 of 64 KB
+  // 4, or 3 of 64 KB; the 8-bit forward with the logits (DT = 1): 3, the fourth is the epilogue's
+  constexpr int kStagesH = static_cast<int>(kStages * size_t(kStageBytes) / kStageBytesH) - (kOp8 && DT == 1 ? 1 : 0);
   static_assert(kStagesH >= 3 && kStagesH <= kStages, "the stage ring fits the shared memory of the 1-half layout");
   constexpr int kAccBufs = HALVES == 1 ? 2 : 1;
   constexpr int kRowsPerUnit = HALVES * kBM;
-  constexpr bool kOp8 = MODE == kModePartials8;
   constexpr int kStageK = kOp8 ? kBK8 : kBK;  // K elements per stage: one 128-byte line either way
   extern __shared__ unsigned char smem_raw[];
   // Stage buffers start on a 1024-byte boundary (the 128-byte swizzle pattern
@@ -945,7 +1001,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_empty[b], kEpiWarps);
+      mbar_init(&sm.acc_empty[b], kOp8 ? kEpiWarps8 : kEpiWarps);
     }
     mbar_init(&sm.mma_done, 1);
     sm.abort = 0;
@@ -1069,7 +1125,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
       umma_commit(&sm.mma_done);
       thread_wait_watch(&sm.mma_done, 0u, abort, kWatchOwnDrain, &g_watchdog_linear, false);
     }
-  } else if (warp == kSyncWarp) {
+  } else if (!kOp8 && warp == kSyncWarp) {
     if (lockstep) lockstep_service(p.sync_tag, sm, abort, lane);
   } else {
     // ---- epilogue ----
@@ -1122,11 +1178,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
           if (tloc >= 0 && tloc < vcols) p.target_logit[row] = tl;
         }
       } else if constexpr (MODE == kModePartials8) {
-        unsigned char* staging_all = reinterpret_cast<unsigned char*>(
-            (reinterpret_cast<uintptr_t>(&sm + 1) + 1023) & ~static_cast<uintptr_t>(1023));
         const bool ok = epilogue8<ENT>(
-            p, tmap_out, taddr, staging_all + q * 2 * kStoreBoxBytes,
-            reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN, row, n, lane, store_boxes,
+            p, tmap_out, taddr, base + kStagesH * size_t(kStageBytesH) + (warp - 2) * 2 * kStoreBoxBytes,
+            *reinterpret_cast<Exchange8*>(base + kStages * size_t(kStageBytes) + 1024), epi8(warp), row, n, lane,
+            store_boxes,
             [&] { return warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear); },
             [&] { mbar_arrive(&sm.acc_empty[b]); });
         if (!ok) break;
@@ -1206,10 +1261,9 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
 // one-block kernel, and so are the bits.
 // ---------------------------------------------------------------------------
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 6;  // with the logits five, the sixth is the epilogue's
 constexpr unsigned kPairStageBytes = 2 * kStageABytes;  // 128 rows of A, 128 of B
-constexpr int kPairThreads = 32 * (2 + kEpiWarps);
-static_assert(kPairStages * size_t(kPairStageBytes) <= kStages * size_t(kStageBytes), "the one-block kernel's ring");
+static_assert(kPairStages * size_t(kPairStageBytes) == kStages * size_t(kStageBytes), "the one-block kernel's layout");
 
 struct alignas(8) PairSmem {
   uint64_t full[kPairStages];
@@ -1260,11 +1314,12 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-template <bool ENT>
-__global__ void __launch_bounds__(kPairThreads, 1)
+template <bool ENT, bool LOGITS>
+__global__ void __launch_bounds__(kThreads8, 1)
     linear_partials8_pair_kernel(const __grid_constant__ CUtensorMap tmap_hidden,
                                  const __grid_constant__ CUtensorMap tmap_weight,
                                  const __grid_constant__ CUtensorMap tmap_logits, const LinearParams p) {
+  constexpr int kRing = kPairStages - (LOGITS ? 1 : 0);
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1281,7 +1336,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.acc_full[b], 1);
-      mbar_init(&sm.acc_empty[b], 2 * kEpiWarps);
+      mbar_init(&sm.acc_empty[b], 2 * kEpiWarps8);
     }
     mbar_init(&sm.mma_done, 1);
     sm.abort = 0;
@@ -1313,8 +1368,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int m, n;
         unit_coords(u, p.num_m, p.num_n, p.m_group, m, n);
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const int s = static_cast<int>(it % kPairStages);
-          const unsigned ph = static_cast<unsigned>((it / kPairStages) & 1);
+          const int s = static_cast<int>(it % kRing);
+          const unsigned ph = static_cast<unsigned>((it / kRing) & 1);
           if (!thread_wait_watch(&sm.empty[s], ph ^ 1u, abort, kWatchStageFree, &g_watchdog_linear, true)) {
             ok = false;
             break;
@@ -1329,8 +1384,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // The leader waits (bounded, whatever happened) for the pair's copies still in flight; the other block
       // waits for the leader at the end.
       if (rank == 0) {
-        for (int64_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i) {
-          if (!thread_wait_watch(&sm.full[i % kPairStages], static_cast<unsigned>((i / kPairStages) & 1), abort,
+        for (int64_t i = it > kRing ? it - kRing : 0; i < it; ++i) {
+          if (!thread_wait_watch(&sm.full[i % kRing], static_cast<unsigned>((i / kRing) & 1), abort,
                                  kWatchOwnDrain, &g_watchdog_linear, false))
             break;
         }
@@ -1349,8 +1404,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kAccCols);
         for (int kb = 0; kb < p.k_blocks; ++kb, ++it) {
-          const int s = static_cast<int>(it % kPairStages);
-          const unsigned ph = static_cast<unsigned>((it / kPairStages) & 1);
+          const int s = static_cast<int>(it % kRing);
+          const unsigned ph = static_cast<unsigned>((it / kRing) & 1);
           if (!thread_wait_watch(&sm.full[s], ph, abort, kWatchMma, &g_watchdog_linear, true)) {
             ok = false;
             break;
@@ -1373,8 +1428,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     // ---- epilogue: this block's 128 rows ----
     const int q = warp & 3;
-    unsigned char* staging_all = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(&sm + 1) + 1023) & ~static_cast<uintptr_t>(1023));
     int local = 0;
     uint32_t store_boxes = 0;
     for (int64_t u = pair0; u < total; u += pairs, ++local) {
@@ -1385,8 +1438,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int64_t row = (static_cast<int64_t>(2) * m + rank) * kBM + q * 32 + lane;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kAccCols);
       const bool ok = epilogue8<ENT>(
-          p, tmap_logits, taddr, staging_all + q * 2 * kStoreBoxBytes,
-          reinterpret_cast<float*>(staging_all + kStagingBytes8) + q * kBN, row, n, lane, store_boxes,
+          p, tmap_logits, taddr, base + kRing * size_t(kPairStageBytes) + (warp - 2) * 2 * kStoreBoxBytes,
+          *reinterpret_cast<Exchange8*>(base + kPairStages * size_t(kPairStageBytes) + 1024), epi8(warp), row, n, lane,
+          store_boxes,
           [&] { return warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_linear); },
           [&] {
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
@@ -1418,12 +1472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Forward on e4m3 operands with a scale per row of each.
-template <bool ENT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool ENT, bool LOGITS>
+__global__ void __launch_bounds__(kThreads8, 1)
     linear_partials8_kernel(const __grid_constant__ CUtensorMap tmap_hidden,
                             const __grid_constant__ CUtensorMap tmap_weight,
                             const __grid_constant__ CUtensorMap tmap_logits, const LinearParams p) {
-  gemm_body<kModePartials8, ENT, BIL_F32>(tmap_hidden, tmap_weight, tmap_logits, p);
+  gemm_body<kModePartials8, ENT, LOGITS ? 1 : 0>(tmap_hidden, tmap_weight, tmap_logits, p);
 }
 
 // Backward, first pass: hidden . weight^T recomputed, dZ stored (16-bit DT).
@@ -2005,14 +2059,19 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   p.m_group = pair ? kMGroup / 2 : kMGroup;
   p.row_scale = hidden_scale;
   p.col_scale = weight_scale;
-  GemmKernel kernel = pair ? (ent ? linear_partials8_pair_kernel<true> : linear_partials8_pair_kernel<false>)
-                           : (ent ? linear_partials8_kernel<true> : linear_partials8_kernel<false>);
+  GemmKernel kernel;
+  if (pair)
+    kernel = logits != nullptr ? (ent ? linear_partials8_pair_kernel<true, true> : linear_partials8_pair_kernel<false, true>)
+                               : (ent ? linear_partials8_pair_kernel<true, false> : linear_partials8_pair_kernel<false, false>);
+  else
+    kernel = logits != nullptr ? (ent ? linear_partials8_kernel<true, true> : linear_partials8_kernel<false, true>)
+                               : (ent ? linear_partials8_kernel<true, false> : linear_partials8_kernel<false, false>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes8)) !=
       cudaSuccess)
     return BIL_E_CUDA;
   const int blocks = pair ? 2 : 1;  // of a unit
   const int64_t grid = std::min<int64_t>(static_cast<int64_t>(p.num_m) * p.num_n, sms / blocks) * blocks;
-  if (launch_pdl(kernel, grid, pair ? kPairThreads : kThreads, kSmemBytes8, s, blocks, mh, mw, mo, p) != cudaSuccess)
+  if (launch_pdl(kernel, grid, kThreads8, kSmemBytes8, s, blocks, mh, mw, mo, p) != cudaSuccess)
     return BIL_E_CUDA;
   return bil_logp_merge(p.part_max, p.part_sum, p.part_ent, n_rows, static_cast<int32_t>(num_tiles), num_tiles,
                         p.target_logit, target_ids, ignore_index, vocab, logp, lse, entropy, 0, stream);
