@@ -223,7 +223,8 @@ int bil_logp_bwd(const void *logits, int dtype, int64_t n_rows, int64_t vocab, i
 /*
  * bil_logp_topk_workspace_bytes -- bytes of device workspace that
  * bil_logp_topk_fwd needs (entropy != 0: with the entropy output): the tiles'
- * partials and the maxima of their chunks.  Host arithmetic only.
+ * partials and the maxima of their chunks.  0 for few rows of a 16-bit type (at
+ * least eight tiles wide), which need none.  Host arithmetic only.
  */
 int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, int32_t k, int entropy,
                                   int64_t *bytes);
@@ -243,7 +244,7 @@ int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int3
  *                is outside the vocabulary has its alternatives all the same.)
  *  workspace     256-byte aligned device memory of at least
  *                bil_logp_topk_workspace_bytes bytes, scratch; two calls in
- *                flight at once need two.
+ *                flight at once need two.  Not looked at where that is 0.
  * vocab and n_rows up to 2^31 - 1, at most BIL_MAX_FUSED_TILES tiles.  Other
  * arguments as for bil_logp_fwd.
  */

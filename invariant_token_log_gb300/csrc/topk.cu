@@ -27,7 +27,14 @@
 // to 265 us (they lie in 16 places 512 bytes apart, and the row kernel was bound
 // by the 45 KB of DRAM lines it read again per row).
 //
-// Bound: HBM, one read of the logits (16384 x 151936 bf16: 4.98 GB).
+// Up to 48 rows of a 16-bit type take one kernel that does both, a cluster of
+// blocks a row (topk_cluster_kernel).
+//
+// Bound: HBM, one read of the logits.  4096 x 151936 bf16, k = 20: 204 us, 6.1 TB/s
+// (0.90 of a plain copy's rate), 184 us of it the copy's floor and 10 us the row
+// kernel's; with the entropy 242 us (the streaming kernel's instructions then
+// count as much as its bytes); float32 406 us, 6.1 TB/s.  One row: 7 us, the
+// latency of the launch, of one tile and of the choice.
 //
 //   topk_grad_sum_kernel  g + sum_j gk_j, what the softmax term is scaled by;
 //   (bil_logp_bwd)        d = -(g + sum gk) p - gh p (a + H), one pass;
@@ -199,14 +206,11 @@ struct ChunkMax {
 // the group, one selection and a funnel shift by what is left of the offset (one
 // code for all eight offsets, which differ from row to row).  Of float32: the
 // 16-byte units, a case an offset (8-byte reads 32 bytes apart would take the
-// banks nearly twice as long).  LIMIT (16-bit): only 8-byte words below `limit`
-// bytes are read (global memory).
-template <int DT, bool LIMIT>
-__device__ __forceinline__ void load_group_at(const unsigned char* tile, unsigned off, int g, uint32_t (&w)[Group<DT>::kW],
-                                              int limit) {
+// banks nearly twice as long).
+template <int DT>
+__device__ __forceinline__ void load_group_at(const unsigned char* tile, unsigned off, int g, uint32_t (&w)[Group<DT>::kW]) {
   constexpr int kW = Group<DT>::kW;
   if constexpr (Elem<DT>::kBytes == 4) {
-    static_assert(!LIMIT, "float32 tiles are read from their stage alone");
     switch (off >> 2) {
       case 0: load_group<DT, 0>(tile, g, 0, w); break;
       case 1: load_group<DT, 1>(tile, g, 0, w); break;
@@ -218,8 +222,7 @@ __device__ __forceinline__ void load_group_at(const unsigned char* tile, unsigne
     uint32_t v[kW + 2];
 #pragma unroll
     for (int q = 0; q < kW / 2 + 1; ++q) {
-      uint2 x = make_uint2(0u, 0u);
-      if (!LIMIT || at + 8 * q < limit) x = *reinterpret_cast<const uint2*>(tile + at + 8 * q);
+      const uint2 x = *reinterpret_cast<const uint2*>(tile + at + 8 * q);
       v[2 * q] = x.x;
       v[2 * q + 1] = x.y;
     }
@@ -238,22 +241,98 @@ __device__ __forceinline__ void stage_group(const unsigned char* tile, unsigned 
   if constexpr (ALIGNED)
     load_group<DT, -1>(tile, g, 0, w);
   else
-    load_group_at<DT, false>(tile, off, g, w, 0);
+    load_group_at<DT>(tile, off, g, w);
   if (valid - g * kGroup < kGroup) Group<DT>::mask_tail(w, valid - g * kGroup);
 }
 
-// The lane's groups of a tile off 16-byte boundaries, as tile_load_regs gives those of one on them.
-template <int DT, bool LIMIT>
+// The lane's groups of a staged tile off 16-byte boundaries, as tile_load_regs
+// gives those of one on them.
+template <int DT>
 __device__ __forceinline__ void load_regs_at(const unsigned char* tile, unsigned off, int valid, int lane, TileRegs<DT>& r) {
-  const int limit = (static_cast<int>(off) + valid * Elem<DT>::kBytes + 15) & ~15;
 #pragma unroll
   for (int i = 0; i < TileRegs<DT>::kMaxGroups; ++i) {
     const int g = lane + kLanes * i;
     if (g * kGroup < valid) {
-      load_group_at<DT, LIMIT>(tile, off, g, r.w[i], limit);
+      load_group_at<DT>(tile, off, g, r.w[i]);
       if (valid - g * kGroup < kGroup) Group<DT>::mask_tail(r.w[i], valid - g * kGroup);
     }
   }
+}
+
+// The same from global memory (16-bit types): the aligned 16-byte units that hold
+// the tile, each read once, by the lane that has the group that begins in it; the
+// rest of a group is in the next lane's unit.  (Each lane reading the three 8-byte
+// words of its groups: 32 rows of 151936 columns, 151939 apart, 14.8 us; so 10.7.)
+template <int DT>
+__device__ __forceinline__ void load_regs_shifted(const unsigned char* tile, unsigned off, int valid, int lane,
+                                                  TileRegs<DT>& r) {
+  constexpr int kGroups = TileRegs<DT>::kMaxGroups;
+  const uint4* units = reinterpret_cast<const uint4*>(tile);
+  const int n = (static_cast<int>(off) + valid * Elem<DT>::kBytes + 15) / 16;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int g = lane + kLanes * i;
+    const uint4 u = g < n ? units[g] : make_uint4(0u, 0u, 0u, 0u);
+    r.w[i][0] = u.x, r.w[i][1] = u.y, r.w[i][2] = u.z, r.w[i][3] = u.w;
+  }
+  uint4 past = make_uint4(0u, 0u, 0u, 0u);
+  if (lane == 0 && kGroups * kLanes < n) past = units[kGroups * kLanes];
+  const bool two = (off & 8u) != 0, one = (off & 4u) != 0;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const uint32_t next[4] = {i + 1 < kGroups ? r.w[(i + 1) % kGroups][0] : past.x,
+                              i + 1 < kGroups ? r.w[(i + 1) % kGroups][1] : past.y,
+                              i + 1 < kGroups ? r.w[(i + 1) % kGroups][2] : past.z,
+                              i + 1 < kGroups ? r.w[(i + 1) % kGroups][3] : past.w};
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = r.w[i][j];
+      v[4 + j] = __shfl_sync(0xffffffffu, lane == 0 ? next[j] : r.w[i][j], (lane + 1) % kLanes);
+    }
+#pragma unroll
+    for (int j = 0; j < 6; ++j) v[j] = two ? v[j + 2] : v[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = one ? v[j + 1] : v[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[i][j] = __funnelshift_r(v[j], v[j + 1], 8u * (off & 3u));
+    const int left = valid - (lane + kLanes * i) * kGroup;
+    if (left > 0 && left < kGroup) Group<DT>::mask_tail(r.w[i], left);
+  }
+}
+
+// As in the streaming forward, a tile's entropy sum from a clamped pass over the
+// logits (in global memory), where the plain one gave NaN; mx_all: the tile's
+// maximum.  Off 16-byte boundaries two groups at a time: all of them, shifted, do
+// not fit beside what the pass keeps.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ float clamped_entropy(const unsigned char* src, int valid, int lane, float mx_all, float rcp,
+                                                 TileRegs<DT>& regs) {
+  if constexpr (ALIGNED) {
+    tile_load_regs<DT>(src, valid, lane, regs);
+    return tile_reduce_regs<DT, true, true>(regs, valid, lane, rcp).u;
+  }
+  const float shift = (mx_all == -INFINITY) ? 0.0f : mx_all;
+  const float c = __fmul_rn(rcp, kLog2e);
+  const uint64_t shift2 = pk(shift, shift), c2 = pk(c, c);
+  uint64_t a[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll 2
+  for (int g = lane; g * kGroup < valid; g += kLanes) {
+    const int left = valid - g * kGroup;
+    uint32_t w[Group<DT>::kW];
+    // the 4-byte words that hold a column of the tile
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src) + g * kGroup * Elem<DT>::kBytes;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(at & ~static_cast<uintptr_t>(3));
+    const uint32_t* end = reinterpret_cast<const uint32_t*>(src + valid * Elem<DT>::kBytes);
+    uint32_t v[Group<DT>::kW + 1];
+#pragma unroll
+    for (int j = 0; j <= Group<DT>::kW; ++j) v[j] = q + j < end ? q[j] : 0u;
+#pragma unroll
+    for (int j = 0; j < Group<DT>::kW; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], 8u * (at & 3u));
+    if (left < kGroup) Group<DT>::mask_tail(w, left);
+    Group<DT>::template sum_acc<true, true>(a, u, w, shift2, c2);
+  }
+  return finish_tile<true>(0.0f, a, u).u;
 }
 
 // A tile of a 16-bit type in registers: its chunk maxima, to `out`, and the
@@ -446,21 +525,14 @@ __global__ void __launch_bounds__(kTopkMaxWarps * kLanes, 2) topk_stream_kernel(
         if (ALIGNED)
           tile_load_regs<DT>(stage, valid, lane, regs);
         else
-          load_regs_at<DT, false>(stage, off, valid, lane, regs);
+          load_regs_at<DT>(stage, off, valid, lane, regs);
         __syncwarp();  // the stage has been read
         issue();
         const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, chunks, p.tile_chunks)
                                             : regs_max<DT, false>(regs, valid, lane, chunks, p.tile_chunks));
         tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
                    : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
-        if (ENT && tp.u != tp.u) {  // as in the streaming forward: u from a clamped pass
-          if (ALIGNED) {
-            tile_load_regs<DT>(src, valid, lane, regs);
-          } else {
-            load_regs_at<DT, true>(src - off, off, valid, lane, regs);
-          }
-          tp.u = tile_reduce_regs<DT, ENT, true>(regs, valid, lane, p.rcp).u;
-        }
+        if (ENT && tp.u != tp.u) tp.u = clamped_entropy<DT, ALIGNED>(src, valid, lane, mx_all, p.rcp, regs);
         done = true;
       }
     }
@@ -896,20 +968,22 @@ __device__ __forceinline__ void select_columns(const RowColumns<DT, SW>& cols, i
   }
 }
 
+struct TopkOut {
+  float* logp;
+  float* lse;
+  float* entropy;
+  int64_t* top_ids;
+  float* top_logp;
+};
+
+// A row's results from its chunk maxima and partials (in global or in shared
+// memory): one warp, or SW + 1 of a block.
 template <int DT, bool ENT, int SW>
-__global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW == 1 ? 6 : 4)
-    topk_row_kernel(const TopkParams p, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp) {
-  constexpr int kRows = SW == 1 ? 4 : 1;  // rows of a block
-  __shared__ SelShared<SW> shared[kRows];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
-  const int64_t row = SW == 1 ? static_cast<int64_t>(blockIdx.x) * kRows + warp : blockIdx.x;
-  if (row >= p.n_rows) return;  // a warp of its own: no barrier follows
-  SelShared<SW>& sm = shared[SW == 1 ? warp : 0];
-  const int64_t t = p.targets[row];
-  int64_t* ids = top_ids + row * p.k;
-  float* top = top_logp + row * p.k;
+__device__ __forceinline__ void finish_row(const TopkParams& p, const TopkOut& out, int64_t row, int64_t t,
+                                           const unsigned char* chunks, const float* part_max, const float* part_sum,
+                                           const float* part_ent, SelShared<SW>& sm, int warp, int lane) {
+  int64_t* ids = out.top_ids + row * p.k;
+  float* top = out.top_logp + row * p.k;
   const int tid = SW == 1 ? lane : static_cast<int>(threadIdx.x);
   constexpr int kThreads = SW == 1 ? kLanes : (SW + 1) * kLanes;
   if (t == p.ignore_index) {
@@ -918,9 +992,9 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW =
       top[j] = 0.0f;
     }
     if (tid == 0) {
-      logp[row] = 0.0f;
-      if (lse != nullptr) lse[row] = 0.0f;
-      if (ENT) entropy[row] = 0.0f;
+      out.logp[row] = 0.0f;
+      if (out.lse != nullptr) out.lse[row] = 0.0f;
+      if (ENT) out.entropy[row] = 0.0f;
     }
     return;
   }
@@ -929,7 +1003,7 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW =
     RowColumns<DT, SW> cols;
     cols.row = src;
     cols.num_tiles = p.num_tiles;
-    cols.chunks = p.chunk_max + row * p.chunk_pitch;
+    cols.chunks = chunks;
     cols.units = static_cast<int>(p.chunk_pitch / 16);
     cols.vocab = static_cast<int>(p.vocab);
     cols.tile_v = p.tile_v;
@@ -940,10 +1014,8 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW =
     select_columns<DT, SW>(cols, p.k, sm);
   }
   if (SW == 1 || warp == SW) {
-    const int64_t o = row * p.num_tiles;
     float H = 0.0f;
-    const float L = merge_lse<ENT, true>(p.part_max + o, p.part_sum + o, ENT ? p.part_ent + o : nullptr, p.num_tiles,
-                                         lane, &H, sm.scratch);
+    const float L = merge_lse<ENT, true>(part_max, part_sum, part_ent, p.num_tiles, lane, &H, sm.scratch);
     if (lane == 0) {
       sm.lse = L;
       float z = __int_as_float(0x7fc00000);
@@ -951,9 +1023,9 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW =
         z = Elem<DT>::one(src + t * Elem<DT>::kBytes);
         if (p.rcp != 1.0f) z = __fmul_rn(z, p.rcp);
       }
-      logp[row] = __fsub_rn(z, L);
-      if (lse != nullptr) lse[row] = L;
-      if (ENT) entropy[row] = H;
+      out.logp[row] = __fsub_rn(z, L);
+      if (out.lse != nullptr) out.lse[row] = L;
+      if (ENT) out.entropy[row] = H;
     }
   }
   if constexpr (SW == 1)
@@ -967,6 +1039,99 @@ __global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW =
     ids[j] = entry_column(e);
     top[j] = __fsub_rn(z, sm.lse);
   }
+}
+
+
+template <int DT, bool ENT, int SW>
+__global__ void __launch_bounds__(SW == 1 ? 4 * kLanes : (SW + 1) * kLanes, SW == 1 ? 6 : 4)
+    topk_row_kernel(const TopkParams p, const TopkOut out) {
+  constexpr int kRows = SW == 1 ? 4 : 1;  // rows of a block
+  __shared__ SelShared<SW> shared[kRows];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
+  const int64_t row = SW == 1 ? static_cast<int64_t>(blockIdx.x) * kRows + warp : blockIdx.x;
+  if (row >= p.n_rows) return;  // a warp of its own: no barrier follows
+  const int64_t o = row * p.num_tiles;
+  finish_row<DT, ENT, SW>(p, out, row, p.targets[row], p.chunk_max + row * p.chunk_pitch, p.part_max + o,
+                          p.part_sum + o, ENT ? p.part_ent + o : nullptr, shared[SW == 1 ? warp : 0], warp, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows of a 16-bit type: one kernel and no workspace.  A row is shared by a
+// cluster of eight blocks, as in the small-batch forward: each warp reduces its
+// tiles from global memory with the functions of the pass above, chunk maxima and
+// partials go to the first block over distributed shared memory, and after the
+// cluster's barrier that block ends the row.
+// ---------------------------------------------------------------------------
+
+constexpr int kClusterTiles = 256;            // most tiles of a row
+constexpr size_t kClusterChunks = 24 * 1024;  // most bytes of a row's chunk maxima
+
+// The address of `p` (a shared variable of this block) in the block of rank `rank`.
+template <typename T>
+__device__ __forceinline__ T* cluster_ptr(T* p, uint32_t rank) {
+  uint64_t r;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(r);
+}
+
+template <int DT, bool ALIGNED, bool ENT>
+__global__ void __launch_bounds__((kFewRowWarps + 1) * kLanes, 3)
+    topk_cluster_kernel(const TopkParams p, const TopkOut out) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];  // the row's chunk maxima (the first block's)
+  __shared__ SelShared<kFewRowWarps> sm;
+  __shared__ float part[3][kClusterTiles];
+  constexpr int EB = Elem<DT>::kBytes;
+  constexpr int kWarps = kFewRowWarps + 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int64_t row = static_cast<int64_t>(blockIdx.x) / kSplitCtas;
+  const int64_t t = p.targets[row];
+  // the first block has to have started before the others write into it; the first tiles are loaded meanwhile
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  TileRegs<DT> regs;
+  const unsigned char* src;
+  int valid;
+  unsigned off;
+  const auto load = [&](int tile) {
+    src = p.logits + (row * p.ld + static_cast<int64_t>(tile) * p.tile_v) * EB;
+    valid = static_cast<int>(min(static_cast<int64_t>(p.tile_v), p.vocab - static_cast<int64_t>(tile) * p.tile_v));
+    off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(src) & 15u);
+    if (ALIGNED)
+      tile_load_regs<DT>(src, valid, lane, regs);
+    else
+      load_regs_shifted<DT>(src - off, off, valid, lane, regs);
+  };
+  int tile = t != p.ignore_index ? warp * kSplitCtas + rank : p.num_tiles;
+  if (tile < p.num_tiles) load(tile);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  unsigned char* chunks = cluster_ptr(smem_raw, 0);
+  while (tile < p.num_tiles) {
+    const bool whole = valid == TileRegs<DT>::kMaxTile;
+    unsigned char* at = chunks + static_cast<int64_t>(tile) * p.tile_chunks * EB;
+    const float mx_all = warp_max(whole ? regs_max<DT, true>(regs, valid, lane, at, p.tile_chunks)
+                                        : regs_max<DT, false>(regs, valid, lane, at, p.tile_chunks));
+    TilePartial tp = whole ? regs_sums<DT, true, ENT>(regs, valid, lane, mx_all, p.rcp)
+                           : regs_sums<DT, false, ENT>(regs, valid, lane, mx_all, p.rcp);
+    if (ENT && tp.u != tp.u) tp.u = clamped_entropy<DT, ALIGNED>(src, valid, lane, mx_all, p.rcp, regs);
+    if (lane == 0) {
+      *cluster_ptr(&part[0][tile], 0) = tp.m;
+      *cluster_ptr(&part[1][tile], 0) = tp.s;
+      if (ENT) *cluster_ptr(&part[2][tile], 0) = tp.u;
+    }
+    if (tile == p.num_tiles - 1) {  // the rest of the row's last 16 bytes
+      const int pad = p.num_tiles * p.tile_chunks + lane;
+      if (pad < p.chunk_pitch / EB) store_value<DT>(chunks, pad, -INFINITY);
+    }
+    tile += kSplitCtas * kWarps;
+    if (tile < p.num_tiles) load(tile);
+  }
+  cluster_sync_all();
+  if (rank != 0) return;
+  finish_row<DT, ENT, kFewRowWarps>(p, out, row, t, smem_raw, part[0], part[1], part[2], sm, warp, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1103,6 +1268,20 @@ TopkWorkspace topk_workspace(int dtype, int64_t n_rows, int64_t num_tiles, int t
   return w;
 }
 
+// Whether the forward takes the cluster kernel (and no workspace): rows of a
+// 16-bit type with a tile or more for every block of a cluster, and all their
+// blocks on the device at a time.  151936 columns of bfloat16, k = 20, in a CUDA
+// graph: 1 row 7.1 us (the two kernels 8.1), 32 rows 8.7 (9.9), 48 rows 9.7 (10.8),
+// 64 rows 13.0 (12.2), 128 rows 18.5 (15.8); rows off 16-byte boundaries 7.0 to 11.9
+// (8.2 to 12.9) up to 48.  A call from Python: 20 us (27).
+#ifndef BIL_TOPK_CLUSTER_ROWS
+#define BIL_TOPK_CLUSTER_ROWS 48
+#endif
+bool use_cluster(int dtype, int64_t n_rows, int64_t num_tiles, int tile_v, const TopkWorkspace& w) {
+  return dtype != BIL_F32 && n_rows <= BIL_TOPK_CLUSTER_ROWS && num_tiles >= kSplitCtas && num_tiles <= kClusterTiles &&
+         tile_v <= 4096 && w.pitch <= kClusterChunks;
+}
+
 // The sizes both the workspace query and the forward check.
 int check_topk_sizes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, int32_t k, int64_t* num_tiles) {
   if (n_rows < 0 || vocab < 1 || k < 1 || k > vocab) return BIL_E_INVALID_ARG;
@@ -1113,8 +1292,16 @@ int check_topk_sizes(int dtype, int64_t n_rows, int64_t vocab, int32_t tile_v, i
 }
 
 template <int DT, bool ALIGNED, bool ENT>
-int launch_topk_t(TopkParams p, float* logp, float* lse, float* entropy, int64_t* top_ids, float* top_logp,
-                  cudaStream_t stream) {
+int launch_topk_t(TopkParams p, const TopkOut& out, cudaStream_t stream) {
+  if (p.chunk_max == nullptr) {  // no workspace: few rows
+    if constexpr (Elem<DT>::kBytes == 2) {
+      return launch_pdl(topk_cluster_kernel<DT, ALIGNED, ENT>, p.n_rows * kSplitCtas, (kFewRowWarps + 1) * kLanes,
+                        static_cast<size_t>(p.chunk_pitch), stream, kSplitCtas, p, out) == cudaSuccess
+                 ? BIL_OK
+                 : BIL_E_CUDA;
+    }
+    return BIL_E_INVALID_ARG;
+  }
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   p.stage_bytes =
@@ -1140,22 +1327,20 @@ int launch_topk_t(TopkParams p, float* logp, float* lse, float* entropy, int64_t
   // One warp a row from four rows an SM on.
   const cudaError_t e =
       p.n_rows >= 4 * static_cast<int64_t>(sms)
-          ? launch_pdl(topk_row_kernel<DT, ENT, 1>, (p.n_rows + 3) / 4, 4 * kLanes, 0, stream, 1, p, logp, lse, entropy,
-                       top_ids, top_logp)
+          ? launch_pdl(topk_row_kernel<DT, ENT, 1>, (p.n_rows + 3) / 4, 4 * kLanes, 0, stream, 1, p, out)
           : launch_pdl(topk_row_kernel<DT, ENT, kFewRowWarps>, p.n_rows, (kFewRowWarps + 1) * kLanes, 0, stream, 1, p,
-                       logp, lse, entropy, top_ids, top_logp);
+                       out);
   return e == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
 template <int DT>
-int launch_topk(const TopkParams& p, bool ent, float* logp, float* lse, float* entropy, int64_t* top_ids,
-                float* top_logp, cudaStream_t stream) {
+int launch_topk(const TopkParams& p, bool ent, const TopkOut& out, cudaStream_t stream) {
   const bool vec = aligned_to(p.logits, 16) && (p.n_rows <= 1 || (p.ld * Elem<DT>::kBytes) % 16 == 0);
   if (vec)
-    return ent ? launch_topk_t<DT, true, true>(p, logp, lse, entropy, top_ids, top_logp, stream)
-               : launch_topk_t<DT, true, false>(p, logp, lse, entropy, top_ids, top_logp, stream);
-  return ent ? launch_topk_t<DT, false, true>(p, logp, lse, entropy, top_ids, top_logp, stream)
-             : launch_topk_t<DT, false, false>(p, logp, lse, entropy, top_ids, top_logp, stream);
+    return ent ? launch_topk_t<DT, true, true>(p, out, stream)
+               : launch_topk_t<DT, true, false>(p, out, stream);
+  return ent ? launch_topk_t<DT, false, true>(p, out, stream)
+             : launch_topk_t<DT, false, false>(p, out, stream);
 }
 
 template <int DT>
@@ -1192,7 +1377,8 @@ int bil_logp_topk_workspace_bytes(int dtype, int64_t n_rows, int64_t vocab, int3
   if (bytes == nullptr) return BIL_E_INVALID_ARG;
   int64_t num_tiles = 0;
   if (int st = check_topk_sizes(dtype, n_rows, vocab, tile_v, k, &num_tiles)) return st;
-  *bytes = static_cast<int64_t>(topk_workspace(dtype, n_rows, num_tiles, tile_v, entropy != 0).total);
+  const TopkWorkspace w = topk_workspace(dtype, n_rows, num_tiles, tile_v, entropy != 0);
+  *bytes = use_cluster(dtype, n_rows, num_tiles, tile_v, w) ? 0 : static_cast<int64_t>(w.total);
   return BIL_OK;
 }
 
@@ -1210,16 +1396,17 @@ int bil_logp_topk_fwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
   float rcp = 1.0f;
   if (int st = bil_internal::temperature_rcp(temperature, &rcp)) return st;
   if (n_rows == 0) return BIL_OK;
+  const bool ent = entropy != nullptr;
+  const TopkWorkspace w = topk_workspace(dtype, n_rows, num_tiles, tile_v, ent);
+  const bool cluster = use_cluster(dtype, n_rows, num_tiles, tile_v, w);
   if (logits == nullptr || target_ids == nullptr || logp == nullptr || top_ids == nullptr || top_logp == nullptr ||
-      workspace == nullptr)
+      (!cluster && workspace == nullptr))
     return BIL_E_INVALID_ARG;
   if (!aligned_to(logits, static_cast<size_t>(eb)) || !aligned_to(target_ids, 8) || !aligned_to(logp, 4) ||
       (lse && !aligned_to(lse, 4)) || (entropy && !aligned_to(entropy, 4)) || !aligned_to(top_ids, 8) ||
-      !aligned_to(top_logp, 4) || !aligned_to(workspace, 256))
+      !aligned_to(top_logp, 4) || (!cluster && !aligned_to(workspace, 256)))
     return BIL_E_ALIGN;
-  const bool ent = entropy != nullptr;
-  const TopkWorkspace w = topk_workspace(dtype, n_rows, num_tiles, tile_v, ent);
-  if (workspace_bytes < static_cast<int64_t>(w.total)) return BIL_E_INVALID_ARG;
+  if (!cluster && workspace_bytes < static_cast<int64_t>(w.total)) return BIL_E_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
@@ -1238,14 +1425,17 @@ int bil_logp_topk_fwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
   p.ignore_index = ignore_index;
   p.rcp = rcp;
   p.k = k;
-  p.chunk_max = ws;
-  p.part_max = reinterpret_cast<float*>(ws + w.chunks);
-  p.part_sum = reinterpret_cast<float*>(ws + w.chunks + w.part);
-  p.part_ent = ent ? reinterpret_cast<float*>(ws + w.chunks + 2 * w.part) : nullptr;
+  if (!cluster) {
+    p.chunk_max = ws;
+    p.part_max = reinterpret_cast<float*>(ws + w.chunks);
+    p.part_sum = reinterpret_cast<float*>(ws + w.chunks + w.part);
+    p.part_ent = ent ? reinterpret_cast<float*>(ws + w.chunks + 2 * w.part) : nullptr;
+  }
+  const TopkOut out{logp, lse, entropy, top_ids, top_logp};
   switch (dtype) {
-    case BIL_BF16: return launch_topk<BIL_BF16>(p, ent, logp, lse, entropy, top_ids, top_logp, s);
-    case BIL_F16: return launch_topk<BIL_F16>(p, ent, logp, lse, entropy, top_ids, top_logp, s);
-    default: return launch_topk<BIL_F32>(p, ent, logp, lse, entropy, top_ids, top_logp, s);
+    case BIL_BF16: return launch_topk<BIL_BF16>(p, ent, out, s);
+    case BIL_F16: return launch_topk<BIL_F16>(p, ent, out, s);
+    default: return launch_topk<BIL_F32>(p, ent, out, s);
   }
 }
 

@@ -84,7 +84,9 @@ def logp_topk(logits: torch.Tensor, target_ids: torch.Tensor, k: int, ignore_ind
     top_logp = torch.empty((n, k), dtype=torch.float32, device=dev)
     need = _workspace_bytes(code, n, v, tile_v, k, return_entropy)
     if workspace is None:
-        workspace, have = torch.empty(need or 1, dtype=torch.uint8, device=dev), need
+        have = need
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need_cuda(workspace)
         have = workspace.numel() * workspace.element_size()
@@ -93,7 +95,7 @@ def logp_topk(logits: torch.Tensor, target_ids: torch.Tensor, k: int, ignore_ind
     fn = _lib.load().bil_logp_topk_fwd
     args = (x2.data_ptr(), code, n, v, x2.stride(0) if n > 1 else width, t1.data_ptr(), int(ignore_index), tile_v,
             float(temperature), k, logp.data_ptr(), lse.data_ptr(), entropy.data_ptr() if return_entropy else None,
-            top_ids.data_ptr(), top_logp.data_ptr(), workspace.data_ptr(), have, 1 if validate else 0,
+            top_ids.data_ptr(), top_logp.data_ptr(), workspace.data_ptr() if have else None, have, 1 if validate else 0,
             _stream_handle(index))
     st = fn(*args) if _get_device() == index else _on_device(index, fn, *args)
     if st:

@@ -460,3 +460,41 @@ def test_empty_and_refusals():
         bil.logp_topk_bwd(x, t, ids, lse[:3], logp, top)
     with pytest.raises(ValueError):
         bil.logp_topk_bwd(x, t, ids, lse, logp, top, entropy=lse)
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=IDS[1:])
+@pytest.mark.parametrize("tile_v", [512, 4096])
+@pytest.mark.parametrize("vocab,pad", [(33000, 0), (40007, 0), (40008, 5)])
+@pytest.mark.parametrize("k", [1, 20, 128])
+def test_few_rows_and_many_give_the_same_bits(vocab, pad, tile_v, k, dtype):
+    """Rows that need every way of the choice, few (a cluster a row) and among many (two kernels)."""
+    n = 9
+    x = rows(n, vocab, dtype, 41, pad=pad)
+    noise = torch.randn(vocab, generator=gen(42), device="cuda")
+    x[1] = 2.0                                            # all equal
+    x[2] = (2 * noise).round().to(dtype)                  # crowded
+    x[3] = -INF
+    x[3, vocab - 1] = 1.0                                 # one column left
+    x[4] = NAN                                            # none at all
+    x[5, 7::3] = NAN
+    x[6] = torch.finfo(dtype).min
+    x[7] = -INF                                           # nothing left
+    x[8, 100] = INF
+    t = targets(n, vocab, 41)
+    t[0] = IGNORE
+    check(x, t, k, tile_v=tile_v)
+    few = bil.logp_topk(x, t, k, tile_v=tile_v, return_entropy=True)
+    many = bil.logp_topk(x.repeat(20, 1), t.repeat(20), k, tile_v=tile_v, return_entropy=True)
+    for a, b in zip(few, many):
+        b = b.reshape(20, *a.shape)
+        for c in (b[0], b[11], b[19]):
+            assert torch.equal(a.nan_to_num(nan=7.0) if a.is_floating_point() else a,
+                               c.nan_to_num(nan=7.0) if c.is_floating_point() else c)
+
+
+def test_workspace_of_few_rows():
+    assert topk_mod.workspace_bytes(torch.bfloat16, 40, 151936, 20) == 0
+    assert topk_mod.workspace_bytes(torch.bfloat16, 1000, 151936, 20) > 0
+    assert topk_mod.workspace_bytes(torch.float32, 40, 151936, 20) > 0   # a 16-bit type's alone
+    assert topk_mod.workspace_bytes(torch.bfloat16, 40, 7 * 4096, 20) > 0  # eight tiles or more
+    assert topk_mod.workspace_bytes(torch.bfloat16, 1, 300 * 4096, 20) > 0  # and 256 at most
