@@ -43,8 +43,8 @@
 //                            tcgen05.mma kind::f8f6f4 over 128-element K
 //                            blocks (the same 128-byte lines), the partial
 //                            of the accumulator scaled by row and column.
-// For more than 128 rows that forward has a kernel of its own on pairs of blocks,
-// linear_partials8_pair_kernel.
+// For more than 128 rows of more than 1024 elements that forward has a kernel of
+// its own on pairs of blocks, linear_partials8_pair_kernel.
 //
 // What fixes the bits of z[r, c] is the K order (K blocks in order, four
 // K=16 steps each, from a zeroed accumulator), the same for every row and
@@ -1252,7 +1252,9 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
 // vocabulary columns), and gets the accumulator of its own 128 rows.  A K block of
 // 128 takes 32 KB of copies a block instead of 48 KB, and the ring has six stages
 // instead of four: e4m3's MMAs take a stage in 512 cycles, and with one block a
-// tile the copies' latency showed (tensor pipe 79% active at 2048 x 38912 x 4096).
+// tile the copies' latency showed (tensor pipe 79% active at 2048 x 38912 x 4096;
+// with pairs 88%, 175 us = 3.73 PFLOP/s under a profiler at 1.70 GHz).  4096 x
+// 151936 x 4096: 1.40 ms = 3.65 PFLOP/s in short runs, 1.58 ms at the power cap.
 //
 // Both blocks' copies count on the leader's (rank 0's) `full` barrier, which the
 // leader arms for the bytes of both; its MMA thread's commits arrive at both
@@ -2016,16 +2018,17 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
   }
-  // Pairs of blocks where their rounds of 256-row units, at 7/8 of the time of a round of 128-row tiles (the
-  // measured ratio: 173 to 190 us for sixteen rounds at K = 4096), come to less: 4096 rows of 151936 columns do (126
-  // rounds either way: 1.54 against 1.61 ms), 333 rows of 32003 do not (4 against 3: 54 against 42 us), nor does
-  // one row tile.  A batch of fewer rows than a tile goes in a box of exactly its rows, as in
-  // bil_linear_logp_partials.
+  // Pairs of blocks where K is long enough for the copies to bound one block's kernel, and where their rounds of
+  // 256-row units, at 7/8 of the time of a round of 128-row tiles, come to less.  Pairs against single blocks, us:
+  // 4096 x 151936 x 4096 1398 and 1455, 2048 x 38912 x 4096 194 and 211, x 2048 113 and 119, x 1024 98 and 94 (the
+  // epilogue bounds both), 4096 x 152064 x 1024 593 and 580, 384 x 128256 x 4096 (more rounds) 200 and 179.  A
+  // batch of fewer rows than a tile goes in a box of exactly its rows, as in bil_linear_logp_partials.
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   if (static_cast<size_t>(smem_optin) < kSmemBytes8) return BIL_E_UNSUPPORTED;
   const int64_t tiles = (n_rows + kBM - 1) / kBM * num_tiles, units = (n_rows + 2 * kBM - 1) / (2 * kBM) * num_tiles;
-  const bool pair = n_rows > kBM && 7 * ((units + sms / 2 - 1) / (sms / 2)) < 8 * ((tiles + sms - 1) / sms);
+  const bool pair =
+      n_rows > kBM && hidden_size > 1024 && 7 * ((units + sms / 2 - 1) / (sms / 2)) < 8 * ((tiles + sms - 1) / sms);
   const int a_rows = static_cast<int>(n_rows < kBM ? n_rows : kBM);
   CUtensorMap mh, mw;
   if (int st = make_map8(&mh, hidden, n_rows, hidden_size, ld_hidden, a_rows)) return st;

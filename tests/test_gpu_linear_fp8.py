@@ -224,3 +224,27 @@ def test_empty_and_refusals():
     with pytest.raises(bil.BilError) as e:
         bil.linear_logp_fp8(hq, hs, wq, ws, t, validate=True)
     assert e.value.status == _lib.E_TARGET_RANGE
+
+
+@pytest.mark.parametrize("n,h,v", [(129, 1168, 257), (200, 1040, 9001), (513, 2064, 3000), (700, 4096, 2600)])
+def test_long_hidden_rows_in_large_and_small_batches(n, h, v):
+    """More than 128 rows of more than 1024 elements (pairs of blocks) against 64 bits, in every form of the
+    outputs, and bit for bit against batches of one row tile (single blocks)."""
+    hq, hs, wq, ws, t = make_case(n, h, v, seed=10)
+    rz, rlogp, rlse, rent = reference(hq, hs, wq, ws, t, 0.7)
+    full = bil.linear_logp_fp8(hq, hs, wq, ws, t, temperature=0.7, return_entropy=True, return_logits=True)
+    size = (hq.double().abs() @ wq.double().abs().t()) * ws.double().abs() * hs.double()[:, None]
+    bound = ((h / 32 + 1) * 2.0 ** -23 + 2.0 ** -20) * size + 2.0 ** -23 * rz.abs()  # as above
+    assert bool(((full[3].double() - rz).abs() <= bound).all())
+    close(full[0], rlogp, LOGP_ATOL, "logp")
+    close(full[1], rlse, LOGP_ATOL, "lse")
+    close(full[2], rent, ENTROPY_ATOL, "entropy")
+    plain = bil.linear_logp_fp8(hq, hs, wq, ws, t, temperature=0.7)
+    half = bil.linear_logp_fp8(hq, hs, wq, ws, t, temperature=0.7, return_logits=True, logits_dtype=torch.bfloat16)
+    for other in (plain, half):
+        assert all(np.array_equal(f32_bits(a), f32_bits(b)) for a, b in zip(other[:2], full[:2]))
+    assert torch.equal(half[2], full[3].to(torch.bfloat16))
+    for s in (slice(0, 100), slice(n - 128, n), slice(n - 1, n)):
+        part = bil.linear_logp_fp8(hq[s], hs[s], wq, ws, t[s], temperature=0.7, return_entropy=True, return_logits=True)
+        for a, b in zip(part, full):
+            assert np.array_equal(f32_bits(a), f32_bits(b[s]))
