@@ -18,8 +18,11 @@
 // squares and its maximum are one reduction; 2^-100 keeps an all-zero row's
 // scale positive.
 //
-// Bound: HBM.  Every element is read once and written once (16384 x 4096 bf16:
-// 537 MB, 79 us at the measured copy rate).  A row is held between its
+// Bound: HBM.  Every element is read once and written once.  16384 x 4096 bf16 (a
+// plain copy's rate would be 6.8 TB/s): the forward with a residual 537 MB, 78 us,
+// 6.85 TB/s; to 8 bits 470 MB, 70 us, 6.7 TB/s; the backward with dh 537 MB, 88 us,
+// 6.1 TB/s, 8 us of it the weight's sums over the blocks.  Rows off 16-byte
+// boundaries (16384 x 4097): 95, 115 and 168 us.  A row is held between its
 // reduction and its output: thread r of the row's TPR threads has the 8-element
 // groups r, r + TPR, ... (at most 4).  TPR and the sums' order follow from the
 // width alone, so a row's bits do not depend on the batch.  The forward keeps
@@ -51,7 +54,8 @@ constexpr int kMaxRowThreads = 512;
 constexpr int kMaxStages = 4;       // of the backward's ring
 
 __device__ unsigned int g_watchdog_norm;
-constexpr unsigned kWatchNorm = 1024u;  // the backward's wait for a row
+constexpr unsigned kWatchNorm = 1024u;  // the wait for a row of a ring
+constexpr int kDrained = 2;             // of a block's abort flag: nothing is in flight any more
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 static_assert(BIL_MAX_NORM_WIDTH == kMaxRowThreads * kMaxGroups * kVec, "the widest row a block holds");
@@ -323,6 +327,17 @@ struct RowRing {
       at += slot;
     }
   }
+  // Where the wait for stage s (phase `parity`) gave up: the thread that fills waits (bounded) for the copies
+  // that may still be in flight, those of the `ahead` rows from this one on, once; no stage is filled after.
+  __device__ __forceinline__ void drain(int s, unsigned parity, int stages, int64_t ahead, volatile int* abort) {
+    if (*abort == kDrained) return;
+    for (int k = 0; k < stages && k < ahead; ++k) {
+      const int t = s + k < stages ? s + k : s + k - stages;
+      if (!thread_wait_watch(&full[t], s + k < stages ? parity : parity ^ 1u, abort, kWatchNorm, &g_watchdog_norm, false))
+        break;
+    }
+    *abort = kDrained;
+  }
 };
 
 enum NormMode { kNormPlain = 0, kNormQuant = 1, kQuantOnly = 2 };
@@ -379,7 +394,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   if (BULK) {
     // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
     // barriers still met by every thread, and fills no further stage.)
-    warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm);
+    if (!warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm) && threadIdx.x == 0)
+      ring.drain(stage, parity, p.stages, (p.n_rows - row + gridDim.x - 1) / gridDim.x, abort);
     x.base = ring_smem + static_cast<size_t>(stage) * ring.stage_bytes;
     res.base = x.base + ring.slot;
   }
@@ -552,7 +568,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
     if (BULK) {
       // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
       // barriers still met by every thread, and fills no further stage.)
-      warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm);
+      if (!warp_wait_watch(&full[stage], parity, abort, kWatchNorm, &g_watchdog_norm) && threadIdx.x == 0)
+        rows.drain(stage, parity, p.stages, row == part ? p.stages : p.stages - 1, abort);
       h.base = ring + static_cast<size_t>(stage) * rows.stage_bytes;
       dy.base = h.base + rows.slot;
       dh.base = h.base + 2 * rows.slot;
@@ -799,7 +816,7 @@ int launch_fwd(NormKernel kernel, NormParams& p, int path, int eb, cudaStream_t 
 }
 
 // Blocks of the backward: per_sm a multiprocessor, at most one a row (eight
-// rows a block where a warp takes a row): 768 threads an SM at up to 88
+// rows a block where a warp takes a row): 768 threads an SM at up to 80
 // registers, or 512 at 128 with four groups a lane; 1024 where a warp takes a row.
 int bwd_per_sm(int row_threads, int per_thread) {
   if (row_threads == kLanes) return 4;
