@@ -37,6 +37,7 @@
 #include "device_common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "layout.h"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -48,10 +49,13 @@
 
 namespace {
 
-constexpr int kVec = 8;             // elements of a group
-constexpr int kMaxGroups = 4;       // groups a thread holds
-constexpr int kMaxRowThreads = 512;
-constexpr int kMaxStages = 4;       // of the backward's ring
+using bil_layout::kMaxGroups;
+using bil_layout::kMaxRowThreads;
+using bil_layout::kMaxStages;
+using bil_layout::kVec;
+using bil_layout::row_shape;
+using bil_layout::slot_bytes;
+static_assert(bil_layout::kWarp == kLanes, "the layouts count in the same warps");
 
 __device__ unsigned int g_watchdog_norm;
 constexpr unsigned kWatchNorm = 1024u;  // the wait for a row of a ring
@@ -293,9 +297,6 @@ struct NormParams {
   float* dw_part;  // [parts, width]
   int stages;      // of the ring, where there is one
 };
-
-// Shared memory of a row that may start anywhere in a 16-byte unit.
-__host__ __device__ inline unsigned slot_bytes(int row_bytes) { return static_cast<unsigned>((row_bytes + 15 + 15) & ~15); }
 
 // A block's ring of stages, each the rows of up to three operands in slots of
 // their own, which one thread fills with bulk copies of the 16-byte aligned spans
@@ -703,16 +704,6 @@ bool rows_start_on(const void* p, int64_t n_rows, int64_t ld_bytes, size_t a) {
   return aligned_to(p, a) && (n_rows <= 1 || ld_bytes % static_cast<int64_t>(a) == 0);
 }
 
-// A row's threads and the groups each holds (rounded up to what is compiled), by
-// the width alone: as few warps as hold the row in `most` groups a lane (four in
-// the forward, two in the backward, whose rows past 8192 elements take four).
-void row_shape(int width, int most, int* threads, int* per_thread) {
-  const int groups = (width + kVec - 1) / kVec;
-  if (groups > kMaxRowThreads * most) most = kMaxGroups;
-  *threads = (groups + kLanes * most - 1) / (kLanes * most) * kLanes;
-  const int need = (groups + *threads - 1) / *threads;
-  *per_thread = need <= 1 ? 1 : need <= 2 ? 2 : 4;
-}
 constexpr int kFwdGroups = 4, kBwdGroups = 2;
 
 // Threads of a block: one row, or eight rows of one warp each.
@@ -746,7 +737,7 @@ NormKernel fwd_kernel(int dtype, int ng, int path) {
 template <int DT, int PATH>
 NormKernel bwd_kernel_ng(int ng, bool bulk) {
   if (bulk) return ng <= 2 ? norm_bwd_kernel<DT, 2, true, PATH> : norm_bwd_kernel<DT, 4, true, PATH>;
-  if constexpr (DT == BIL_F32)  // rows too wide for the ring (with dh, past 9472 elements)
+  if constexpr (DT == BIL_F32)  // rows too wide for the ring (past 9636 elements with dh, 14460 without)
     if (ng == 4) return norm_bwd_kernel<DT, 4, false, PATH>;
   return ng == 1 ? norm_bwd_kernel<DT, 1, false, PATH> : norm_bwd_kernel<DT, 2, false, PATH>;
 }
@@ -797,46 +788,25 @@ int launch_fwd(NormKernel kernel, NormParams& p, int path, int eb, cudaStream_t 
     if (grid > INT32_MAX) return BIL_E_UNSUPPORTED;
     return launch_pdl(kernel, grid, threads, 0, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
   }
-  // Through the ring: as many blocks as hold 1024 threads an SM, or 640 of float32 (at up to 64, 96 registers
-  // a thread) with two stages each; fewer blocks, then one stage, for the widest rows.
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  const size_t limit = bil_layout::dynamic_limit(smem_optin);
   const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (p.residual != nullptr ? 2 : 1);
-  int per_sm = std::max(1, std::min(32, (eb == 4 ? 640 : 1024) / p.row_threads));
-  for (;; --per_sm) {
-    const size_t room = static_cast<size_t>(228 * 1024) / per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
-    p.stages = static_cast<int>(std::min<size_t>(3, room / stage_bytes));
-    if (p.stages >= 2 || per_sm == 1) break;
-  }
+  int per_sm = 0;
+  bil_layout::fwd_ring(stage_bytes, p.row_threads, eb, limit, &per_sm, &p.stages);
   if (p.stages < 1) return BIL_E_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit)) != cudaSuccess)
     return BIL_E_CUDA;
   const int64_t grid = std::min<int64_t>(p.n_rows, static_cast<int64_t>(sms) * per_sm);
   return launch_pdl(kernel, grid, p.row_threads, stage_bytes * p.stages, s, 1, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
 // Blocks of the backward: per_sm a multiprocessor, at most one a row (eight
-// rows a block where a warp takes a row): 768 threads an SM at up to 80
-// registers, or 512 at 128 with four groups a lane; 1024 where a warp takes a row.
-int bwd_per_sm(int row_threads, int per_thread) {
-  if (row_threads == kLanes) return 4;
-  return std::max(1, (per_thread == 4 ? 512 : 768) / row_threads);
-}
+// rows a block where a warp takes a row).
 int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms, int per_sm) {
   const int64_t rows_per_block = block_threads(row_threads) / row_threads;
   return std::max<int64_t>(1, std::min<int64_t>((n_rows + rows_per_block - 1) / rows_per_block,
                                                 static_cast<int64_t>(sms) * per_sm));
-}
-
-// The ring of the backward: of up to *per_sm blocks an SM the most that leave each
-// three stages, or one block with two.  0 stages: the rows are too wide for that.
-void ring_shape(size_t stage_bytes, int* per_sm, int* stages) {
-  for (; *per_sm >= 1; --*per_sm) {
-    const size_t room = static_cast<size_t>(228 * 1024) / *per_sm - 1024 - 512;  // 1 KB reserved, the block's variables
-    *stages = static_cast<int>(std::min<size_t>(kMaxStages, room / stage_bytes));
-    if (*stages >= 3 || (*per_sm == 1 && *stages == 2)) return;
-  }
-  *stages = 0;
 }
 
 // The backward's partial sums, at most: one row of `width` a block.
@@ -845,7 +815,7 @@ int bwd_parts(int64_t n_rows, int64_t width, int64_t* parts) {
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   int threads = 0, ng = 0;
   row_shape(static_cast<int>(width), kBwdGroups, &threads, &ng);
-  *parts = bwd_blocks(n_rows, threads, sms, bwd_per_sm(threads, ng));
+  *parts = bwd_blocks(n_rows, threads, sms, bil_layout::bwd_per_sm(threads, ng));
   return BIL_OK;
 }
 
@@ -1032,13 +1002,14 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   row_shape(p.width, kBwdGroups, &p.row_threads, &ng);
   const int threads = block_threads(p.row_threads);
   // Rows of more than one warp come through the ring.
-  const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (dh != nullptr ? 3 : 2);
-  int per_sm = bwd_per_sm(p.row_threads, ng);
-  if (p.row_threads > kLanes) ring_shape(stage_bytes, &per_sm, &p.stages);
-  const bool bulk = p.stages != 0;
-  if (!bulk) per_sm = bwd_per_sm(p.row_threads, ng);
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
+  const size_t limit = bil_layout::dynamic_limit(smem_optin);
+  const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (dh != nullptr ? 3 : 2);
+  int per_sm = bil_layout::bwd_per_sm(p.row_threads, ng);
+  if (p.row_threads > kLanes) bil_layout::bwd_ring(stage_bytes, limit, &per_sm, &p.stages);
+  const bool bulk = p.stages != 0;
+  if (!bulk) per_sm = bil_layout::bwd_per_sm(p.row_threads, ng);
   const int64_t grid = bwd_blocks(n_rows, p.row_threads, sms, per_sm);
   parts = grid;
   const bool full = rows_start_on(h, n_rows, ld_h * eb, 16) && rows_start_on(dy, n_rows, ld_dy * eb, 16) && p.vec_dx &&
@@ -1050,7 +1021,7 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   const size_t smem = bulk                            ? stage_bytes * p.stages
                       : threads == p.row_threads ? 0  // the warps' sums
                                                  : static_cast<size_t>(threads / kLanes) * p.groups * kVec * sizeof(float);
-  if (bulk && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) !=
+  if (bulk && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit)) !=
                       cudaSuccess)
     return BIL_E_CUDA;
   if (launch_pdl(kernel, grid, threads, smem, s, 1, p) != cudaSuccess) return BIL_E_CUDA;
