@@ -79,4 +79,22 @@ inline void bwd_ring(size_t stage_bytes, size_t limit, int* per_sm, int* stages)
   *stages = 0;
 }
 
+// ---- the pass over the logits of the forward with the alternatives ----
+
+constexpr int kTopkMaxWarps = 8;  // of a block
+constexpr size_t kTopkStatics = 128;
+
+// Warps of a block and blocks of an SM.  One stage a warp: its copy is on the way
+// while the tile before it is reduced from registers (or, past 8 KB, while the
+// other warps reduce theirs), and 16 warps (at up to 128 registers a thread) have
+// 128 KB of stages.  (Measured at 16384 x 151936 bf16: two stages for 14 warps
+// 843 us, one for 16 warps 792 us: the reduction's latencies want the warps.)
+// Two blocks an SM where that leaves them four warps each or more, else one.
+inline void topk_stream(size_t stage_bytes, size_t limit, int* warps, int* blocks) {
+  for (*blocks = 2; *blocks >= 1; --*blocks) {
+    *warps = static_cast<int>(std::min<size_t>(kTopkMaxWarps, dynamic_room(*blocks, kTopkStatics, limit) / stage_bytes));
+    if (*blocks == 1 || *warps >= 4) return;
+  }
+}
+
 }  // namespace bil_layout

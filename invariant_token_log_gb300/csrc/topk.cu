@@ -44,13 +44,14 @@
 #include "device_common.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "layout.h"
 #include "logp_device.cuh"
 
 #include <algorithm>
 
 namespace {
 
-constexpr int kTopkMaxWarps = 8;  // warps of a block of the stream kernel
+using bil_layout::kTopkMaxWarps;
 constexpr int kChunk = 64;        // columns of a chunk
 
 typedef unsigned long long u64;
@@ -1217,22 +1218,6 @@ __global__ void __launch_bounds__(BIL_MAX_TOPK + kLanes) topk_grad_fix_kernel(co
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// How the stream kernel is laid out: warps of a block, blocks of an SM.  One
-// stage a warp: its copy is on the way while the tile before it is reduced from
-// registers (or, past 8 KB, while the other warps reduce theirs), and 16 warps
-// (at up to 128 registers a thread) have 128 KB of stages.  (Measured at 16384 x
-// 151936 bf16: two stages for 14 warps 843 us, one for 16 warps 792 us: the
-// reduction's latencies want the warps.)  Two blocks an SM where that leaves
-// them four warps each or more, else one.
-constexpr size_t kSmSmemBytes = 228 * 1024;  // an SM's shared memory, 1 KB of it reserved for each block
-void stream_layout(size_t stage_bytes, int* warps, int* blocks) {
-  for (*blocks = 2; *blocks >= 1; --*blocks) {
-    const size_t room = kSmSmemBytes / *blocks - 1024 - 128;  // 128: the barriers
-    *warps = static_cast<int>(std::min<size_t>(kTopkMaxWarps, room / stage_bytes));
-    if (*blocks == 1 || *warps >= 4) return;
-  }
-}
-
 // Tiles of a unit: the cut of the rows that gives the least time, a warp's time
 // being its units' tiles and a quarter of a tile a unit for the change of row.
 int unit_tiles(int64_t n_rows, int num_tiles, int64_t warps) {
@@ -1306,8 +1291,10 @@ int launch_topk_t(TopkParams p, const TopkOut& out, cudaStream_t stream) {
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   p.stage_bytes =
       static_cast<unsigned>(align_up(static_cast<size_t>(p.tile_v) * Elem<DT>::kBytes + (ALIGNED ? 0 : 16), 128));
+  const size_t limit = bil_layout::dynamic_limit(smem_optin);
   int warps = 0, blocks = 0;
-  stream_layout(p.stage_bytes, &warps, &blocks);
+  bil_layout::topk_stream(p.stage_bytes, limit, &warps, &blocks);
+  if (warps < 1) return BIL_E_UNSUPPORTED;
   const int64_t slots = static_cast<int64_t>(sms) * blocks;
   p.unit_tiles = unit_tiles(p.n_rows, p.num_tiles, slots * warps);
   p.units = (p.num_tiles + p.unit_tiles - 1) / p.unit_tiles;
@@ -1316,12 +1303,10 @@ int launch_topk_t(TopkParams p, const TopkOut& out, cudaStream_t stream) {
   warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(warps, (units + slots - 1) / slots)));
   const int64_t grid = std::min<int64_t>(slots, (units + warps - 1) / warps);
   const size_t smem = static_cast<size_t>(warps) * p.stage_bytes;
-  if (smem > static_cast<size_t>(smem_optin) - 1024) return BIL_E_UNSUPPORTED;
   auto kernel = topk_stream_kernel<DT, ALIGNED, ENT>;
-  // past what needs no opt-in (48 KB with the kernel's own variables); always to the same limit, so that host
-  // threads do not undo each other's
+  // past what needs no opt-in (48 KB with the kernel's own variables)
   if (smem > 47 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin - 1024) != cudaSuccess)
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit)) != cudaSuccess)
     return BIL_E_CUDA;
   if (launch_pdl(kernel, grid, warps * kLanes, smem, stream, 1, p) != cudaSuccess) return BIL_E_CUDA;
   // One warp a row from four rows an SM on.

@@ -79,3 +79,24 @@ def test_norm_rings_fit(tmp_path):
     assert out.returncode == 0, out.stdout
     # where float32 rows leave the backward's ring, without and with dh: four slots of two stages, six of two
     assert out.stdout.split() == ["widest", "14460", "9636"]
+
+
+TOPK = HEAD + r"""
+int main() {
+  for (int eb = 2; eb <= 4; eb += 2)
+    for (int tile = 8; tile * eb <= 64 * 1024; tile += 8)
+      for (int pad = 0; pad <= 16; pad += 16) {  // rows off 16-byte boundaries
+        const size_t stage = (size_t(tile) * eb + pad + 127) / 128 * 128;
+        int warps = 0, blocks = 0;
+        topk_stream(stage, dynamic_limit(kOptin), &warps, &blocks);
+        if (warps < 1 || warps > kTopkMaxWarps || blocks < 1) ++bad, printf("no warps at tile %d\n", tile);
+        check("pass", tile, 10 * eb + pad / 16, blocks, kTopkStatics, warps, stage);
+      }
+  return bad != 0;
+}
+"""
+
+
+def test_topk_stages_fit(tmp_path):
+    out = run(tmp_path, TOPK)
+    assert out.returncode == 0, out.stdout
