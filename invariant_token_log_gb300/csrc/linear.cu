@@ -762,21 +762,30 @@ __device__ __forceinline__ int epi8(int warp) { return warp % 4 + 4 * ((warp - 2
 __device__ __forceinline__ void quarter_sync(int q) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + q), "n"(2 * kLanes) : "memory");
 }
+// The same, and whether both have the tile's accumulator (`ok`: this warp's wait for it did not run out).  The
+// warps leave their loops by this answer alone, which is the same for both, so that neither is left waiting
+// for the other; a second quarter_sync has to follow before the next tile's answer.
+__device__ __forceinline__ bool quarter_ok(Exchange8& x, int e, int lane, bool ok) {
+  const int q = e % 4;
+  if (lane == 0) x.ok[e] = ok ? 1 : 0;
+  quarter_sync(q);
+  return x.ok[q] != 0 && x.ok[q + 4] != 0;
+}
 
 // The 8-bit forward's epilogue of column tile n for warp e (of eight: quarter e
 // % 4 of the tile's rows, half e / 4 of its columns): row `row` (of the lane) of
 // the accumulator at `taddr` (the tile's first column).  `wait` waits for the
 // accumulator, `release` (one lane) hands it back.  False: a wait ran out, of
-// this warp or of the quarter's other (which says so at the first barrier, so
-// that neither is left waiting at one).
+// this warp or of the quarter's other.
 template <bool ENT, typename Wait, typename Release>
 __device__ __forceinline__ bool epilogue8(const LinearParams& p, const CUtensorMap& tmap_out, uint32_t taddr,
                                           unsigned char* staging, Exchange8& x, int e, int64_t row, int n, int lane,
                                           uint32_t& store_boxes, Wait wait, Release release) {
   const int q = e % 4, half = e / 4;
   if (row - lane >= p.n_rows) {  // no row of the quarter exists (the other warp finds the same)
-    if (!wait()) return false;
+    if (!quarter_ok(x, e, lane, wait())) return false;
     if (lane == 0) release();
+    quarter_sync(q);
     return true;
   }
   const bool valid = row < p.n_rows;
@@ -814,9 +823,7 @@ __device__ __forceinline__ bool epilogue8(const LinearParams& p, const CUtensorM
     }
   }
   x.max[e][lane] = mx;
-  if (lane == 0) x.ok[e] = ok ? 1 : 0;
-  quarter_sync(q);
-  if (x.ok[q] == 0 || x.ok[q + 4] == 0) return false;
+  if (!quarter_ok(x, e, lane, ok)) return false;
   mx = fmaxf(mx, x.max[e ^ 4][lane]);
   const float c = __fmul_rn(__fmul_rn(sh, p.rcp), kLog2e);
   const float shift = __fmul_rn(mx == -INFINITY ? 0.0f : mx, c);
