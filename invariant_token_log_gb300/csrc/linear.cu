@@ -1392,13 +1392,22 @@ __global__ void __launch_bounds__(kThreads8, 1)
       }
       // The leader waits (bounded, whatever happened) for the pair's copies still in flight; the other block
       // waits for the leader at the end.
+      const int64_t last = it > kRing ? it - kRing : 0;  // the ring's last fills
       if (rank == 0) {
-        for (int64_t i = it > kRing ? it - kRing : 0; i < it; ++i) {
+        for (int64_t i = last; i < it; ++i) {
           if (!thread_wait_watch(&sm.full[i % kRing], static_cast<unsigned>((i / kRing) & 1), abort,
                                  kWatchOwnDrain, &g_watchdog_linear, false))
             break;
         }
       }
+      // The leader's commits arrive in this block's shared memory: it stays until the last of them are there,
+      // `empty` of the ring's last fills and mma_done (the epilogue waits for every acc_full).
+      for (int64_t i = last; i < it; ++i) {
+        if (!thread_wait_watch(&sm.empty[i % kRing], static_cast<unsigned>((i / kRing) & 1), abort, kWatchOwnDrain,
+                               &g_watchdog_linear, false))
+          break;
+      }
+      if (rank != 0) thread_wait_watch(&sm.mma_done, 0u, abort, kWatchOwnDrain, &g_watchdog_linear, false);
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -1430,7 +1439,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
         if (!ok) break;
         umma_commit_pair(&sm.acc_full[b]);
       }
-      // Every MMA this thread issued completes before the blocks free tensor memory.
+      // Every MMA this thread issued completes before the blocks free tensor memory (the other block's copy
+      // thread waits for its own arrival of this).
       umma_commit_pair(&sm.mma_done);
       thread_wait_watch(&sm.mma_done, 0u, abort, kWatchOwnDrain, &g_watchdog_linear, false);
     }
