@@ -406,7 +406,7 @@ const char* bil_contract_id(void) {
          ";linear=z=fp32 tcgen05 sum over K blocks of 64 in order; tile 256, one thread per row,"
          " 8 slots over columns 8g+j, g in order, ((a0+a1)+(a2+a3))+((a4+a5)+(a6+a7))"
          ";linear8=z=(acc*rn sw)*rn sh, acc fp32 tcgen05 sum over K blocks of 128 in order; v=acc*rn sw;"
-         " m_t=(max v*rn sh)*rn rcp; t=fma(v,c,-(max v*rn c)), c=(sh*rn rcp)*rn log2e; slots as linear over each 128 columns, added"
+         " m_t=(max v*rn sh)*rn rcp; t=(v-rn max v)*rn c, c=(sh*rn rcp)*rn log2e; slots as linear over each 128 columns, added"
          ";topk=columns by (x desc, -0=+0, column asc), NaN last; logp=x*rn rcp-rn LSE;"
          " bwd named columns d=fma(-G,p,W)[-rn gh*(p*(max(a,-FLT_MAX)+H))][*rcp]"
          ";norm=h=rn_T(x+rn r); thread r of TPR: groups of 8 r, r+TPR, ... in order, fma;"

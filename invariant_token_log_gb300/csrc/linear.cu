@@ -521,8 +521,11 @@ __device__ __forceinline__ void row_partial(uint32_t taddr, int vcols, float rcp
 // (sw: the column's scale, sh >= 0: the row's); the partial takes the row's
 // scale out of the maximum and into the exponent's constant:
 //   mx = max over valid c of v_c (exact);  m = (mx *rn sh) *rn rcp
-//   t_c = fma(v_c, c, -(mx *rn c)),  c = (sh *rn rcp) *rn log2e
-// with e_c = 2^t_c, summed over each half of 128 columns in eight slots and by the
+//   t_c = (v_c -rn mx) *rn c,  c = (sh *rn rcp) *rn log2e
+// so that the maximum's own term is 1 whatever its size, and m, rounded as the
+// logit is, its logit: a product fma(v_c, c, -(mx *rn c)), an instruction less a
+// pair, would put the rounding of mx c, which m does not have, into every term.
+// With e_c = 2^t_c, summed over each half of 128 columns in eight slots and by the
 // tree of row_partial, the two halves' sums added; the entropy sum alike (no
 // clamp: an accumulator is never infinite); the target logit is (v_t *rn sh) *rn
 // rcp.  A thread has one half; `sw` is its warp's copy of the half's column
@@ -613,18 +616,18 @@ struct HalfRow {
     });
     return mx;
   }
-  // the half's sums for t = fma(v, c, -shift)
+  // the half's sums for t = (v - shift) c
   template <bool ENT>
   __device__ __forceinline__ void sums(float c, float shift, float& sum, float& ent) {
     uint64_t a2[4] = {0, 0, 0, 0}, u2[4] = {0, 0, 0, 0};
-    const uint64_t c2 = pk(c, c), shift2 = pk(-shift, -shift);
+    const uint64_t c2 = pk(c, c), shift2 = pk(shift, shift);
     chunks([&](uint32_t (&r)[kChunk], int c0) {
 #pragma unroll
       for (int k = 0; k < kChunk; k += 4) {
         const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(sw + c0 + k);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint64_t t = fma2(mul2(pair(r, k + 2 * h), h == 0 ? w.x : w.y), c2, shift2);
+          const uint64_t t = mul2(sub2(mul2(pair(r, k + 2 * h), h == 0 ? w.x : w.y), shift2), c2);
           float e0 = ex2_approx(lo_of(t)), e1 = ex2_approx(hi_of(t));
           if (!FULL) {  // columns past the vocabulary add nothing
             if (c0 + k + 2 * h >= vcols) e0 = 0.0f;
@@ -826,7 +829,7 @@ __device__ __forceinline__ bool epilogue8(const LinearParams& p, const CUtensorM
   if (!quarter_ok(x, e, lane, ok)) return false;
   mx = fmaxf(mx, x.max[e ^ 4][lane]);
   const float c = __fmul_rn(__fmul_rn(sh, p.rcp), kLog2e);
-  const float shift = __fmul_rn(mx == -INFINITY ? 0.0f : mx, c);
+  const float shift = mx == -INFINITY ? 0.0f : mx;
   float sum, ent = 0.0f;
   if (vcols == kHalfCols) {
     HalfRow<true> h;
