@@ -328,6 +328,22 @@ def logp_bwd(logits: torch.Tensor, target_ids: torch.Tensor, lse: torch.Tensor, 
     return out.reshape(logits.shape) if out.numel() == logits.numel() else out
 
 
+class _FirstDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad, *sources):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the kernels have no second derivative")
+
+
+def _first_derivative(grad: torch.Tensor, *sources: torch.Tensor | None) -> torch.Tensor:
+    """A gradient the kernels computed from `sources`.  Under create_graph it is tied to them, so that
+    differentiating it is an error rather than the derivative of a constant."""
+    return _FirstDerivative.apply(grad, *sources) if torch.is_grad_enabled() else grad
+
+
 class BatchInvariantLogp(torch.autograd.Function):
     """logp = BatchInvariantLogp.apply(logits, target_ids, ignore_index, tile_v, validate, temperature)
 

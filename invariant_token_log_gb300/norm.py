@@ -22,6 +22,7 @@ from .logp import (
     _DEVICE_OBJECTS,
     _code,
     _device_object,
+    _first_derivative,
     _get_device,
     _need_cuda,
     _on_device,
@@ -213,7 +214,7 @@ class RMSNorm(torch.autograd.Function):
         h, weight, rstd = ctx.saved_tensors
         if grad_y is None:  # only the stream was used: it passes through
             return grad_h, None, grad_h, None
-        dx, dw = rms_norm_bwd(grad_y, h, weight, rstd, grad_h)
+        dx, dw = (_first_derivative(d, grad_y, h, weight) for d in rms_norm_bwd(grad_y, h, weight, rstd, grad_h))
         return dx, dw.to(weight.dtype), dx if ctx.needs_input_grad[2] else None, None
 
 

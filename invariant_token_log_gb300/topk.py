@@ -20,6 +20,7 @@ from .logp import (
     _code,
     _device_object,
     _f32_1d,
+    _first_derivative,
     _get_device,
     _need_cuda,
     _on_device,
@@ -182,7 +183,7 @@ class BatchInvariantLogpTopk(torch.autograd.Function):
         d = logp_topk_bwd(logits, target_ids, ids, lse, grad_logp, grad_top, ctx.ignore_index,
                           temperature=ctx.temperature, entropy=None if grad_ent is None else ent,
                           grad_entropy=grad_ent)
-        return d, None, None, None, None, None, None
+        return _first_derivative(d, logits), None, None, None, None, None, None
 
 
 def batch_invariant_logp_topk(logits: torch.Tensor, target_ids: torch.Tensor, k: int,
