@@ -43,8 +43,8 @@
 //                            tcgen05.mma kind::f8f6f4 over 128-element K
 //                            blocks (the same 128-byte lines), the partial
 //                            of the accumulator scaled by row and column.
-// For more than 128 rows of more than 1024 elements that forward has a kernel of
-// its own on pairs of blocks, linear_partials8_pair_kernel.
+// For more than 128 rows that are long enough that forward has a kernel of its own
+// on pairs of blocks, linear_partials8_pair_kernel.
 //
 // What fixes the bits of z[r, c] is the K order (K blocks in order, four
 // K=16 steps each, from a zeroed accumulator), the same for every row and
@@ -2038,17 +2038,23 @@ int bil_linear_logp_fp8_fwd(const void* hidden, const float* hidden_scale, const
   if (validate) {
     if (int st = bil_internal::check_targets_host(target_ids, n_rows, ignore_index, vocab, s)) return st;
   }
-  // Pairs of blocks where K is long enough for the copies to bound one block's kernel, and where their rounds of
-  // 256-row units, at 7/8 of the time of a round of 128-row tiles, come to less.  Pairs against single blocks, us:
-  // 4096 x 151936 x 4096 1398 and 1455, 2048 x 38912 x 4096 194 and 211, x 2048 113 and 119, x 1024 98 and 94 (the
-  // epilogue bounds both), 4096 x 152064 x 1024 593 and 580, 384 x 128256 x 4096 (more rounds) 200 and 179.  A
-  // batch of fewer rows than a tile goes in a box of exactly its rows, as in bil_linear_logp_partials.
+  // Pairs of blocks where the copies bound one block's kernel (below that the epilogue bounds both), and where their
+  // rounds of 256-row units, at 7/8 of the time of a round of 128-row tiles, come to less.  The copies' time goes with
+  // K, and rows that do not lie on 128-byte lines, each line of a box then two of memory, take half as long again.
+  // Pairs against single blocks, us, kernels alone: on lines, K = 1024: 512 x 32003 42.1 and 40.0, 2048 x 38912 97.4
+  // and 93.3, 4096 x 151936 596 and 579; 1792: 46.2 and 46.2, 110 and 107, 689 and 675; 1920: 48.3 and 48.2, 112 and
+  // 112; 2048: 48.3 and 48.2, 113 and 118, 740 and 759; 4096: 69 and 75, 195 and 208, 1398 and 1455.  Off lines, 784:
+  // 43 and 41, 97 and 93, 592 and 583; 1104: 45 and 42 (four rounds of tiles: the start of a pair weighs more), 106
+  // and 110, 684 and 759; 1296: 46 and 46, 114 and 124, 717 and 831; 2064: 52 and 59, 143 and 175, 979 and 1232.  More
+  // rounds: 384 x 128256 x 4096 202 and 179.  A batch of fewer rows than a tile goes in a box of exactly its rows, as
+  // in bil_linear_logp_partials.
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   if (static_cast<size_t>(smem_optin) < kSmemBytes8) return BIL_E_UNSUPPORTED;
   const int64_t tiles = (n_rows + kBM - 1) / kBM * num_tiles, units = (n_rows + 2 * kBM - 1) / (2 * kBM) * num_tiles;
-  const bool pair =
-      n_rows > kBM && hidden_size > 1024 && 7 * ((units + sms / 2 - 1) / (sms / 2)) < 8 * ((tiles + sms - 1) / sms);
+  const bool lines = aligned_to(hidden, 128) && aligned_to(weight, 128) && ld_hidden % 128 == 0 && ld_weight % 128 == 0;
+  const bool pair = n_rows > kBM && hidden_size > (lines ? 1792 : 1024) &&
+                    7 * ((units + sms / 2 - 1) / (sms / 2)) < 8 * ((tiles + sms - 1) / sms);
   const int a_rows = static_cast<int>(n_rows < kBM ? n_rows : kBM);
   CUtensorMap mh, mw;
   if (int st = make_map8(&mh, hidden, n_rows, hidden_size, ld_hidden, a_rows)) return st;
