@@ -265,6 +265,9 @@ int bil_logp_topk_fwd(const void *logits, int dtype, int64_t n_rows, int64_t voc
  *  top_ids       [n_rows, k] int64: the forward's, or any other columns whose
  *                log-probabilities were taken against the same lse.
  *  grad_top      [n_rows, k] float32: gk.
+ *  dlogits       as for bil_logp_bwd; it must not overlap the logits, which are
+ *                read again after it is written (BIL_E_INVALID_ARG where it is
+ *                their buffer).
  *  workspace     [n_rows] float32 device scratch (receives G).
  * Other arguments as for bil_logp_bwd (ignored rows are +0.0, rows whose target
  * is outside the vocabulary NaN).

@@ -1448,6 +1448,7 @@ int bil_logp_topk_bwd(const void* logits, int dtype, int64_t n_rows, int64_t voc
       !aligned_to(dlogits, static_cast<size_t>(ob)) || !aligned_to(workspace, 4) ||
       (entropy && !aligned_to(entropy, 4)) || (grad_entropy && !aligned_to(grad_entropy, 4)))
     return BIL_E_ALIGN;
+  if (dlogits == logits) return BIL_E_INVALID_ARG;  // the named columns' logits are read after the full pass
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   topk_grad_sum_kernel<<<static_cast<unsigned>((n_rows + 7) / 8), 256, 0, s>>>(grad_logp, grad_top, k, n_rows,
                                                                               workspace);

@@ -117,7 +117,8 @@ def logp_topk_bwd(logits: torch.Tensor, target_ids: torch.Tensor, top_ids: torch
     """dlogits of g * logp + sum_j gk_j * top_logp_j (+ gh * entropy) from the saved LSE (and entropy).
 
     ``top_ids`` and ``grad_top`` [*lead, k]: the forward's columns, or any others, and
-    the gradients of their log-probabilities.  Other arguments as for ``logp_bwd``."""
+    the gradients of their log-probabilities.  ``out`` must not be the logits.  Other
+    arguments as for ``logp_bwd``."""
     _need_cuda(logits, target_ids, top_ids, lse, grad_logp, grad_top, out, entropy, grad_entropy)
     if (entropy is None) != (grad_entropy is None):
         raise ValueError("entropy and grad_entropy go together")
