@@ -29,7 +29,7 @@ def score(x, residual, norm_weight, weight_q, weight_scale, targets, k=20, eps=1
     rows as ``quantize_rows`` gives them, once per weight.  ``rows`` at a time, so
     that rows x vocabulary float32 logits are all that is kept of the head."""
     parts = []
-    for i in range(0, x.shape[0], rows):
+    for i in range(0, max(x.shape[0], 1), rows):  # no rows are one empty part
         s = slice(i, i + rows)
         q, scale, stream = bil.rms_norm_quant(x[s], norm_weight, residual=residual[s], eps=eps)
         logp, _, entropy, logits = bil.linear_logp_fp8(q, scale, weight_q, weight_scale, targets[s],
