@@ -8,6 +8,15 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 
+@pytest.fixture(autouse=True)
+def _no_wait_ran_out(request):
+    """After every GPU test: no kernel's bounded wait ran out in it (a kernel goes on with what is there)."""
+    yield
+    if "gpu" in request.keywords:
+        from gpu_helpers import check_watchdog
+        check_watchdog()
+
+
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (runs the CUDA library)")
     config.addinivalue_line("markers", "slow: long-running CPU test")
