@@ -631,7 +631,9 @@ int bil_linear_logp_fwd_static(const void *hidden, const void *weight, int dtype
  * accumulator, 64 the copy thread's wait for a free stage, 128 the MMA
  * thread's wait for a stage or a free accumulator, 256 a wait of either for
  * its own copies or MMAs to finish.  512: bil_watchdog_selftest.
- * bil_logp_topk_fwd: 1 and 8.  bil_rms_norm_bwd: 1024, its wait for a row.
+ * bil_logp_topk_fwd: 1 and 8.  bil_rms_norm_bwd, and bil_rms_norm_fwd,
+ * bil_rms_norm_quant and bil_quantize_rows of rows that are no multiple of 8
+ * elements or start off 16-byte boundaries: 1024, the wait for a row.
  */
 int bil_watchdog_status(unsigned int *flags, int clear);
 

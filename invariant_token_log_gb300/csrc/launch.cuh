@@ -13,9 +13,9 @@ namespace {
 // behind that kernel's tail).  Only kernels that wait for their predecessor
 // with griddep_wait() before touching global memory are launched this way:
 // the forward's stream, cluster and merge kernels, the forward kernels of
-// topk.cu, the norm's kernels and the 8-bit LM head.  (The logits path's backward is not: the wait made its
-// element-by-element loads twice as slow.)  cluster > 1:
-// thread-block clusters of that many blocks along x.
+// topk.cu, the norm's kernels and the 8-bit LM head.  (The logits path's
+// backward is not: the wait made its element-by-element loads twice as slow.)
+// cluster > 1: thread-block clusters of that many blocks along x.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), int64_t grid, int block, size_t smem, cudaStream_t stream,
                        int cluster, Args&&... args) {

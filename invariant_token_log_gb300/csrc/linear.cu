@@ -1263,8 +1263,9 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmap_hidden, const 
 // 128 takes 32 KB of copies a block instead of 48 KB, and the ring has six stages
 // instead of four: e4m3's MMAs take a stage in 512 cycles, and with one block a
 // tile the copies' latency showed (tensor pipe 79% active at 2048 x 38912 x 4096;
-// with pairs 88%, 175 us = 3.73 PFLOP/s under a profiler at 1.70 GHz).  4096 x
-// 151936 x 4096: 1.40 ms = 3.65 PFLOP/s in short runs, 1.58 ms at the power cap.
+// with pairs 87%, 182 us = 3.59 PFLOP/s under a profiler at 1.66 GHz).  4096 x
+// 151936 x 4096: 1.36 ms = 3.76 PFLOP/s in short runs, 1.57 to 1.61 ms at the power
+// cap.
 //
 // Both blocks' copies count on the leader's (rank 0's) `full` barrier, which the
 // leader arms for the bytes of both; its MMA thread's commits arrive at both

@@ -20,16 +20,19 @@
 //
 // Bound: HBM.  Every element is read once and written once.  16384 x 4096 bf16 (a
 // plain copy's rate would be 6.8 TB/s): the forward with a residual 537 MB, 78 us,
-// 6.85 TB/s; to 8 bits 470 MB, 70 us, 6.7 TB/s; the backward with dh 537 MB, 88 us,
-// 6.1 TB/s, 8 us of it the weight's sums over the blocks.  Rows off 16-byte
-// boundaries (16384 x 4097): 95, 115 and 168 us.  A row is held between its
+// 6.85 TB/s; to 8 bits 470 MB, 70 us, 6.7 TB/s; the backward with dh 537 MB, 87 us,
+// 6.2 TB/s, 8 us of it the weight's sums over the blocks (norm_dw_kernel: a block for
+// every 32 columns, too few for the SMs; it weighs most on narrow rows: 16384 x 1024
+// 33 us, 0.59 of the copy's rate, 65536 x 512 55 us, 0.72).  Rows off 16-byte
+// boundaries (16384 x 4097): 97, 119 and 171 us.  A row is held between its
 // reduction and its output: thread r of the row's TPR threads has the 8-element
 // groups r, r + TPR, ... (at most 4).  TPR and the sums' order follow from the
 // width alone, so a row's bits do not depend on the batch.  The forward keeps
 // the row in registers, packed, four groups a lane: as many bytes in flight for
 // as few registers and barriers as can be.  The backward, whose registers hold
 // the weight's sums, has two groups a lane and streams its rows through shared
-// memory with bulk copies, a few rows ahead.  A row that does not start on a
+// memory with bulk copies, a few rows ahead (but for rows of one warp, and float32
+// rows of which not two stages fit).  A row that does not start on a
 // 16-byte boundary is read by the 16-byte units that hold its elements, shifted
 // into place.
 
@@ -737,7 +740,9 @@ NormKernel fwd_kernel(int dtype, int ng, int path) {
 template <int DT, int PATH>
 NormKernel bwd_kernel_ng(int ng, bool bulk) {
   if (bulk) return ng <= 2 ? norm_bwd_kernel<DT, 2, true, PATH> : norm_bwd_kernel<DT, 4, true, PATH>;
-  if constexpr (DT == BIL_F32)  // rows too wide for the ring (past 9636 elements with dh, 14460 without)
+  // Rows too wide for the ring (past 9636 elements with dh, 14460 without) in registers, which do not hold them:
+  // 472 bytes a thread are spilled, 1028 where rows lie anywhere.  4096 x 16000 with dh 293 us, 0.53 of a copy's rate.
+  if constexpr (DT == BIL_F32)
     if (ng == 4) return norm_bwd_kernel<DT, 4, false, PATH>;
   return ng == 1 ? norm_bwd_kernel<DT, 1, false, PATH> : norm_bwd_kernel<DT, 2, false, PATH>;
 }

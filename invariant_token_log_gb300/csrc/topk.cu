@@ -30,11 +30,13 @@
 // Up to 48 rows of a 16-bit type take one kernel that does both, a cluster of
 // blocks a row (topk_cluster_kernel).
 //
-// Bound: HBM, one read of the logits.  4096 x 151936 bf16, k = 20: 204 us, 6.1 TB/s
-// (0.90 of a plain copy's rate), 184 us of it the copy's floor and 10 us the row
-// kernel's; with the entropy 242 us (the streaming kernel's instructions then
-// count as much as its bytes); float32 406 us, 6.1 TB/s.  One row: 7 us, the
-// latency of the launch, of one tile and of the choice.
+// Bound: HBM, one read of the logits.  4096 x 151936 bf16, k = 20, no row ignored:
+// 212 us, 5.9 TB/s (0.86 of a plain copy's rate, whose time would be 183 us); with
+// the entropy 214 us, where the forward without alternatives takes 196: the choice
+// of columns adds 9%.  Rows 151939 apart 234 and 268 us.  float32 405 us, 6.1 TB/s
+// (0.91).  4096 x 32000 60 us, 0.65: the row kernel's time is per row and weighs more
+// on short ones.  One row: 7 us, the latency of the launch, of one tile and of the
+// choice.
 //
 //   topk_grad_sum_kernel  g + sum_j gk_j, what the softmax term is scaled by;
 //   (bil_logp_bwd)        d = -(g + sum gk) p - gh p (a + H), one pass;
@@ -356,8 +358,8 @@ __device__ __forceinline__ float regs_max(const TileRegs<DT>& t, int valid, int 
 // the lane's groups it is the last too): Group::sum_acc with nothing added for
 // the columns that are not there.  As -inf, which they are in the maximum, they
 // would make the entropy sum 0 * inf, and the tile would be summed again with
-// the clamp (4096 x 32003 bf16: a row's last tile of eight, and 114 us where
-// whole groups take 71).
+// the clamp (4096 x 32003 bf16, a row's last tile of eight: 114 us, and 85 so; 4096
+// x 32000, whose last group is whole, 65).
 template <int DT, bool ENT>
 __device__ __forceinline__ void sum_tail(uint64_t (&a)[4], uint64_t (&u)[4], const uint32_t (&w)[Group<DT>::kW], int valid,
                                          int lane, uint64_t shift2, uint64_t c2) {
