@@ -571,6 +571,136 @@ int bil_rms_norm_bwd(const void *dy, const void *h, const void *weight, const fl
                      bil_stream_t stream);
 
 /*
+ * bil_layer_norm_fwd -- layer norm of a stream, with dropout of x and the
+ * residual's addition.  With f_c = 0 for a dropped element and 65536 / (65536 -
+ * border) for the others (f = 1 without dropout), border = p_drop * 65536
+ * rounded to nearest even:
+ *     h    = x f + residual, rounded to dtype   (neither: h = x)
+ *     mean = mean_c h_c,   rstd = 1 / sqrt(mean_c (h_c - mean)^2 + eps)
+ *     y    = (h - mean) * rstd * weight + bias, rounded once
+ * in float32 between the loads and the stores; the squares are of the centred
+ * row.  A row's bits do not depend on the other rows, but for its mask, which is
+ * a function of the seed, the step and the row's number (bil_dropout).
+ *
+ *  x, residual   [n_rows, ld_x], [n_rows, ld_residual] of dtype; residual NULL:
+ *                none.
+ *  weight, bias  [width] of weight_dtype, dtype or BIL_F32, 16-byte aligned;
+ *                bias NULL: none.
+ *  width         1 to BIL_MAX_NORM_WIDTH.
+ *  eps           >= 0, finite.
+ *  p_drop        0: no dropout; else as for bil_dropout, with seed, step and rng.
+ *  y             [n_rows, ld_y] of dtype.
+ *  h             [n_rows, ld_h] of dtype: with a residual or dropout; otherwise
+ *                NULL.  (y or h may be x's or the residual's own buffer, one of
+ *                them each.)
+ *  mean, rstd    [n_rows] float32 for bil_layer_norm_bwd; NULL: not stored.
+ */
+int bil_layer_norm_fwd(const void *x, const void *residual, const void *weight, const void *bias, int dtype,
+                       int weight_dtype, int64_t n_rows, int64_t width, int64_t ld_x, int64_t ld_residual, float eps,
+                       double p_drop, uint64_t seed, uint64_t step, const int64_t *rng, void *y, int64_t ld_y, void *h,
+                       int64_t ld_h, float *mean, float *rstd, bil_stream_t stream);
+
+/*
+ * bil_layer_norm_bwd_workspace_bytes -- bytes of device workspace that
+ * bil_layer_norm_bwd needs on the current device for n_rows rows of `width`,
+ * with the bias's gradient (need_bias) or without.
+ */
+int bil_layer_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int need_bias, int64_t *bytes);
+
+/*
+ * bil_layer_norm_bwd -- backward of bil_layer_norm_fwd.  With u = (h - mean) *
+ * rstd and v = dy * weight:
+ *     d  = rstd * (v - mean_c v - u * mean_c(v u)) + dh
+ *     dresidual = d,   dx = d f     (f as in the forward; without dropout dx = d)
+ *     dweight = sum over rows of dy * u,   dbias = sum over rows of dy
+ * dx's and dresidual's bits depend on the row alone; dweight's and dbias's are
+ * reproducible for a given n_rows on a given GPU (fixed order, no atomics).
+ *
+ *  dy            [n_rows, ld_dy] of dtype: the gradient of y.
+ *  h             [n_rows, ld_h]: the forward's h (x where there was none).
+ *  mean, rstd    [n_rows]: the forward's.
+ *  dh            NULL, or [n_rows, ld_dh] of dtype: the gradient of h as an
+ *                output of its own (the residual stream going on).
+ *  p_drop, seed, step, rng  the forward's (the rng words with their values then).
+ *  dx            [n_rows, ld_dx] of dtype (it may be dy's or dh's buffer).
+ *  dresidual     NULL, or with dropout [n_rows, ld_dresidual] of dtype: the
+ *                residual's gradient (without dropout it is dx).
+ *  dweight       [width] float32.  n_rows = 0 sets it, and dbias, to zero.
+ *  dbias         [width] float32, or NULL: not computed.
+ *  workspace     16-byte aligned device memory of at least
+ *                bil_layer_norm_bwd_workspace_bytes bytes; two calls in flight at
+ *                once need two.
+ */
+int bil_layer_norm_bwd(const void *dy, const void *h, const void *weight, const float *mean, const float *rstd,
+                       const void *dh, int dtype, int weight_dtype, int64_t n_rows, int64_t width, int64_t ld_dy,
+                       int64_t ld_h, int64_t ld_dh, double p_drop, uint64_t seed, uint64_t step, const int64_t *rng,
+                       void *dx, int64_t ld_dx, void *dresidual, int64_t ld_dresidual, float *dweight, float *dbias,
+                       void *workspace, int64_t workspace_bytes, bil_stream_t stream);
+
+/*
+ * bil_dropout -- y = x f + residual, rounded to dtype, with f = 0 for a dropped
+ * element (whatever its x is) and 65536 / (65536 - border) for the others, border =
+ * p_drop * 65536 rounded to nearest even.  The mask is a function of the seed, the
+ * step and the element's place, and is never stored: the same call on the gradient
+ * of y, without a residual, gives the gradient of x.
+ *
+ * Elements 8j to 8j + 7 of row r take the 16-bit parts (each word's lower part
+ * first) of Philox4x32-10 for the counter (r * ceil(width / 8) + j, step) of two
+ * 64-bit numbers, lower word first, under the seed as key; an element is dropped
+ * where its part is below border.
+ *
+ *  x, residual   [n_rows, ld_x], [n_rows, ld_residual] of dtype; residual NULL:
+ *                none.
+ *  p_drop        in [0, 1), below 1 - 2^-17.
+ *  seed, step    any 64-bit numbers.
+ *  rng           NULL, or two int64 on the device, 8-byte aligned: the seed in
+ *                the place of `seed`, and a number added to `step`, read when the
+ *                call runs (a captured call gets new masks from new values).
+ *  y             [n_rows, ld_y] of dtype (it may be x's or the residual's buffer).
+ */
+int bil_dropout(const void *x, const void *residual, int dtype, int64_t n_rows, int64_t width, int64_t ld_x,
+                int64_t ld_residual, double p_drop, uint64_t seed, uint64_t step, const int64_t *rng, void *y,
+                int64_t ld_y, bil_stream_t stream);
+
+/*
+ * bil_embedding_fwd -- out[i] = scale * weight[ids[i]], rounded to dtype.  A row
+ * whose id is outside [0, vocab) is NaN, and nothing is read for it.
+ *
+ *  ids           [n] int64 on the device.
+ *  weight        [vocab, ld_weight] of dtype.
+ *  out           [n, ld_out] of dtype.
+ *  n, vocab      below 2^31 - 4096 and 2^31 - 1.
+ */
+int bil_embedding_fwd(const int64_t *ids, int64_t n, const void *weight, int dtype, int64_t vocab, int64_t width,
+                      int64_t ld_weight, float scale, void *out, int64_t ld_out, bil_stream_t stream);
+
+/*
+ * bil_embedding_bwd_workspace_bytes -- bytes of device workspace that
+ * bil_embedding_bwd needs for n tokens of `width` columns.
+ */
+int bil_embedding_bwd_workspace_bytes(int64_t n, int64_t width, int64_t *bytes);
+
+/*
+ * bil_embedding_bwd -- the table's gradient, every row of it:
+ *     dweight[v] = scale * (sum of dy[i] over the i with ids[i] = v), rounded once,
+ *     or (accumulate) dweight[v] + that, where v has an i
+ * The sum is float32, in an order that the ids fix: the bits are reproducible.  Ids
+ * outside [0, vocab), and those equal to padding_idx, add nothing.
+ *
+ *  dy            [n, ld_dy] of dtype.
+ *  padding_idx   -1: none.
+ *  dweight       [vocab, ld_dweight] of dweight_dtype, dtype or BIL_F32.  Rows
+ *                without a token are set to zero, or (accumulate) left alone.
+ *  workspace     256-byte aligned device memory of at least
+ *                bil_embedding_bwd_workspace_bytes bytes; two calls in flight at
+ *                once need two.
+ */
+int bil_embedding_bwd(const void *dy, int dtype, int64_t n, int64_t width, int64_t ld_dy, const int64_t *ids,
+                      int64_t vocab, float scale, int64_t padding_idx, void *dweight, int dweight_dtype,
+                      int64_t ld_dweight, int accumulate, void *workspace, int64_t workspace_bytes,
+                      bil_stream_t stream);
+
+/*
  * bil_sum_f32 -- dst[i] = ((srcs[0][i] + srcs[1][i]) + srcs[2][i]) + ... for
  * i < n: float32 sums in the order of `srcs` (1 <= count <= 16; `srcs` is a
  * host array of device pointers; dst may be one of the sources).  Adds the
@@ -634,6 +764,7 @@ int bil_linear_logp_fwd_static(const void *hidden, const void *weight, int dtype
  * bil_logp_topk_fwd: 1 and 8.  bil_rms_norm_bwd, and bil_rms_norm_fwd,
  * bil_rms_norm_quant and bil_quantize_rows of rows that are no multiple of 8
  * elements or start off 16-byte boundaries: 1024, the wait for a row.
+ * bil_layer_norm_bwd and bil_layer_norm_fwd: as the norm's.
  */
 int bil_watchdog_status(unsigned int *flags, int clear);
 

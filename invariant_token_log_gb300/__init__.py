@@ -9,7 +9,10 @@ PyTorch front end.  Build the library with
 ``python -m invariant_token_log_gb300.build``.
 """
 from ._lib import BilError, contract_id, library_path, load  # noqa: F401
+from .drop import Dropout, dropout, dropout_bwd, dropout_fwd  # noqa: F401
+from .embed import Embedding, embedding, embedding_bwd, embedding_fwd  # noqa: F401
 from .host_pipeline import HostStreamedLogp  # noqa: F401
+from .layernorm import LayerNorm, layer_norm, layer_norm_bwd, layer_norm_fwd  # noqa: F401
 from .linear import (  # noqa: F401
     LINEAR_TILE_V,
     LinearLogp,

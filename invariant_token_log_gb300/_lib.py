@@ -24,7 +24,7 @@ LAYOUT_K_MAJOR, LAYOUT_MN_MAJOR = 0, 1
 
 # every entry point the header declares: name -> (restype, argtypes)
 _i32, _i64, _p, _u = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint
-_f = ctypes.c_float
+_f, _d, _u64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint64
 SIGNATURES = {
     "bil_contract_id": (ctypes.c_char_p, []),
     "bil_status_string": (ctypes.c_char_p, [_i32]),
@@ -62,6 +62,15 @@ SIGNATURES = {
     "bil_rms_norm_bwd_workspace_bytes": (_i32, [_i64, _i64, ctypes.POINTER(_i64)]),
     "bil_rms_norm_bwd": (_i32, [_p, _p, _p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i64,
                                 _p]),
+    "bil_layer_norm_fwd": (_i32, [_p, _p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _f, _d, _u64, _u64, _p, _p, _i64,
+                                  _p, _i64, _p, _p, _p]),
+    "bil_layer_norm_bwd_workspace_bytes": (_i32, [_i64, _i64, _i32, ctypes.POINTER(_i64)]),
+    "bil_layer_norm_bwd": (_i32, [_p, _p, _p, _p, _p, _p, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _d, _u64, _u64, _p,
+                                  _p, _i64, _p, _i64, _p, _p, _p, _i64, _p]),
+    "bil_dropout": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _d, _u64, _u64, _p, _p, _i64, _p]),
+    "bil_embedding_fwd": (_i32, [_p, _i64, _p, _i32, _i64, _i64, _i64, _f, _p, _i64, _p]),
+    "bil_embedding_bwd_workspace_bytes": (_i32, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "bil_embedding_bwd": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _f, _i64, _p, _i32, _i64, _i32, _p, _i64, _p]),
     "bil_sum_f32": (_i32, [ctypes.POINTER(ctypes.c_void_p), _i32, _i64, _p, _p]),
     "bil_probe_exp_rate": (_i32, [ctypes.c_int32, ctypes.c_int32, _p, _p, _p]),
     "bil_linear_logp_fwd_static": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p, _p, _i32,

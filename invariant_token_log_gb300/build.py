@@ -18,9 +18,12 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("bil.cu", "linear.cu", "norm.cu", "topk.cu")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in (
+    "bil.cu", "linear.cu", "norm.cu", "topk.cu", "layer_norm.cu", "dropout.cu", "embedding.cu")]
 HEADERS = [os.path.join(ROOT, "include", "bil.h")] + [
-    os.path.join(HERE, "csrc", f) for f in ("device_common.cuh", "launch.cuh", "layout.h", "logp_device.cuh", "internal.h")]
+    os.path.join(HERE, "csrc", f) for f in (
+        "device_common.cuh", "launch.cuh", "layout.h", "logp_device.cuh", "internal.h", "norm_device.cuh", "philox.cuh",
+        "rows_device.cuh")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall"]

@@ -654,10 +654,11 @@ int bil_watchdog_status(unsigned int* flags, int clear) {
   unsigned int linear = 0;
   if (int st = bil_internal::linear_watchdog(&linear, clear)) return st;
   *flags |= linear;
-  unsigned int topk = 0, norm = 0;
+  unsigned int topk = 0, norm = 0, layer = 0;
   if (int st = bil_internal::topk_watchdog(&topk, clear)) return st;
   if (int st = bil_internal::norm_watchdog(&norm, clear)) return st;
-  *flags |= topk | norm;
+  if (int st = bil_internal::layer_norm_watchdog(&layer, clear)) return st;
+  *flags |= topk | norm | layer;
   return BIL_OK;
 }
 
