@@ -23,7 +23,7 @@ SOURCES = [os.path.join(HERE, "csrc", f) for f in (
 HEADERS = [os.path.join(ROOT, "include", "bil.h")] + [
     os.path.join(HERE, "csrc", f) for f in (
         "device_common.cuh", "launch.cuh", "layout.h", "logp_device.cuh", "internal.h", "norm_device.cuh", "philox.cuh",
-        "rows_device.cuh")]
+        "rows_device.cuh", "tc_device.cuh")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall"]
