@@ -700,6 +700,83 @@ int bil_embedding_bwd(const void *dy, int dtype, int64_t n, int64_t width, int64
                       int64_t ld_dweight, int accumulate, void *workspace, int64_t workspace_bytes,
                       bil_stream_t stream);
 
+/* Reductions of bil_linear_cross_entropy_*: a loss a row, their mean over the rows
+ * that are not ignored (over none: 0), their sum. */
+#define BIL_REDUCE_NONE 0
+#define BIL_REDUCE_MEAN 1
+#define BIL_REDUCE_SUM 2
+
+/*
+ * bil_linear_cross_entropy_fwd_workspace_bytes -- bytes of device workspace of
+ * bil_linear_cross_entropy_fwd, with label smoothing (smoothing != 0) or without:
+ * a copy of the rows, and 8 (12) bytes for each row and 128 vocabulary columns.
+ */
+int bil_linear_cross_entropy_fwd_workspace_bytes(int64_t n_rows, int64_t hidden_size, int64_t vocab, int smoothing,
+                                                 int64_t *bytes);
+
+/*
+ * bil_linear_cross_entropy_fwd -- the LM head's projection z = hidden . weight^T with
+ * softmax cross entropy; the logits are not stored.  For a row with target t, e =
+ * label_smoothing, f = z_loss:
+ *     loss = lse - (1 - e) z_t - (e / vocab) sum_c z_c + f lse^2
+ * An ignored row's loss and lse are 0, its hidden row is not read.  A target
+ * outside [0, vocab) that is not ignored makes the row's loss NaN.
+ *
+ *  hidden, weight  [n_rows, ld_hidden] and [vocab, ld_weight] of dtype, BIL_BF16 or
+ *                BIL_F16; rows on 16-byte boundaries.
+ *  label_smoothing  0 to 1.
+ *  z_loss        finite.
+ *  reduction     BIL_REDUCE_*.
+ *  loss          float32: [n_rows] with BIL_REDUCE_NONE, else one.
+ *  lse           [n_rows] float32 for bil_linear_cross_entropy_bwd; NULL: not stored.
+ *  workspace     256-byte aligned device memory; two calls in flight at once need two.
+ *  validate      as for bil_logp_fwd.
+ * The bits are reproducible; a row's lse does not depend on the other rows.
+ */
+int bil_linear_cross_entropy_fwd(const void *hidden, const void *weight, int dtype, int64_t n_rows, int64_t hidden_size,
+                                 int64_t ld_hidden, int64_t vocab, int64_t ld_weight, const int64_t *target_ids,
+                                 int64_t ignore_index, float label_smoothing, float z_loss, int reduction, float *loss,
+                                 float *lse, void *workspace, int64_t workspace_bytes, int validate,
+                                 bil_stream_t stream);
+
+/*
+ * bil_linear_cross_entropy_bwd_workspace_bytes -- bytes of device workspace of
+ * bil_linear_cross_entropy_bwd on the current device: a copy of the rows, dz of one
+ * piece of the vocabulary (2 bytes for each row and column), dhidden in float32 (for
+ * few rows up to 16 of it).
+ */
+int bil_linear_cross_entropy_bwd_workspace_bytes(int64_t n_rows, int64_t hidden_size, int64_t vocab, int64_t piece,
+                                                 int64_t *bytes);
+
+/*
+ * bil_linear_cross_entropy_bwd -- the gradients of bil_linear_cross_entropy_fwd.  With
+ * g the gradient of a row's loss (grad_loss of the row, grad_loss[0], or with
+ * BIL_REDUCE_MEAN grad_loss[0] over the rows that are not ignored):
+ *     dz_c = g ((1 + 2 f lse) exp(z_c - lse) - (1 - e) [c = t] - e / vocab)
+ *     dhidden = dz . weight,   dweight = dz^T . hidden
+ * z is computed again, a piece of the vocabulary at a time.  dz is rounded to dtype
+ * under a common factor that brings the largest g (1 - e) to 2^12 (so rows whose g is
+ * far below the largest keep an absolute, not a relative accuracy in BIL_F16); the
+ * products are accumulated in float32 and rounded once.  An ignored row's dhidden is
+ * zero and its hidden row is not read; a target outside [0, vocab) makes dhidden's
+ * row, and dweight, NaN.
+ *
+ *  lse           [n_rows]: the forward's.
+ *  grad_loss     float32 on the device: [n_rows] with BIL_REDUCE_NONE, else one.
+ *  piece         columns of a piece (rounded up to 256); 0: what keeps its dz below
+ *                512 MiB, 4096 at least.
+ *  dhidden       [n_rows, ld_dhidden] of dhidden_dtype, dtype or BIL_F32, rows on
+ *                16-byte boundaries; NULL: not computed.
+ *  dweight       [vocab, ld_dweight] of dweight_dtype, likewise (n_rows = 0: zero).
+ * Other arguments as for the forward.  The bits are reproducible on a given GPU.
+ */
+int bil_linear_cross_entropy_bwd(const void *hidden, const void *weight, int dtype, int64_t n_rows, int64_t hidden_size,
+                                 int64_t ld_hidden, int64_t vocab, int64_t ld_weight, const int64_t *target_ids,
+                                 int64_t ignore_index, float label_smoothing, float z_loss, int reduction,
+                                 const float *lse, const float *grad_loss, int64_t piece, void *dhidden,
+                                 int dhidden_dtype, int64_t ld_dhidden, void *dweight, int dweight_dtype,
+                                 int64_t ld_dweight, void *workspace, int64_t workspace_bytes, bil_stream_t stream);
+
 /*
  * bil_sum_f32 -- dst[i] = ((srcs[0][i] + srcs[1][i]) + srcs[2][i]) + ... for
  * i < n: float32 sums in the order of `srcs` (1 <= count <= 16; `srcs` is a
@@ -764,7 +841,8 @@ int bil_linear_logp_fwd_static(const void *hidden, const void *weight, int dtype
  * bil_logp_topk_fwd: 1 and 8.  bil_rms_norm_bwd, and bil_rms_norm_fwd,
  * bil_rms_norm_quant and bil_quantize_rows of rows that are no multiple of 8
  * elements or start off 16-byte boundaries: 1024, the wait for a row.
- * bil_layer_norm_bwd and bil_layer_norm_fwd: as the norm's.
+ * bil_layer_norm_bwd and bil_layer_norm_fwd: as the norm's;
+ * bil_linear_cross_entropy_*: the LM-head kernel's.
  */
 int bil_watchdog_status(unsigned int *flags, int clear);
 

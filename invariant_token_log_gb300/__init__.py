@@ -9,6 +9,12 @@ PyTorch front end.  Build the library with
 ``python -m invariant_token_log_gb300.build``.
 """
 from ._lib import BilError, contract_id, library_path, load  # noqa: F401
+from .cross_entropy import (  # noqa: F401
+    LinearCrossEntropy,
+    linear_cross_entropy,
+    linear_cross_entropy_bwd,
+    linear_cross_entropy_fwd,
+)
 from .drop import Dropout, dropout, dropout_bwd, dropout_fwd  # noqa: F401
 from .embed import Embedding, embedding, embedding_bwd, embedding_fwd  # noqa: F401
 from .host_pipeline import HostStreamedLogp  # noqa: F401

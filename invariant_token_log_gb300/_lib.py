@@ -71,6 +71,12 @@ SIGNATURES = {
     "bil_embedding_fwd": (_i32, [_p, _i64, _p, _i32, _i64, _i64, _i64, _f, _p, _i64, _p]),
     "bil_embedding_bwd_workspace_bytes": (_i32, [_i64, _i64, ctypes.POINTER(_i64)]),
     "bil_embedding_bwd": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _i64, _f, _i64, _p, _i32, _i64, _i32, _p, _i64, _p]),
+    "bil_linear_cross_entropy_fwd_workspace_bytes": (_i32, [_i64, _i64, _i64, _i32, ctypes.POINTER(_i64)]),
+    "bil_linear_cross_entropy_fwd": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i64, _f, _f, _i32, _p, _p, _p,
+                                            _i64, _i32, _p]),
+    "bil_linear_cross_entropy_bwd_workspace_bytes": (_i32, [_i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]),
+    "bil_linear_cross_entropy_bwd": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _p, _i64, _f, _f, _i32, _p, _p,
+                                            _i64, _p, _i32, _i64, _p, _i32, _i64, _p, _i64, _p]),
     "bil_sum_f32": (_i32, [ctypes.POINTER(ctypes.c_void_p), _i32, _i64, _p, _p]),
     "bil_probe_exp_rate": (_i32, [ctypes.c_int32, ctypes.c_int32, _p, _p, _p]),
     "bil_linear_logp_fwd_static": (_i32, [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p, _p, _i32,

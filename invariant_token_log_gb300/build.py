@@ -19,7 +19,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in (
-    "bil.cu", "linear.cu", "norm.cu", "topk.cu", "layer_norm.cu", "dropout.cu", "embedding.cu")]
+    "bil.cu", "linear.cu", "norm.cu", "topk.cu", "layer_norm.cu", "dropout.cu", "embedding.cu",
+    "cross_entropy.cu")]
 HEADERS = [os.path.join(ROOT, "include", "bil.h")] + [
     os.path.join(HERE, "csrc", f) for f in (
         "device_common.cuh", "launch.cuh", "layout.h", "logp_device.cuh", "internal.h", "norm_device.cuh", "philox.cuh",

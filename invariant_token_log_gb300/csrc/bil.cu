@@ -654,11 +654,12 @@ int bil_watchdog_status(unsigned int* flags, int clear) {
   unsigned int linear = 0;
   if (int st = bil_internal::linear_watchdog(&linear, clear)) return st;
   *flags |= linear;
-  unsigned int topk = 0, norm = 0, layer = 0;
+  unsigned int topk = 0, norm = 0, layer = 0, xent = 0;
   if (int st = bil_internal::topk_watchdog(&topk, clear)) return st;
   if (int st = bil_internal::norm_watchdog(&norm, clear)) return st;
   if (int st = bil_internal::layer_norm_watchdog(&layer, clear)) return st;
-  *flags |= topk | norm | layer;
+  if (int st = bil_internal::xent_watchdog(&xent, clear)) return st;
+  *flags |= topk | norm | layer | xent;
   return BIL_OK;
 }
 

@@ -51,9 +51,10 @@ class BIL_INTERNAL NvtxRange {
 // bil_watchdog_status); cleared when `clear` is non-zero.
 BIL_INTERNAL int linear_watchdog(unsigned int* flags, int clear);
 
-// The same of the kernels in topk.cu, in norm.cu and in layer_norm.cu.
+// The same of the kernels in topk.cu, in norm.cu, in layer_norm.cu and in cross_entropy.cu.
 BIL_INTERNAL int topk_watchdog(unsigned int* flags, int clear);
 BIL_INTERNAL int norm_watchdog(unsigned int* flags, int clear);
 BIL_INTERNAL int layer_norm_watchdog(unsigned int* flags, int clear);
+BIL_INTERNAL int xent_watchdog(unsigned int* flags, int clear);
 
 }  // namespace bil_internal
