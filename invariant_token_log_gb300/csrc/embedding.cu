@@ -74,16 +74,34 @@ __global__ void __launch_bounds__(kLookupThreads) embedding_lookup_kernel(const 
 
 // ---------------------------------------------------------------------------
 // Sorting the places by token: least significant digit first, two kernels a digit
-// (the tiles' digit counts, then each tile's places to where they belong).
+// (the tiles' digit counts, then each tile's places to where they belong).  A few
+// blocks of small latency each; of the table's zeros, most of what the gradient
+// writes, further blocks of the same launches store a part meanwhile.
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / kLanes;
-constexpr int kSortPer = 16;                            // places a thread
-constexpr int kSortTile = kSortThreads * kSortPer;
+constexpr int kFewPer = 4, kManyPer = 16;               // places a thread (see sort_per)
 constexpr int kDigitBits = 9;                           // 151936 tokens and the one behind them: two digits
 constexpr int kDigits = 1 << kDigitBits;
 static_assert(kDigits == 2 * kSortThreads, "a thread has two digits");
+
+// Rows [begin, end) of the table's gradient to set to zero: row_bytes of each, ld bytes apart.
+struct Zeros {
+  unsigned char* to;
+  int64_t ld, begin, end, row_bytes;
+};
+
+// Row `row`, by threads `thread` of `threads`: 16 bytes at a time where it starts on a boundary of them, and a rest.
+__device__ __forceinline__ void store_zero_row(const Zeros& z, int64_t row, int thread, int threads) {
+  unsigned char* to = z.to + row * z.ld;
+  int64_t done = 0;
+  if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0) {
+    done = z.row_bytes & ~static_cast<int64_t>(15);
+    for (int64_t i = thread; i < done / 16; i += threads) reinterpret_cast<uint4*>(to)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  for (int64_t i = done / 2 + thread; i < z.row_bytes / 2; i += threads) reinterpret_cast<uint16_t*>(to)[i] = 0;
+}
 
 struct SortParams {
   const int64_t* ids;     // of the first digit: the tokens themselves
@@ -94,7 +112,20 @@ struct SortParams {
   uint32_t* places_out;
   uint32_t* counts;       // [tiles, kDigits]
   int n, tiles, shift;
+  Zeros zeros;            // by the blocks from `tiles` on
 };
+
+// All of the rows, by threads `thread` of `threads`.  Rows one after the other are one long row.
+__device__ __forceinline__ void store_zeros(const Zeros& z, int64_t thread, int64_t threads) {
+  if (z.ld == z.row_bytes && z.row_bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(z.to) & 15u) == 0) {
+    uint4* to = reinterpret_cast<uint4*>(z.to + z.begin * z.ld);
+    const int64_t units = (z.end - z.begin) * (z.row_bytes / 16);
+    for (int64_t i = thread; i < units; i += threads) to[i] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  for (int64_t row = z.begin + thread / kLanes; row < z.end; row += threads / kLanes)
+    store_zero_row(z, row, static_cast<int>(thread % kLanes), kLanes);
+}
 
 template <bool FIRST>
 __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
@@ -103,17 +134,22 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
   return static_cast<uint32_t>(id >= 0 && id < p.vocab && id != p.padding ? id : p.vocab);
 }
 
-template <bool FIRST>
+template <bool FIRST, int PER>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
   __shared__ uint32_t counts[kDigits];
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) counts[d] = 0;
   griddep_wait();
   griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= p.tiles) {
+    store_zeros(p.zeros, static_cast<int64_t>(blockIdx.x - p.tiles) * kSortThreads + threadIdx.x,
+                static_cast<int64_t>(gridDim.x - p.tiles) * kSortThreads);
+    return;
+  }
   __syncthreads();
-  const int first = static_cast<int>(blockIdx.x) * kSortTile;
-#pragma unroll 4
-  for (int j = 0; j < kSortPer; ++j) {
-    const int64_t i = static_cast<int64_t>(first) + j * kSortThreads + threadIdx.x;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kSortThreads * PER);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int64_t i = first + j * kSortThreads + threadIdx.x;
     if (i < p.n) atomicAdd(&counts[(sort_key<FIRST>(p, static_cast<int>(i)) >> p.shift) & (kDigits - 1)], 1u);
   }
   __syncthreads();
@@ -121,28 +157,45 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
     p.counts[static_cast<int64_t>(blockIdx.x) * kDigits + d] = counts[d];
 }
 
-// A warp takes its 512 places in order, 32 at a time; those with one digit rank by
+// A warp takes its 32 PER places in order, 32 at a time; those with one digit rank by
 // lane.  Where a digit's places of this tile begin: the counts of the smaller digits
 // in every tile, and of this one in the tiles before.
-template <bool FIRST>
+template <bool FIRST, int PER>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortParams p) {
   __shared__ uint32_t of_warp[kSortWarps][kDigits];  // counts, then where the warp's begin
   __shared__ uint32_t scan[kSortWarps];
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
-  for (int d = threadIdx.x; d < kDigits * kSortWarps; d += kSortThreads) of_warp[0][d] = 0;
+  for (int d = threadIdx.x; d < kDigits * kSortWarps; d += kSortThreads) of_warp[d / kDigits][d % kDigits] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSortTile + warp * (kSortPer * kLanes);
-  uint32_t key[kSortPer];
-  uint32_t rank[kSortPer];
+  if (static_cast<int>(blockIdx.x) >= p.tiles) {
+    store_zeros(p.zeros, static_cast<int64_t>(blockIdx.x - p.tiles) * kSortThreads + threadIdx.x,
+                static_cast<int64_t>(gridDim.x - p.tiles) * kSortThreads);
+    return;
+  }
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kSortThreads * PER) + warp * (PER * kLanes);
+  uint32_t key[PER];
+  uint32_t rank[PER];
 #pragma unroll
-  for (int j = 0; j < kSortPer; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const int64_t i = first + j * kLanes + lane;
     key[j] = i < p.n ? sort_key<FIRST>(p, static_cast<int>(i)) : 0u;
   }
+  // this thread's two digits: their counts in all tiles and in those before this one
+  uint32_t total[2] = {0, 0}, ahead[2] = {0, 0};
+#pragma unroll 8
+  for (int t = 0; t < p.tiles; ++t) {
+    const uint2 c = *reinterpret_cast<const uint2*>(p.counts + static_cast<int64_t>(t) * kDigits + 2 * threadIdx.x);
+    total[0] += c.x;
+    total[1] += c.y;
+    if (t < static_cast<int>(blockIdx.x)) {
+      ahead[0] += c.x;
+      ahead[1] += c.y;
+    }
+  }
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kSortPer; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const bool have = first + j * kLanes + lane < p.n;
     const uint32_t d = have ? (key[j] >> p.shift) & (kDigits - 1) : kDigits;  // kDigits: none
     const unsigned peers = __match_any_sync(0xffffffffu, d);
@@ -153,18 +206,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     if (have && before == 0) of_warp[warp][d] = at + static_cast<uint32_t>(__popc(peers));
     __syncwarp();
     rank[j] = at + static_cast<uint32_t>(__popc(before));
-  }
-  // this thread's two digits: their counts in all tiles and in those before this one
-  uint32_t total[2] = {0, 0}, ahead[2] = {0, 0};
-#pragma unroll 4
-  for (int t = 0; t < p.tiles; ++t) {
-    const uint2 c = *reinterpret_cast<const uint2*>(p.counts + static_cast<int64_t>(t) * kDigits + 2 * threadIdx.x);
-    total[0] += c.x;
-    total[1] += c.y;
-    if (t < static_cast<int>(blockIdx.x)) {
-      ahead[0] += c.x;
-      ahead[1] += c.y;
-    }
   }
   uint32_t sum = total[0] + total[1];
 #pragma unroll
@@ -189,7 +230,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kSortPer; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const int64_t i = first + j * kLanes + lane;
     if (i >= p.n) continue;
     const uint32_t to = of_warp[warp][(key[j] >> p.shift) & (kDigits - 1)] + rank[j];
@@ -214,6 +255,8 @@ struct SumParams {
   float scale;
   unsigned char* dw;
   int vec_dw, accumulate;
+  Zeros zeros;             // rows without a token among these
+  int sum_blocks, zero_blocks;
   float* parts;            // [segments, 2, groups * 8]: a token's sum that goes on from the segment before, and
                            // one that begins here and goes on behind
 };
@@ -244,18 +287,52 @@ __device__ __forceinline__ void put_part(const SumParams& p, int segment, int wh
   o[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
 }
 
-// One segment of places for one slab of columns: a group a thread.
+// A thread's segment and group in block `block`; false: it has none.
+__device__ __forceinline__ bool sum_unit(const SumParams& p, int64_t block, int& segment, int& g) {
+  const int sub = static_cast<int>(threadIdx.x) / p.row_threads, per_block = kSumThreads / p.row_threads;
+  const int64_t unit = block * per_block + sub;
+  segment = static_cast<int>(unit / p.slabs);
+  g = static_cast<int>(unit % p.slabs) * p.row_threads + static_cast<int>(threadIdx.x) - sub * p.row_threads;
+  return sub < per_block && segment < p.segments && g < p.groups;
+}
+
+// Zeros in the rows of one block that have no token: 32 rows, a lane looking for each.
+constexpr int kZeroRows = 32;
+__device__ __forceinline__ void zero_rows(const SumParams& p, int64_t block) {
+  const int64_t first = p.zeros.begin + block * kZeroRows;
+  const int64_t mine = first + threadIdx.x % kLanes;
+  int low = 0, high = p.n;  // the first place whose token is not below
+  while (low < high) {
+    const int mid = low + (high - low) / 2;
+    if (static_cast<int64_t>(p.keys[mid]) < mine)
+      low = mid + 1;
+    else
+      high = mid;
+  }
+  const bool none = mine < p.zeros.end && (low == p.n || static_cast<int64_t>(p.keys[low]) != mine);
+  unsigned rows = __ballot_sync(0xffffffffu, none);
+  while (rows != 0) {
+    store_zero_row(p.zeros, first + __ffs(rows) - 1, threadIdx.x, kSumThreads);
+    rows &= rows - 1;
+  }
+}
+
+// One segment of places for one slab of columns: a group a thread.  The blocks that
+// store zeros lie evenly among those that sum: the ones write while the others wait.
 template <int DT, int OT, bool FULL>
 __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const SumParams p) {
   using R = Row<DT>;
   constexpr int kAhead = DT == BIL_F32 ? 4 : 8;
   griddep_wait();
   griddep_launch_dependents();
-  const int per_block = kSumThreads / p.row_threads;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.row_threads;
-  const int segment = static_cast<int>(unit / p.slabs);
-  const int g = static_cast<int>(unit % p.slabs) * p.row_threads + (static_cast<int>(threadIdx.x) & (p.row_threads - 1));
-  if (segment >= p.segments || g >= p.groups) return;
+  const int64_t all = static_cast<int64_t>(p.sum_blocks) + p.zero_blocks, block = blockIdx.x;
+  const int64_t zeros_before = block * p.zero_blocks / all;
+  if ((block + 1) * p.zero_blocks / all != zeros_before) {
+    zero_rows(p, zeros_before);
+    return;
+  }
+  int segment, g;
+  if (!sum_unit(p, block - zeros_before, segment, g)) return;
   const int begin = segment * p.segment;
   const int end = min(p.n, begin + p.segment);
   const uint32_t none = static_cast<uint32_t>(p.vocab);
@@ -265,16 +342,27 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const SumPar
   float sum[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) sum[j] = 0.0f;
+  // The tokens and places of the next rows are loaded with the rows of these.
+  uint32_t next_key[kAhead], next_place[kAhead];
+  auto look = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      next_key[k] = i0 + k < end ? p.keys[i0 + k] : none;
+      next_place[k] = i0 + k < end ? p.places[i0 + k] : 0u;
+    }
+  };
+  look(begin);
   for (int i0 = begin; i0 < end; i0 += kAhead) {
     uint32_t key[kAhead];
     uint32_t w[kAhead][R::kW];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      key[k] = i0 + k < end ? p.keys[i0 + k] : none;
+      key[k] = next_key[k];
       if (key[k] == none) continue;
-      const RowStart row(p.dy + static_cast<int64_t>(p.places[i0 + k]) * p.ld_dy * R::EB);
+      const RowStart row(p.dy + static_cast<int64_t>(next_place[k]) * p.ld_dy * R::EB);
       R::template load_path<FULL ? kFullRows : kAnyRows>(row.base, row.off, g, p.width, w[k]);
     }
+    look(i0 + kAhead);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (i0 + k >= end) continue;
@@ -307,16 +395,12 @@ template <int OT>
 __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const SumParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_block = kSumThreads / p.row_threads;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.row_threads;
-  const int segment = static_cast<int>(unit / p.slabs);
-  const int g = static_cast<int>(unit % p.slabs) * p.row_threads + (static_cast<int>(threadIdx.x) & (p.row_threads - 1));
-  if (segment >= p.segments || g >= p.groups) return;
+  int segment, g;
+  if (!sum_unit(p, blockIdx.x, segment, g)) return;
   const int64_t begin = static_cast<int64_t>(segment) * p.segment, end = begin + p.segment;
   if (end >= p.n) return;
-  const uint32_t key = p.keys[end - 1];
-  if (key == static_cast<uint32_t>(p.vocab) || p.keys[end] != key) return;       // goes on behind
-  if (begin > 0 && p.keys[begin - 1] == key) return;                             // and begins here
+  const uint32_t key = p.keys[end - 1], behind = p.keys[end], before = begin > 0 ? p.keys[begin - 1] : ~0u;
+  if (key == static_cast<uint32_t>(p.vocab) || behind != key || before == key) return;
   float sum[kVec];
   auto part = [&](int s, int which, float (&v)[kVec]) {
     const float4* o = reinterpret_cast<const float4*>(p.parts + (static_cast<int64_t>(s) * 2 + which) * p.groups * kVec + g * kVec);
@@ -324,21 +408,27 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const SumPa
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   };
   part(segment, 1, sum);
-  // the segments that begin with the token, by halving
-  int low = segment + 1, high = p.segments;  // low does, high does not
-  while (high - low > 1) {
-    const int mid = low + (high - low) / 2;
-    if (p.keys[static_cast<int64_t>(mid) * p.segment] == key)
-      low = mid;
-    else
-      high = mid;
-  }
-#pragma unroll 4
-  for (int s = segment + 1; s <= low; ++s) {
-    float v[kVec];
-    part(s, 0, v);
+  // the segments that begin with the token, a few at a time: their parts are loaded with their first tokens
+  constexpr int kAhead = 8;
+  for (int s0 = segment + 1; s0 < p.segments; s0 += kAhead) {
+    uint32_t first[kAhead];
+    float v[kAhead][kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) sum[j] = __fadd_rn(sum[j], v[j]);
+    for (int k = 0; k < kAhead; ++k) {
+      first[k] = static_cast<uint32_t>(p.vocab);
+      if (s0 + k >= p.segments) continue;
+      first[k] = p.keys[static_cast<int64_t>(s0 + k) * p.segment];
+      part(s0 + k, 0, v[k]);  // (of another token: not used)
+    }
+    bool more = true;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      more = more && first[k] == key;
+      if (!more) continue;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) sum[j] = __fadd_rn(sum[j], v[k][j]);
+    }
+    if (!more) break;
   }
   put_sum<OT>(p, key, g, sum);
 }
@@ -349,12 +439,22 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const SumPa
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
-// Places a segment: 32, or as many as leave 2048 segments (of a power of two).
+// Places a segment: 16, or as many as leave 2048 segments (of a power of two).
 int segment_places(int64_t n) {
-  int s = 32;
+  int s = 16;
   while (static_cast<int64_t>(s) * 2048 < n) s *= 2;
   return s;
 }
+
+// Places a thread of the sort's tiles: few, so that a short sort has blocks for more SMs (16384 tokens: 16); many
+// from 64 such tiles on, since every tile reads the counts of all.
+int sort_per(int64_t n) { return n <= 64 * kSortThreads * kFewPer ? kFewPer : kManyPer; }
+int64_t sort_tiles(int64_t n) {
+  const int64_t tile = static_cast<int64_t>(kSortThreads) * sort_per(n);
+  return (n + tile - 1) / tile;
+}
+
+constexpr int64_t kEarlyZeros = 32 << 20;  // bytes of zeros in a launch of the sort: its few microseconds at 6.6 TB/s
 
 struct Layout {
   size_t keys, counts, parts, total;
@@ -362,7 +462,7 @@ struct Layout {
 
 Layout layout_of(int64_t n, int64_t width) {
   Layout l;
-  const int64_t tiles = (n + kSortTile - 1) / kSortTile, segments = (n + segment_places(n) - 1) / segment_places(n);
+  const int64_t tiles = sort_tiles(n), segments = (n + segment_places(n) - 1) / segment_places(n);
   l.keys = round256(static_cast<size_t>(n) * 4);
   l.counts = round256(static_cast<size_t>(tiles) * kDigits * 4);
   l.parts = round256(static_cast<size_t>(segments) * 2 * static_cast<size_t>((width + kVec - 1) / kVec * kVec) * 4);
@@ -372,7 +472,7 @@ Layout layout_of(int64_t n, int64_t width) {
 
 int check_sizes(int64_t n, int64_t vocab, int64_t width) {
   if (n < 0 || vocab < 1 || width < 1) return BIL_E_INVALID_ARG;
-  if (n > INT32_MAX - kSortTile || vocab > INT32_MAX - 1 || width > INT32_MAX / 16) return BIL_E_UNSUPPORTED;
+  if (n > INT32_MAX - 65536 || vocab > INT32_MAX - 1 || width > INT32_MAX / 16) return BIL_E_UNSUPPORTED;
   return BIL_OK;
 }
 
@@ -383,11 +483,11 @@ int pow2_threads(int groups, int most) {
 }
 
 template <int DT, int OT>
-cudaError_t launch_sums(const SumParams& p, bool full, int64_t grid, cudaStream_t s) {
-  cudaError_t e = launch_pdl(full ? embedding_sum_kernel<DT, OT, true> : embedding_sum_kernel<DT, OT, false>, grid,
-                             kSumThreads, 0, s, 1, p);
+cudaError_t launch_sums(const SumParams& p, bool full, cudaStream_t s) {
+  cudaError_t e = launch_pdl(full ? embedding_sum_kernel<DT, OT, true> : embedding_sum_kernel<DT, OT, false>,
+                             static_cast<int64_t>(p.sum_blocks) + p.zero_blocks, kSumThreads, 0, s, 1, p);
   if (e != cudaSuccess || p.segments < 2) return e;
-  return launch_pdl(embedding_join_kernel<OT>, grid, kSumThreads, 0, s, 1, p);
+  return launch_pdl(embedding_join_kernel<OT>, p.sum_blocks, kSumThreads, 0, s, 1, p);
 }
 
 }  // namespace
@@ -456,11 +556,14 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
     if (workspace_bytes < static_cast<int64_t>(layout_of(n, width).total)) return BIL_E_INVALID_ARG;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!accumulate &&
-      cudaMemset2DAsync(dweight, static_cast<size_t>(ld_dweight) * ob, 0, static_cast<size_t>(width) * ob,
-                        static_cast<size_t>(vocab), s) != cudaSuccess)
-    return BIL_E_CUDA;
-  if (n == 0) return BIL_OK;
+  if (n == 0) {
+    return accumulate || cudaMemset2DAsync(dweight, static_cast<size_t>(ld_dweight) * ob, 0, static_cast<size_t>(width) * ob,
+                                           static_cast<size_t>(vocab), s) == cudaSuccess
+               ? BIL_OK
+               : BIL_E_CUDA;
+  }
+  int sms = 0, smem_optin = 0;
+  if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   const Layout l = layout_of(n, width);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   uint32_t* buf[4];
@@ -472,20 +575,33 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   q.padding = padding_idx;
   q.counts = reinterpret_cast<uint32_t*>(ws + 4 * l.keys);
   q.n = static_cast<int>(n);
-  q.tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
+  q.tiles = static_cast<int>(sort_tiles(n));
+  Zeros zeros{static_cast<unsigned char*>(dweight), ld_dweight * ob, 0, accumulate ? 0 : vocab, width * ob};
+  int launches = 0;
+  for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += kDigitBits) launches += 2;
+  // What the sort's launches have time for; the sums' launch stores the others.
+  const int64_t early = std::min(zeros.end, launches * (kEarlyZeros / zeros.row_bytes + 1));
+  const bool few = sort_per(n) == kFewPer;
   int at = 0;  // the pair of buffers that the next digit is written to
-  for (q.shift = 0; q.shift == 0 || (vocab >> q.shift) != 0; q.shift += kDigitBits) {
-    const bool first = q.shift == 0;
+  for (int i = 0; i < launches; ++i) {
+    const bool first = i < 2, count = i % 2 == 0;
+    q.shift = i / 2 * kDigitBits;
     q.keys = buf[at ^ 2];
     q.places = buf[(at ^ 2) + 1];
     q.keys_out = buf[at];
     q.places_out = buf[at + 1];
-    if (launch_pdl(first ? sort_count_kernel<true> : sort_count_kernel<false>, q.tiles, kSortThreads, 0, s, 1, q) !=
-            cudaSuccess ||
-        launch_pdl(first ? sort_place_kernel<true> : sort_place_kernel<false>, q.tiles, kSortThreads, 0, s, 1, q) !=
-            cudaSuccess)
-      return BIL_E_CUDA;
-    at ^= 2;
+    q.zeros = zeros;
+    q.zeros.begin = early * i / launches;
+    q.zeros.end = early * (i + 1) / launches;
+    const int64_t units = ((q.zeros.end - q.zeros.begin) * q.zeros.row_bytes / 16 + kSortThreads - 1) / kSortThreads;
+    const int64_t zero_blocks = early == 0 ? 0 : std::max<int64_t>(1, std::min<int64_t>(units, 8 * static_cast<int64_t>(sms)));
+    void (*kernel)(SortParams) =
+        count ? (first ? (few ? sort_count_kernel<true, kFewPer> : sort_count_kernel<true, kManyPer>)
+                       : (few ? sort_count_kernel<false, kFewPer> : sort_count_kernel<false, kManyPer>))
+              : (first ? (few ? sort_place_kernel<true, kFewPer> : sort_place_kernel<true, kManyPer>)
+                       : (few ? sort_place_kernel<false, kFewPer> : sort_place_kernel<false, kManyPer>));
+    if (launch_pdl(kernel, q.tiles + zero_blocks, kSortThreads, 0, s, 1, q) != cudaSuccess) return BIL_E_CUDA;
+    if (!count) at ^= 2;
   }
 
   SumParams p{};
@@ -500,8 +616,8 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   p.ld_dw = ld_dweight;
   p.width = static_cast<int>(width);
   p.groups = (p.width + kVec - 1) / kVec;
-  p.row_threads = pow2_threads(p.groups, kSumThreads);
-  p.slabs = (p.groups + p.row_threads - 1) / p.row_threads;
+  p.slabs = (p.groups + kSumThreads - 1) / kSumThreads;  // as even as can be
+  p.row_threads = ((p.groups + p.slabs - 1) / p.slabs + 7) / 8 * 8;
   p.scale = scale;
   p.dw = static_cast<unsigned char*>(dweight);
   p.vec_dw = rows_start_on(dweight, vocab, ld_dweight * ob, 16);
@@ -509,17 +625,22 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   p.parts = reinterpret_cast<float*>(ws + 4 * l.keys + l.counts);
   const bool full = width % kVec == 0 && rows_start_on(dy, n, ld_dy * eb, 16);
   const int per_block = kSumThreads / p.row_threads;
-  const int64_t grid = (static_cast<int64_t>(p.segments) * p.slabs + per_block - 1) / per_block;
-  if (grid > INT32_MAX) return BIL_E_UNSUPPORTED;
+  zeros.begin = early;
+  p.zeros = zeros;
+  const int64_t sum_blocks = (static_cast<int64_t>(p.segments) * p.slabs + per_block - 1) / per_block;
+  const int64_t zero_blocks = (zeros.end - zeros.begin + kZeroRows - 1) / kZeroRows;
+  if (sum_blocks + zero_blocks > INT32_MAX) return BIL_E_UNSUPPORTED;
+  p.sum_blocks = static_cast<int>(sum_blocks);
+  p.zero_blocks = static_cast<int>(zero_blocks);
   cudaError_t e;
   if (dtype == BIL_F32)
-    e = launch_sums<BIL_F32, BIL_F32>(p, full, grid, s);
+    e = launch_sums<BIL_F32, BIL_F32>(p, full, s);
   else if (dtype == BIL_BF16)
-    e = dweight_dtype == BIL_F32 ? launch_sums<BIL_BF16, BIL_F32>(p, full, grid, s)
-                                 : launch_sums<BIL_BF16, BIL_BF16>(p, full, grid, s);
+    e = dweight_dtype == BIL_F32 ? launch_sums<BIL_BF16, BIL_F32>(p, full, s)
+                                 : launch_sums<BIL_BF16, BIL_BF16>(p, full, s);
   else
-    e = dweight_dtype == BIL_F32 ? launch_sums<BIL_F16, BIL_F32>(p, full, grid, s)
-                                 : launch_sums<BIL_F16, BIL_F16>(p, full, grid, s);
+    e = dweight_dtype == BIL_F32 ? launch_sums<BIL_F16, BIL_F32>(p, full, s)
+                                 : launch_sums<BIL_F16, BIL_F16>(p, full, s);
   return e == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 

@@ -87,7 +87,7 @@ int bil_layer_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int need_b
   if (n_rows < 0 || width < 1 || bytes == nullptr) return BIL_E_INVALID_ARG;
   if (width > BIL_MAX_NORM_WIDTH) return BIL_E_UNSUPPORTED;
   int64_t parts = 0;
-  if (int st = bwd_parts(n_rows, width, &parts)) return st;
+  if (int st = bwd_parts(n_rows, width, true, &parts)) return st;
   *bytes = parts * width * static_cast<int64_t>(sizeof(float)) * (need_bias ? 2 : 1);
   return BIL_OK;
 }

@@ -69,6 +69,9 @@ inline int bwd_per_sm(int row_threads, int per_thread) {
   return std::max(1, (per_thread == 4 ? 512 : 768) / row_threads);
 }
 
+// The same of the layer norm, whose registers hold the bias's sums besides: 512 at up to 128.
+inline int layer_bwd_per_sm(int row_threads) { return row_threads == kWarp ? 2 : std::max(1, 512 / row_threads); }
+
 // The ring of the backward: of up to *per_sm blocks an SM the most that leave each
 // three stages, or one block with two.  0 stages: the rows are too wide for that.
 inline void bwd_ring(size_t stage_bytes, size_t limit, int* per_sm, int* stages) {

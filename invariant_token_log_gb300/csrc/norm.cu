@@ -171,7 +171,7 @@ int bil_rms_norm_bwd_workspace_bytes(int64_t n_rows, int64_t width, int64_t* byt
   if (n_rows < 0 || width < 1 || bytes == nullptr) return BIL_E_INVALID_ARG;
   if (width > BIL_MAX_NORM_WIDTH) return BIL_E_UNSUPPORTED;
   int64_t parts = 0;
-  if (int st = bwd_parts(n_rows, width, &parts)) return st;
+  if (int st = bwd_parts(n_rows, width, false, &parts)) return st;
   *bytes = parts * width * static_cast<int64_t>(sizeof(float));
   return BIL_OK;
 }
@@ -199,7 +199,7 @@ int bil_rms_norm_bwd(const void* dy, const void* h, const void* weight, const fl
   if (rstd == nullptr || workspace == nullptr) return BIL_E_INVALID_ARG;
   if (!aligned_to(workspace, 16)) return BIL_E_ALIGN;
   int64_t parts = 0;
-  if (int st = bwd_parts(n_rows, width, &parts)) return st;
+  if (int st = bwd_parts(n_rows, width, false, &parts)) return st;
   if (workspace_bytes < parts * width * static_cast<int64_t>(sizeof(float))) return BIL_E_INVALID_ARG;
   NormParams p{};
   p.x = static_cast<const unsigned char*>(h);

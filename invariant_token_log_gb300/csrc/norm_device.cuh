@@ -58,26 +58,41 @@ struct RowReduce {
     m = v.y;
     butterfly<SUM, MAX>(s, m);
   }
-  // the sums of a and of b
+  // The layer norm's, with less latency: the sums of a and of b, the two halves of a warp taking one each from the
+  // first step on, and the warps' results added up by every thread itself (more than one warp a row).
   __device__ __forceinline__ void sums(float& a, float& b) {
-    butterfly2(a, b);
+    const int lane = threadIdx.x % kLanes;
+    const bool upper = lane >= 16;
+    float mine = __fadd_rn(upper ? b : a, __shfl_xor_sync(0xffffffffu, upper ? a : b, 16));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mine = __fadd_rn(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    if (warps == 1) {
+      a = __shfl_sync(0xffffffffu, mine, 0);
+      b = __shfl_sync(0xffffffffu, mine, 16);
+      return;
+    }
+    float2* buf = red + which * (kMaxRowThreads / kLanes);
+    which ^= 1;
+    if (lane % 16 == 0) (upper ? buf[threadIdx.x / kLanes].y : buf[threadIdx.x / kLanes].x) = mine;
+    __syncthreads();
+    a = b = 0.0f;
+    for (int w = 0; w < warps; ++w) {
+      const float2 v = buf[w];
+      a = __fadd_rn(a, v.x);
+      b = __fadd_rn(b, v.y);
+    }
+  }
+  // the sum of a alone
+  __device__ __forceinline__ void sum(float& a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, o));
     if (warps == 1) return;
     float2* buf = red + which * (kMaxRowThreads / kLanes);
     which ^= 1;
-    const int lane = threadIdx.x % kLanes;
-    if (lane == 0) buf[threadIdx.x / kLanes] = make_float2(a, b);
+    if (threadIdx.x % kLanes == 0) buf[threadIdx.x / kLanes].x = a;
     __syncthreads();
-    const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
-    a = v.x;
-    b = v.y;
-    butterfly2(a, b);
-  }
-  __device__ static __forceinline__ void butterfly2(float& a, float& b) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, o));
-      b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, o));
-    }
+    a = 0.0f;
+    for (int w = 0; w < warps; ++w) a = __fadd_rn(a, buf[w].x);
   }
   template <bool SUM, bool MAX>
   __device__ static __forceinline__ void butterfly(float& s, float& m) {
@@ -287,7 +302,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       if (MODE == kQuantOnly) amax = max_nan(amax, fabsf(v));
     }
   }
-  reduce.run<MODE != kQuantOnly, MODE == kNormQuant || MODE == kQuantOnly>(ss, amax);
+  if (LAYER)
+    reduce.sum(ss);
+  else
+    reduce.run<MODE != kQuantOnly, MODE != kNormPlain>(ss, amax);
   if (BULK) {  // every thread has the row: its stage takes another
     if (reduce.warps == 1) __syncwarp();
     const int64_t refill = row + static_cast<int64_t>(p.stages) * gridDim.x;
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
         if (j < count) ss = __fmaf_rn(v, v, ss);
       }
     }
-    reduce.run<true, false>(ss, amax);
+    reduce.sum(ss);
   }
   if (MODE != kQuantOnly) {
     const float ms = __fdiv_rn(ss, static_cast<float>(p.width));
@@ -443,21 +461,29 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
 #pragma unroll
   for (int i = 0; i < NG; ++i)
     if (r + i * tpr < p.groups) wt[i].load(p.weight, r + i * tpr, p.width);
-  float dw[NG][kVec], db[NG][kVec];  // (db: of the layer norm alone)
+  float dw[NG][kVec];
 #pragma unroll
   for (int i = 0; i < NG; ++i)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) dw[i][j] = db[i][j] = 0.0f;
+    for (int j = 0; j < kVec; ++j) dw[i][j] = 0.0f;
+  uint64_t dw2[NG][kVec / 2], db2[NG][kVec / 2];  // the layer norm's, in pairs
+#pragma unroll
+  for (int i = 0; i < NG; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j) dw2[i][j] = db2[i][j] = 0;
   const DropKey drop_key(p.drop);
+  const float inv_width = __fdiv_rn(1.0f, static_cast<float>(p.width));
   int stage = 0;
   unsigned parity = 0;
   for (int64_t row = part; row < p.n_rows; row += parts) {
     // where the rows lie in memory and (BULK, as far past a 16-byte boundary) in the stage
     RowStart h(p.x + row * p.ld_x * R::EB), dy(p.dy + row * p.ld_dy * R::EB);
     RowStart dh(p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr);
-    const float rstd = p.rstd[row], mean = LAYER ? p.mean[row] : 0.0f;
-    // an element of the normed row
-    auto unit = [&](float v) { return LAYER ? __fmul_rn(__fsub_rn(v, mean), rstd) : __fmul_rn(v, rstd); };
+    const float rstd = p.rstd[row];
+    // The layer norm works on pairs of elements, half of the instructions; an element of the normed row is
+    // h rstd - (mean rstd) there, whose rounding is far below the mean's own.
+    const float off = LAYER ? -__fmul_rn(p.mean[row], rstd) : 0.0f;
+    const uint64_t rstd2 = pk(rstd, rstd), off2 = pk(off, off);
     if (BULK) {
       // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its
       // barriers still met by every thread, and fills no further stage.)
@@ -471,6 +497,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
     constexpr int kHeld = BULK ? 1 : NG;
     uint32_t wh[kHeld][R::kW], wd[kHeld][R::kW], wg[kHeld][R::kW];
     float dot = 0.0f, sum = 0.0f;
+    uint64_t dots = 0, sums = 0;
     if (!BULK) {
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
@@ -489,25 +516,38 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
         R::template load_path<PATH>(h.base, h.off, g, p.width, wh[0]);
         R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[0]);
       }
+      if constexpr (LAYER) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float u = unit(R::get(wh[i % kHeld], j)), d = R::get(wd[i % kHeld], j);
-        const float v = __fmul_rn(d, wt[i].get(j));  // (a missing element's is zero: dot and sum need no test)
-        dot = __fmaf_rn(v, u, dot);
-        dw[i][j] = __fmaf_rn(d, u, dw[i][j]);
-        if (LAYER) {
-          sum = __fadd_rn(sum, v);
-          db[i][j] = __fadd_rn(db[i][j], d);
+        for (int j = 0; j < kVec / 2; ++j) {  // (a missing element's d and weight are zero)
+          const uint64_t u = fma2(R::pair(wh[i % kHeld], j), rstd2, off2), d = R::pair(wd[i % kHeld], j);
+          const uint64_t v = mul2(d, wt[i].pair(j));
+          dots = fma2(v, u, dots);
+          sums = add2(sums, v);
+          dw2[i][j] = fma2(d, u, dw2[i][j]);
+          db2[i][j] = add2(db2[i][j], d);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd), d = R::get(wd[i % kHeld], j);
+          dot = __fmaf_rn(__fmul_rn(d, wt[i].get(j)), u, dot);
+          dw[i][j] = __fmaf_rn(d, u, dw[i][j]);
         }
       }
     }
     float none = 0.0f;
-    if (LAYER)
+    if (LAYER) {
+      dot = __fadd_rn(lo_of(dots), hi_of(dots));
+      sum = __fadd_rn(lo_of(sums), hi_of(sums));
       reduce.sums(dot, sum);
-    else
+    } else {
       reduce.run<true, false>(dot, none);
-    const float c = __fdiv_rn(dot, static_cast<float>(p.width));
-    const float c1 = LAYER ? __fdiv_rn(sum, static_cast<float>(p.width)) : 0.0f;
+    }
+    const float c = LAYER ? 0.0f : __fdiv_rn(dot, static_cast<float>(p.width));
+    // of the layer norm's rstd (v - c1 - u c2)
+    const float f1 = LAYER ? -__fmul_rn(__fmul_rn(sum, inv_width), rstd) : 0.0f;
+    const float f2 = LAYER ? -__fmul_rn(__fmul_rn(dot, inv_width), rstd) : 0.0f;
+    const uint64_t f1s = pk(f1, f1), f2s = pk(f2, f2);
     if (BULK) {
       // every thread is done with the stage of the row before this one
       const int64_t refill = row + static_cast<int64_t>(p.stages - 1) * parts;
@@ -523,17 +563,33 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
         R::template load_path<PATH>(h.base, h.off, g, p.width, wh[0]);
         R::template load_path<PATH>(dy.base, dy.off, g, p.width, wd[0]);
       }
+      if (BULK && p.dh != nullptr) R::template load_path<PATH>(dh.base, dh.off, g, p.width, wg[0]);
+      if constexpr (LAYER) {
+        uint64_t v2[kVec / 2];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float u = unit(R::get(wh[i % kHeld], j));
-        float dv = __fmul_rn(R::get(wd[i % kHeld], j), wt[i].get(j));
-        if (LAYER) dv = __fsub_rn(dv, c1);
-        v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, dv));
-      }
-      if (p.dh != nullptr) {
-        if (BULK) R::template load_path<PATH>(dh.base, dh.off, g, p.width, wg[0]);
+        for (int j = 0; j < kVec / 2; ++j) {
+          const uint64_t u = fma2(R::pair(wh[i % kHeld], j), rstd2, off2);
+          v2[j] = fma2(mul2(R::pair(wd[i % kHeld], j), wt[i].pair(j)), rstd2, fma2(u, f2s, f1s));
+        }
+        if (p.dh != nullptr) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(wg[i % kHeld], j));
+          for (int j = 0; j < kVec / 2; ++j) v2[j] = add2(v2[j], R::pair(wg[i % kHeld], j));
+        }
+#pragma unroll
+        for (int j = 0; j < kVec / 2; ++j) {
+          v[2 * j] = lo_of(v2[j]);
+          v[2 * j + 1] = hi_of(v2[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float u = __fmul_rn(R::get(wh[i % kHeld], j), rstd);
+          v[j] = __fmul_rn(rstd, __fmaf_rn(-u, c, __fmul_rn(R::get(wd[i % kHeld], j), wt[i].get(j))));
+        }
+        if (p.dh != nullptr) {
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(wg[i % kHeld], j));
+        }
       }
       uint32_t o[R::kW];
       if constexpr (KIND == kLayerNormDrop) {
@@ -554,7 +610,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
       parity ^= 1u;
     }
   }
-  // (a lambda for the layer norm's two sums; the barriers in it are met by every thread)
+  // (the barrier in it is met by every thread)
   auto put = [&](float* out, const float (&sums_of)[NG][kVec]) {
     if (BULK || tpr == static_cast<int>(blockDim.x)) {
 #pragma unroll
@@ -584,10 +640,21 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
     }
   };
   float* out = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.width * (LAYER && p.need_bias ? 2 : 1);
+  auto apart = [&](const uint64_t (&pairs)[NG][kVec / 2]) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) {
+        dw[i][2 * j] = lo_of(pairs[i][j]);
+        dw[i][2 * j + 1] = hi_of(pairs[i][j]);
+      }
+  };
+  if (LAYER) apart(dw2);
   put(out, dw);
   if (LAYER && p.need_bias) {
+    apart(db2);
     __syncthreads();
-    put(out + p.width, db);
+    put(out + p.width, dw);
   }
 }
 
@@ -724,12 +791,12 @@ int64_t bwd_blocks(int64_t n_rows, int row_threads, int sms, int per_sm) {
 }
 
 // The backward's partial sums, at most: one row of `width` a block.
-int bwd_parts(int64_t n_rows, int64_t width, int64_t* parts) {
+int bwd_parts(int64_t n_rows, int64_t width, bool layer, int64_t* parts) {
   int sms = 0, smem = 0;
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   int threads = 0, ng = 0;
   row_shape(static_cast<int>(width), kBwdGroups, &threads, &ng);
-  *parts = bwd_blocks(n_rows, threads, sms, bil_layout::bwd_per_sm(threads, ng));
+  *parts = bwd_blocks(n_rows, threads, sms, layer ? bil_layout::layer_bwd_per_sm(threads) : bil_layout::bwd_per_sm(threads, ng));
   return BIL_OK;
 }
 
@@ -747,10 +814,11 @@ int launch_bwd(NormParams& p, int dtype, int weight_dtype, bool full, float* dwe
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
   const size_t limit = bil_layout::dynamic_limit(smem_optin);
   const size_t stage_bytes = static_cast<size_t>(slot_bytes(p.width * eb)) * (p.dh != nullptr ? 3 : 2);
-  int per_sm = bil_layout::bwd_per_sm(p.row_threads, ng);
+  const int most = KIND != kRms ? bil_layout::layer_bwd_per_sm(p.row_threads) : bil_layout::bwd_per_sm(p.row_threads, ng);
+  int per_sm = most;
   if (p.row_threads > kLanes) bil_layout::bwd_ring(stage_bytes, limit, &per_sm, &p.stages);
   const bool bulk = p.stages != 0;
-  if (!bulk) per_sm = bil_layout::bwd_per_sm(p.row_threads, ng);
+  if (!bulk) per_sm = most;
   const int64_t grid = bwd_blocks(p.n_rows, p.row_threads, sms, per_sm);
   const int path = row_path(p.width, full, weight_dtype == dtype);
   NormKernel kernel = bwd_kernel<KIND>(dtype, ng, bulk, path);

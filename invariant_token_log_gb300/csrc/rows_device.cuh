@@ -118,6 +118,9 @@ struct Row {
     }
   }
 
+  // Values 2k and 2k + 1 as a packed pair.
+  __device__ static __forceinline__ uint64_t pair(const uint32_t (&w)[kW], int k) { return pk(get(w, 2 * k), get(w, 2 * k + 1)); }
+
   // Words of the 8 values rounded to the type (to nearest even).
   __device__ static __forceinline__ void pack(const float (&v)[kVec], uint32_t (&w)[kW]) {
 #pragma unroll
@@ -167,6 +170,7 @@ struct Weight {
     W::template load_path<PATH>(weight, 0, g, width, w);
   }
   __device__ __forceinline__ float get(int j) const { return W::get(w, j); }
+  __device__ __forceinline__ uint64_t pair(int k) const { return W::pair(w, k); }
 };
 
 // A row's 16-byte boundary and how far past it the row starts.
