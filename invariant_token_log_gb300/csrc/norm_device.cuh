@@ -475,14 +475,24 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
   const float inv_width = __fdiv_rn(1.0f, static_cast<float>(p.width));
   int stage = 0;
   unsigned parity = 0;
+  // The layer norm's statistics of a row are loaded a row ahead.
+  float next_rstd = 0.0f, next_mean = 0.0f;
+  if (LAYER && part < p.n_rows) {
+    next_rstd = p.rstd[part];
+    next_mean = p.mean[part];
+  }
   for (int64_t row = part; row < p.n_rows; row += parts) {
     // where the rows lie in memory and (BULK, as far past a 16-byte boundary) in the stage
     RowStart h(p.x + row * p.ld_x * R::EB), dy(p.dy + row * p.ld_dy * R::EB);
     RowStart dh(p.dh != nullptr ? p.dh + row * p.ld_dh * R::EB : nullptr);
-    const float rstd = p.rstd[row];
+    const float rstd = LAYER ? next_rstd : p.rstd[row];
     // The layer norm works on pairs of elements, half of the instructions; an element of the normed row is
     // h rstd - (mean rstd) there, whose rounding is far below the mean's own.
-    const float off = LAYER ? -__fmul_rn(p.mean[row], rstd) : 0.0f;
+    const float off = LAYER ? -__fmul_rn(next_mean, rstd) : 0.0f;
+    if (LAYER && row + parts < p.n_rows) {
+      next_rstd = p.rstd[row + parts];
+      next_mean = p.mean[row + parts];
+    }
     const uint64_t rstd2 = pk(rstd, rstd), off2 = pk(off, off);
     if (BULK) {
       // (A wait that ran out has set the watchdog's bit; the block goes on to its end with what is there, its

@@ -86,7 +86,7 @@ def test_lookup_shapes_types_and_bad_tokens():
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("n,vocab,width,pad,shift", [(1, 1, 1, 0, 0), (31, 3, 9, 0, 0), (33, 511, 64, 0, 0), (64, 512, 100, 0, 0),
                                                      (1000, 700, 1104, 0, 0), (4096, 20000, 264, 0, 0), (5003, 32003, 1105, 7, 3),
-                                                     (4097, 300, 4097, 0, 0), (70000, 5000, 72, 0, 0)])
+                                                     (4097, 300, 4097, 0, 0), (70000, 5000, 72, 0, 0), (20000, 700000, 72, 0, 0)])
 def test_gradient(dtype, n, vocab, width, pad, shift):
     ids = skewed(n, vocab, 3)
     dy = rows(n, width, dtype, 4, pad=pad, shift=shift)
@@ -95,7 +95,7 @@ def test_gradient(dtype, n, vocab, width, pad, shift):
         check_gradient(bil.embedding_bwd(dy, ids, vocab, out_dtype=torch.float32), dy, ids, vocab, 1.0)
 
 
-@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 65, 4095, 4096, 4097, 8193, 70001])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 65, 1023, 1024, 1025, 4097, 8193, 16384, 16385, 65536, 65537, 70001])
 @pytest.mark.parametrize("pattern", ["one", "two", "each", "blocks"])
 def test_runs_of_tokens(n, pattern):
     """Tokens whose places end inside, at and behind the segments; one token for all places."""
