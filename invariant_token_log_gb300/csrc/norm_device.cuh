@@ -112,6 +112,17 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, unsigned b
       : "memory");
 }
 
+// The 8 elements of a group times their factor, in pairs.
+template <typename R>
+__device__ __forceinline__ void drop_pairs(const uint4& bits, const Dropout& drop, const uint32_t (&w)[R::kW], float (&v)[kVec]) {
+#pragma unroll
+  for (int j = 0; j < kVec / 2; ++j) {
+    const uint64_t x = mul2(R::pair(w, j), pk(drop.times, drop.times));
+    v[2 * j] = drop_keeps(bits, 2 * j, drop.border) ? lo_of(x) : 0.0f;
+    v[2 * j + 1] = drop_keeps(bits, 2 * j + 1, drop.border) ? hi_of(x) : 0.0f;
+  }
+}
+
 struct NormParams {
   const unsigned char* x;
   const unsigned char* residual;  // NULL: none
@@ -229,6 +240,11 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   }
   griddep_wait();
   griddep_launch_dependents();
+  __shared__ DropKeys drop_keys;
+  if (MODE == kLayerDrop) {
+    drop_keys.make(p.drop);
+    __syncthreads();
+  }
   if (row >= p.n_rows) return;  // whole units, one warp a row: no barrier follows
   if (BULK && threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s)
@@ -236,7 +252,6 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   }
   int stage = 0;
   unsigned parity = 0;
-  const DropKey drop_key(p.drop);
   do {
   RowStart x(p.x + row * p.ld_x * R::EB);
   RowStart res(p.residual != nullptr ? p.residual + row * p.ld_r * R::EB : nullptr);
@@ -269,10 +284,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       if (g >= p.groups) continue;
       float v[kVec];
       if constexpr (MODE == kLayerDrop) {
-        const uint4 bits = drop_key.bits(static_cast<uint64_t>(row) * static_cast<uint64_t>(p.groups) + g);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          v[j] = drop_keeps(bits, j, p.drop.border) ? __fmul_rn(R::get(w[i], j), p.drop.times) : 0.0f;
+        const uint4 bits = drop_keys.bits(static_cast<uint64_t>(row) * static_cast<uint64_t>(p.groups) + g);
+        drop_pairs<R>(bits, p.drop, w[i], v);
         if (p.residual != nullptr) {
 #pragma unroll
           for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], R::get(q[i], j));
@@ -287,25 +300,32 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
     }
   }
   float ss = 0.0f, amax = 0.0f;
+  uint64_t sums = 0;
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
     const int g = r + i * tpr;
     if (g >= p.groups) continue;
+    if constexpr (LAYER) {  // in pairs, half of the instructions
+#pragma unroll
+      for (int j = 0; j < kVec / 2; ++j) sums = add2(sums, R::pair(w[i], j));
+      continue;
+    }
     Weight<DT, PATH> wt;
     if (MODE == kNormQuant) wt.load(p.weight, g, p.width);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {  // missing elements are zero, and so are their weights
       const float v = R::get(w[i], j);
-      if (LAYER) ss = __fadd_rn(ss, v);
-      if (MODE != kQuantOnly && !LAYER) ss = __fmaf_rn(v, v, ss);
+      if (MODE != kQuantOnly) ss = __fmaf_rn(v, v, ss);
       if (MODE == kNormQuant) amax = max_nan(amax, fabsf(__fmul_rn(v, wt.get(j))));
       if (MODE == kQuantOnly) amax = max_nan(amax, fabsf(v));
     }
   }
-  if (LAYER)
+  if (LAYER) {
+    ss = __fadd_rn(lo_of(sums), hi_of(sums));
     reduce.sum(ss);
-  else
+  } else {
     reduce.run<MODE != kQuantOnly, MODE != kNormPlain>(ss, amax);
+  }
   if (BULK) {  // every thread has the row: its stage takes another
     if (reduce.warps == 1) __syncwarp();
     const int64_t refill = row + static_cast<int64_t>(p.stages) * gridDim.x;
@@ -319,18 +339,21 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
   if constexpr (LAYER) {  // the squares of what is left of the row without its mean
     mean = __fdiv_rn(ss, static_cast<float>(p.width));
     if (r == 0 && p.mean != nullptr) p.mean[row] = mean;
-    ss = 0.0f;
+    sums = 0;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       const int g = r + i * tpr;
       if (g >= p.groups) continue;
       const int count = PATH >= kFullRows ? kVec : min(kVec, p.width - g * kVec);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float v = __fsub_rn(R::get(w[i], j), mean);
-        if (j < count) ss = __fmaf_rn(v, v, ss);
+      for (int j = 0; j < kVec / 2; ++j) {
+        uint64_t v = sub2(R::pair(w[i], j), pk(mean, mean));
+        if (2 * j >= count) v = 0;
+        if (2 * j + 1 >= count) v = pk(lo_of(v), 0.0f);
+        sums = fma2(v, v, sums);
       }
     }
+    ss = __fadd_rn(lo_of(sums), hi_of(sums));
     reduce.sum(ss);
   }
   if (MODE != kQuantOnly) {
@@ -346,15 +369,14 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_fwd_kernel(const NormPara
       Weight<DT, PATH> wt, bias;
       wt.load(p.weight, g, p.width);
       float v[kVec];
+      const uint64_t mean2 = pk(mean, mean), rstd2 = pk(rstd, rstd);
+      if (p.bias != nullptr) bias.load(p.bias, g, p.width);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(__fsub_rn(R::get(w[i], j), mean), rstd);
-      if (p.bias != nullptr) {
-        bias.load(p.bias, g, p.width);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = __fmaf_rn(v[j], wt.get(j), bias.get(j));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = __fmul_rn(v[j], wt.get(j));
+      for (int j = 0; j < kVec / 2; ++j) {
+        const uint64_t u = mul2(sub2(R::pair(w[i], j), mean2), rstd2);
+        const uint64_t y = p.bias != nullptr ? fma2(u, wt.pair(j), bias.pair(j)) : mul2(u, wt.pair(j));
+        v[2 * j] = lo_of(y);
+        v[2 * j + 1] = hi_of(y);
       }
       uint32_t o[R::kW];
       R::pack(v, o);
@@ -471,7 +493,11 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
   for (int i = 0; i < NG; ++i)
 #pragma unroll
     for (int j = 0; j < kVec / 2; ++j) dw2[i][j] = db2[i][j] = 0;
-  const DropKey drop_key(p.drop);
+  __shared__ DropKeys drop_keys;
+  if (KIND == kLayerNormDrop) {
+    drop_keys.make(p.drop);
+    __syncthreads();
+  }
   const float inv_width = __fdiv_rn(1.0f, static_cast<float>(p.width));
   int stage = 0;
   unsigned parity = 0;
@@ -607,7 +633,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_bwd_kernel(const NormPara
           R::pack(v, o);
           R::template store_path<PATH>(p.dr + row * p.ld_dr * R::EB, g, p.width, p.vec_dr != 0, o);
         }
-        const uint4 bits = drop_key.bits(static_cast<uint64_t>(row) * static_cast<uint64_t>(p.groups) + g);
+        const uint4 bits = drop_keys.bits(static_cast<uint64_t>(row) * static_cast<uint64_t>(p.groups) + g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
           v[j] = drop_keeps(bits, j, p.drop.border) ? __fmul_rn(v[j], p.drop.times) : 0.0f;

@@ -57,10 +57,33 @@ struct DropKey {
   }
 };
 
+// The same for the threads of a block, in shared memory: the ten rounds' keys, made
+// once (a quarter of a call's instructions), and the step.
+struct DropKeys {
+  uint2 key[10];
+  uint2 step;
+  __device__ __forceinline__ void make(const Dropout& d) {  // a barrier has to follow
+    if (threadIdx.x >= 10) return;
+    const DropKey k(d);
+    key[threadIdx.x] = make_uint2(k.key.x + threadIdx.x * 0x9E3779B9u, k.key.y + threadIdx.x * 0xBB67AE85u);
+    if (threadIdx.x == 0) step = k.step;
+  }
+  __device__ __forceinline__ uint4 bits(uint64_t group) const {
+    uint4 c = make_uint4(static_cast<uint32_t>(group), static_cast<uint32_t>(group >> 32), step.x, step.y);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const uint32_t h0 = __umulhi(0xD2511F53u, c.x), l0 = 0xD2511F53u * c.x;
+      const uint32_t h1 = __umulhi(0xCD9E8D57u, c.z), l1 = 0xCD9E8D57u * c.z;
+      c = make_uint4(h1 ^ c.y ^ key[i].x, l1, h0 ^ c.w ^ key[i].y, l0);
+    }
+    return c;
+  }
+};
+
 // Whether element j of a group stays.
 __device__ __forceinline__ bool drop_keeps(const uint4& bits, int j, uint32_t border) {
   const uint32_t w = j < 2 ? bits.x : j < 4 ? bits.y : j < 6 ? bits.z : bits.w;
-  return ((j & 1) ? w >> 16 : w & 0xffffu) >= border;
+  return ((j & 1) ? w : w << 16) >= border << 16;  // (a 16-bit part in the upper half: what lies below does not count)
 }
 
 // ---- host ----
