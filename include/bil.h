@@ -763,8 +763,8 @@ int bil_linear_cross_entropy_bwd_workspace_bytes(int64_t n_rows, int64_t hidden_
  *
  *  lse           [n_rows]: the forward's.
  *  grad_loss     float32 on the device: [n_rows] with BIL_REDUCE_NONE, else one.
- *  piece         columns of a piece (rounded up to 256); 0: what keeps its dz below
- *                512 MiB, 4096 at least.
+ *  piece         columns of a piece (rounded up to 256); 0: what keeps its dz within
+ *                1 GiB, 4096 at least.
  *  dhidden       [n_rows, ld_dhidden] of dhidden_dtype, dtype or BIL_F32, rows on
  *                16-byte boundaries; NULL: not computed.
  *  dweight       [vocab, ld_dweight] of dweight_dtype, likewise (n_rows = 0: zero).

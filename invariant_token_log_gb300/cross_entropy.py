@@ -31,9 +31,15 @@ from .logp import (
     _stream_handle,
     _targets1d,
 )
-from .norm import _call
+from .norm import _call, _padded
 
 _REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
+
+
+def _operand(x: torch.Tensor, what: str) -> torch.Tensor:
+    if x.is_contiguous() and x.shape[1] % 8 == 0 and x.data_ptr() % 16 == 0:
+        return x
+    return _matrix(x, what)
 
 
 def _operands(hidden, weight, target_ids, label_smoothing, reduction):
@@ -57,7 +63,7 @@ def _operands(hidden, weight, target_ids, label_smoothing, reduction):
     dev = _DEVICE_OBJECTS.get(index) or _device_object(index)
     t = _targets1d(target_ids, lead, dev)
     h2 = hidden if hidden.dim() == 2 else hidden.reshape(t.shape[0], hidden.shape[-1])
-    h2, w2 = _matrix(h2, "hidden"), _matrix(weight, "weight")
+    h2, w2 = _operand(h2, "hidden"), _operand(weight, "weight")
     if h2.shape[0] > 1 and h2.stride(0) < h2.shape[1]:
         h2 = h2.contiguous()  # an expanded tensor
     if w2.shape[0] > 1 and w2.stride(0) < w2.shape[1]:
@@ -136,13 +142,14 @@ def linear_cross_entropy_bwd(hidden: torch.Tensor, weight: torch.Tensor, target_
     for x, what, count in ((lse, "lse", n), (grad_loss, "grad_loss", want)):
         if x.get_device() != index or x.numel() != count or not x.dtype.is_floating_point:
             raise ValueError(f"{what} must hold {count} numbers on hidden's device")
-    lse, grad_loss = (x.reshape(-1).to(torch.float32).contiguous() for x in (lse, grad_loss))
+    lse, grad_loss = (x if x.dtype is torch.float32 and x.is_contiguous() else x.to(torch.float32).contiguous()
+                      for x in (lse, grad_loss))
     oc = _lib.F32 if out_dtype == torch.float32 else code
     dh = dw = None
     if need_hidden:
-        dh = torch.empty((n, _pad8(hs)), dtype=out_dtype, device=dev)[:, :hs]
+        dh, _ = _padded(n, hs, 8, out_dtype, dev)
     if need_weight:
-        dw = torch.empty((vocab, _pad8(hs)), dtype=out_dtype, device=dev)[:, :hs]
+        dw, _ = _padded(vocab, hs, 8, out_dtype, dev)
     piece = 0 if piece is None else int(piece)
     workspace, have = _scratch(workspace, _bwd_workspace_bytes(n, hs, vocab, piece, index) if n else 0, dev)
     _call("bil_linear_cross_entropy_bwd", index, h2.data_ptr(), w2.data_ptr(), code, n, hs, _ld(h2), vocab, _ld(w2),
@@ -150,7 +157,7 @@ def linear_cross_entropy_bwd(hidden: torch.Tensor, weight: torch.Tensor, target_
           lse.data_ptr(), grad_loss.data_ptr(), piece, None if dh is None else dh.data_ptr(), oc,
           0 if dh is None else _pad8(hs), None if dw is None else dw.data_ptr(), oc, 0 if dw is None else _pad8(hs),
           workspace.data_ptr(), have, _stream_handle(index))
-    return (None if dh is None else dh.reshape(*lead, hs)), dw
+    return (dh if dh is None or len(lead) == 1 else dh.reshape(*lead, hs)), dw
 
 
 class LinearCrossEntropy(torch.autograd.Function):

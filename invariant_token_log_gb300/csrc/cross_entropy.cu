@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (FLAG) p.part_z[at] = zs;
         }
       } else {
-        const int chunks = vcols <= 0 || row0 >= p.c_rows ? 0 : (vcols + kChunk - 1) / kChunk;
+        // dz has zeros up to the end of a K block of the rows, which the product with them reads.
+        const int rows = min(p.c_rows, EPI == kGrad ? (shape.m_rows + kBK - 1) / kBK * kBK : shape.m_rows);
+        const int chunks = vcols <= 0 || row0 >= rows ? 0 : (vcols + kChunk - 1) / kChunk;
         const bool none = EPI == kGrad && coef.x == 0.0f && coef.y == 0.0f && coef.z == 0.0f;
 #pragma unroll 1
         for (int c = 0; c < kHalf / kChunk; ++c) {
@@ -501,10 +503,31 @@ struct RowsParams {
   int* place;         // [n] each row's place among those that count, -1: none
   float4* coef;       // [padded]
   float* scale;       // of the products' results
+  // the copy of the rows that count (xent_gather_kernel's, or this kernel's where the rows are few)
+  const unsigned char* hidden;
+  int64_t ld_bytes;
+  int width;
+  unsigned char* compact;
+  unsigned* done;     // forward: blocks of the join that are through, set to 0
 };
+
+// Row c of the copy, from row r of hidden; r < 0: zeros.
+__device__ __forceinline__ void copy_row(const RowsParams& p, int r, int c, int thread, int threads) {
+  const int units = p.width / 8, tail = p.width % 8, pitch = (p.width + 7) / 8 * 16;
+  uint4* dst = reinterpret_cast<uint4*>(p.compact + static_cast<int64_t>(c) * pitch);
+  if (r >= 0) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.hidden + r * p.ld_bytes);
+    for (int i = thread; i < units; i += threads) dst[i] = src[i];
+    if (thread < tail)  // nothing is read behind a row
+      reinterpret_cast<uint16_t*>(dst + units)[thread] = reinterpret_cast<const uint16_t*>(src + units)[thread];
+  } else {
+    for (int i = thread; i < pitch / 16; i += threads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
 
 constexpr int kRowsThreads = 1024;
 constexpr int kRowsPer = 8;
+constexpr int kRowsShare = 128;  // of a block's rows, at most
 
 __device__ __forceinline__ void row_coefs(const RowsParams& p, int r, int count, float4& c) {
   float g = p.grad[p.reduction == kNone ? r : 0];
@@ -516,7 +539,9 @@ __device__ __forceinline__ void row_coefs(const RowsParams& p, int r, int count,
   c.w = lse;
 }
 
-// One block.  The rows keep their order.
+// The rows keep their order.  One block; or, for at most kRowsThreads * kRowsPer rows,
+// as many as there are SMs or rows, each of which finds every row's place, and copies its
+// share of them (the first alone writes the lists).
 template <bool BWD>
 __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const RowsParams p) {
   __shared__ int counts[kRowsThreads / kLanes];
@@ -524,16 +549,22 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const RowsParam
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
+  const bool lists = blockIdx.x == 0, copies = p.compact != nullptr;
+  const int share = (p.n + gridDim.x - 1) / gridDim.x, share0 = blockIdx.x * share;  // this block's rows
+  __shared__ int place_of[kRowsShare];
+  if (!BWD && lists && threadIdx.x == 0) *p.done = 0u;
   int total = 0;
   float times = 1.0f;
   if (BWD) {
     int count = 0;
+#pragma unroll 8
     for (int64_t r = threadIdx.x; r < p.n; r += kRowsThreads) count += p.targets[r] != p.ignore_index ? 1 : 0;
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) counts[warp] = count;
     __syncthreads();
     total = __reduce_add_sync(0xffffffffu, counts[lane]);
     float most_a = 0.0f, most_b = 0.0f;
+#pragma unroll 4
     for (int64_t r = threadIdx.x; r < p.n; r += kRowsThreads) {
       if (p.targets[r] == p.ignore_index) continue;
       float4 c;
@@ -556,7 +587,7 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const RowsParam
     const float most = most_a <= 8.0f * most_b ? most_b : most_a;
     const bool usual = most > 1e-30f && most < 1e30f;
     times = usual ? __fdiv_rn(4096.0f, most) : most >= 1e30f ? 1e-30f : most > 0.0f ? 1e30f : 1.0f;
-    if (threadIdx.x == 0) *p.scale = usual ? __fdiv_rn(most, 4096.0f) : most >= 1e30f ? 1e30f : most > 0.0f ? 1e-30f : 1.0f;
+    if (lists && threadIdx.x == 0) *p.scale = usual ? __fdiv_rn(most, 4096.0f) : most >= 1e30f ? 1e30f : most > 0.0f ? 1e-30f : 1.0f;
     __syncthreads();
   }
   int before = 0;  // rows that count in the chunks so far
@@ -585,6 +616,11 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const RowsParam
       const int64_t r = r0 + j;
       if (r >= p.n) continue;
       const bool counts_in = t[j] != p.ignore_index;
+      if (copies && r >= share0 && r < share0 + share) place_of[r - share0] = counts_in ? at : -1;
+      if (!lists) {
+        at += counts_in ? 1 : 0;
+        continue;
+      }
       const bool bad = t[j] < 0 || t[j] >= p.vocab;
       if (BWD) p.place[r] = counts_in ? at : -1;
       if (!counts_in) {
@@ -610,29 +646,22 @@ __global__ void __launch_bounds__(kRowsThreads) xent_rows_kernel(const RowsParam
     before += all;
     __syncthreads();
   }
-  if (threadIdx.x == 0) *p.n_active = before;
+  if (lists && threadIdx.x == 0) *p.n_active = before;
+  if (!copies) return;
+  for (int k = warp; k < share && share0 + k < p.n; k += kRowsThreads / kLanes)
+    if (place_of[k] >= 0) copy_row(p, share0 + k, place_of[k], lane, kLanes);
+  const int end = min(p.n, (before + kUnitRows - 1) / kUnitRows * kUnitRows);
+  for (int c = before + blockIdx.x * (kRowsThreads / kLanes) + warp; c < end; c += gridDim.x * (kRowsThreads / kLanes))
+    copy_row(p, -1, c, lane, kLanes);
 }
 
 // The rows of hidden that count, one after the other; behind the last, zeros up to the end of its unit.
-__global__ void __launch_bounds__(128) xent_gather_kernel(const unsigned char* __restrict__ hidden, int64_t ld_bytes,
-                                                          const int* __restrict__ rows, const int* __restrict__ n_active,
-                                                          int n, int width, unsigned char* __restrict__ out) {
-  const int units = width / 8, tail = width % 8, pitch = (width + 7) / 8 * 16;
+__global__ void __launch_bounds__(128) xent_gather_kernel(const RowsParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int active = *n_active;
-  const int end = min(n, (active + kUnitRows - 1) / kUnitRows * kUnitRows);
-  for (int c = blockIdx.x; c < end; c += gridDim.x) {
-    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(c) * pitch);
-    if (c < active) {
-      const uint4* src = reinterpret_cast<const uint4*>(hidden + static_cast<int64_t>(rows[c]) * ld_bytes);
-      for (int i = threadIdx.x; i < units; i += 128) dst[i] = src[i];
-      if (static_cast<int>(threadIdx.x) < tail)  // nothing is read behind a row
-        reinterpret_cast<uint16_t*>(dst + units)[threadIdx.x] = reinterpret_cast<const uint16_t*>(src + units)[threadIdx.x];
-    } else {
-      for (int i = threadIdx.x; i < pitch / 16; i += 128) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+  const int active = *p.n_active;
+  const int end = min(p.n, (active + kUnitRows - 1) / kUnitRows * kUnitRows);
+  for (int c = blockIdx.x; c < end; c += gridDim.x) copy_row(p, c < active ? p.rows[c] : -1, c, threadIdx.x, 128);
 }
 
 // ---------------------------------------------------------------------------
@@ -653,6 +682,9 @@ struct JoinParams {
   float* lse;       // [n] NULL: not stored
   float* loss;      // [n] by row, or NULL
   float* row_loss;  // by place among the rows that count
+  int reduction;
+  float* total;     // the losses' sum or mean
+  unsigned* done;
 };
 
 constexpr int kJoinSlices = 32;  // of a row's parts: a thread each, lanes along the rows
@@ -664,7 +696,7 @@ __global__ void __launch_bounds__(kJoinSlices * kLanes) xent_join_kernel(const J
   const int active = *p.n_active;
   const int lane = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
   const int row = static_cast<int>(blockIdx.x) * kLanes + lane;
-  if (static_cast<int>(blockIdx.x) * kLanes >= active) return;
+  if (blockIdx.x != 0 && static_cast<int>(blockIdx.x) * kLanes >= active) return;  // (over no rows: the first block)
   float m = -INFINITY, s = 0.0f, z = 0.0f;
   auto add = [&](float pm, float ps) {  // (m, s) and another part
     const float top = fmaxf(m, pm), at = top == -INFINITY ? 0.0f : top;
@@ -684,49 +716,52 @@ __global__ void __launch_bounds__(kJoinSlices * kLanes) xent_join_kernel(const J
   sm[1][slice][lane] = s;
   sm[2][slice][lane] = z;
   __syncthreads();
-  if (slice != 0 || row >= active) return;
-  for (int k = 1; k < kJoinSlices; ++k) {
-    add(sm[0][k][lane], sm[1][k][lane]);
-    z = __fadd_rn(z, sm[2][k][lane]);
-  }
-  const float lse = __fadd_rn(m, logf(s));
-  const int t = p.targets[row];
-  float loss = __int_as_float(0x7fc00000);  // a target outside the vocabulary
-  if (t >= 0) {
-    const float tl = p.target_logit[row];
-    if (p.smoothing == 0.0f) {
-      loss = __fsub_rn(lse, tl);
-    } else {
-      // (1 - e) (lse - z_t) + e (lse - mean z)
-      const float mean = __fdiv_rn(z, static_cast<float>(p.vocab));
-      loss = __fmaf_rn(p.smoothing, __fsub_rn(lse, mean), __fmul_rn(__fsub_rn(1.0f, p.smoothing), __fsub_rn(lse, tl)));
+  if (slice == 0 && row < active) {
+    for (int k = 1; k < kJoinSlices; ++k) {
+      add(sm[0][k][lane], sm[1][k][lane]);
+      z = __fadd_rn(z, sm[2][k][lane]);
     }
-    loss = __fmaf_rn(__fmul_rn(p.z_loss, lse), lse, loss);
+    const float lse = __fadd_rn(m, logf(s));
+    const int t = p.targets[row];
+    float loss = __int_as_float(0x7fc00000);  // a target outside the vocabulary
+    if (t >= 0) {
+      const float tl = p.target_logit[row];
+      if (p.smoothing == 0.0f) {
+        loss = __fsub_rn(lse, tl);
+      } else {
+        // (1 - e) (lse - z_t) + e (lse - mean z)
+        const float mean = __fdiv_rn(z, static_cast<float>(p.vocab));
+        loss = __fmaf_rn(p.smoothing, __fsub_rn(lse, mean), __fmul_rn(__fsub_rn(1.0f, p.smoothing), __fsub_rn(lse, tl)));
+      }
+      loss = __fmaf_rn(__fmul_rn(p.z_loss, lse), lse, loss);
+    }
+    const int r = p.rows[row];
+    if (p.lse != nullptr) p.lse[r] = lse;
+    if (p.loss != nullptr)
+      p.loss[r] = loss;
+    else
+      p.row_loss[row] = loss;
   }
-  const int r = p.rows[row];
-  if (p.lse != nullptr) p.lse[r] = lse;
-  if (p.loss != nullptr)
-    p.loss[r] = loss;
-  else
-    p.row_loss[row] = loss;
-}
-
-// The rows' losses added up, or their mean (over no rows: 0).
-__global__ void __launch_bounds__(1024) xent_total_kernel(const float* __restrict__ row_loss, const int* __restrict__ n_active,
-                                                          int mean, float* __restrict__ loss) {
-  __shared__ float sums[32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int active = *n_active, lane = threadIdx.x % kLanes, warp = threadIdx.x / kLanes;
-  float s = 0.0f;
-#pragma unroll 4
-  for (int64_t i = threadIdx.x; i < active; i += 1024) s = __fadd_rn(s, row_loss[i]);
-  for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-  if (lane == 0) sums[warp] = s;
+  if (p.reduction == kNone) return;
+  // The last block to come here adds up every row's loss, in an order that their number fixes.
+  __shared__ bool last;
+  __threadfence();
   __syncthreads();
-  s = sums[lane];
-  for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-  if (threadIdx.x == 0) *loss = mean ? __fdiv_rn(s, static_cast<float>(max(active, 1))) : s;
+  const unsigned blocks = static_cast<unsigned>(max(1, (active + kLanes - 1) / kLanes));
+  if (threadIdx.x == 0) last = atomicAdd(p.done, 1u) == blocks - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float sum = 0.0f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < active; i += kJoinSlices * kLanes) sum = __fadd_rn(sum, __ldcg(p.row_loss + i));
+  for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+  if (lane == 0) sm[0][0][slice] = sum;
+  __syncthreads();
+  if (slice != 0) return;
+  sum = sm[0][0][lane];
+  for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+  if (lane == 0) *p.total = p.reduction == kMean ? __fdiv_rn(sum, static_cast<float>(max(active, 1))) : sum;
 }
 
 // The backward's end: dhidden's slices added in order, scaled, rounded, each row to its place; zeros where a row
@@ -734,19 +769,23 @@ __global__ void __launch_bounds__(1024) xent_total_kernel(const float* __restric
 template <int OT>
 __global__ void __launch_bounds__(128) xent_spread_kernel(const float* __restrict__ slices, int splits, int64_t slice_rows,
                                                           int64_t ld, const int* __restrict__ place,
-                                                          const float* __restrict__ scale, int n, int width,
+                                                          const float* __restrict__ scale, int n, int width, int chunks,
                                                           unsigned char* __restrict__ out, int64_t ld_out) {
   griddep_wait();
   griddep_launch_dependents();
   const float times = *scale;
-  for (int r = blockIdx.x; r < n; r += gridDim.x) {
+  for (int64_t unit = blockIdx.x; unit < static_cast<int64_t>(n) * chunks; unit += gridDim.x) {
+    const int r = static_cast<int>(unit / chunks);
     const int c = place[r];
-    for (int x = threadIdx.x * 4; x < width; x += 128 * 4) {
+    const int x = (static_cast<int>(unit % chunks) * 128 + static_cast<int>(threadIdx.x)) * 4;
+    if (x < width) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (c >= 0) {
-        v = *reinterpret_cast<const float4*>(slices + c * ld + x);
+        const float* from = slices + c * ld + x;
+        v = *reinterpret_cast<const float4*>(from);
+#pragma unroll 8
         for (int s = 1; s < splits; ++s) {
-          const float4 w = *reinterpret_cast<const float4*>(slices + (s * slice_rows + c) * ld + x);
+          const float4 w = *reinterpret_cast<const float4*>(from + s * slice_rows * ld);
           v = make_float4(__fadd_rn(v.x, w.x), __fadd_rn(v.y, w.y), __fadd_rn(v.z, w.z), __fadd_rn(v.w, w.w));
         }
         v = make_float4(__fmul_rn(v.x, times), __fmul_rn(v.y, times), __fmul_rn(v.z, times), __fmul_rn(v.w, times));
@@ -801,10 +840,10 @@ int launch_gemm(GemmKernel kernel, const CUtensorMap& a, const CUtensorMap& b, c
   return launch_pdl(kernel, grid, kThreads, kSmemBytes, s, 2, a, b, c, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
-constexpr int kRowGroup = 16;  // row units of a raster group where the columns are the vocabulary
-
-// Row units of a raster group such that the pairs at work share every column tile of them.
-int column_group(int num_n, int pairs) { return std::max(1, pairs / std::max(1, num_n)); }
+// Row units of a raster group: of the products whose columns are the vocabulary, and of those whose columns are the
+// hidden size.  (16384 x 151936 x 4096: the forward 11.88 ms with 16, 12.54 with 8, 12.37 with 32; the backward is the
+// same within 1% with 4, 8 and 16.)
+constexpr int kRowGroup = 16, kColumnGroup = 8;
 
 // Slices of dhidden's product (its K is the piece): as many as give the pairs work.
 int dhidden_splits(int64_t n_rows, int64_t hidden_size, int pairs) {
@@ -812,9 +851,22 @@ int dhidden_splits(int64_t n_rows, int64_t hidden_size, int pairs) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, pairs / std::max<int64_t>(1, tiles))));
 }
 
-// Columns of a piece: the vocabulary, or what keeps dz below half a gigabyte (4096 at least).
-int64_t piece_columns(int64_t n_rows, int64_t vocab, int64_t piece) {
-  if (piece == 0) piece = std::max<int64_t>(4096, (int64_t(1) << 28) / std::max<int64_t>(1, n_rows));
+// Columns of a piece: the vocabulary, or what keeps dz within a gigabyte (4096 at least), in as many tiles as give
+// dweight's product whole rounds of the pairs.  (16384 x 151936 x 4096, the whole step: 47.8 ms in pieces of 9728,
+// 47.4 of 19456, 47.2 of 38912 columns: each piece adds to dhidden in float32, and ends three products.)
+int64_t piece_columns(int64_t n_rows, int64_t hidden_size, int64_t vocab, int64_t piece, int pairs) {
+  if (piece == 0) {
+    piece = (int64_t(1) << 29) / std::max<int64_t>(1, n_rows);
+    if (piece >= vocab) return up(vocab, kBN);
+    int64_t a = pairs, b = (hidden_size + kBN - 1) / kBN;
+    while (b != 0) {
+      const int64_t rest = a % b;
+      a = b;
+      b = rest;
+    }
+    const int64_t step = pairs / a * kBN;
+    piece = piece >= step ? piece / step * step : std::max<int64_t>(4096, piece / kBN * kBN);
+  }
   return up(std::min(piece, vocab), kBN);
 }
 
@@ -845,7 +897,7 @@ int bwd_layout(int64_t n, int64_t hidden_size, int64_t vocab, int64_t piece, Bwd
   int sms = 0, smem = 0;
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   l->padded = up(n, kUnitRows);
-  l->piece = piece_columns(n, vocab, piece);
+  l->piece = piece_columns(n, hidden_size, vocab, piece, sms / 2);
   l->splits = dhidden_splits(n, hidden_size, sms / 2);
   l->ld_slice = up(hidden_size, 8);
   l->rows = round256(static_cast<size_t>(l->padded) * 4);
@@ -881,13 +933,17 @@ int check_call(const void* hidden, const void* weight, int dtype, int64_t n, int
   return BIL_OK;
 }
 
-int launch_gather(const void* hidden, int64_t ld_hidden, int64_t hidden_size, const int* rows, const int* n_active, int n,
-                  void* out, cudaStream_t s) {
-  return launch_pdl(xent_gather_kernel, std::min<int64_t>(n, 1 << 20), 128, 0, s, 1,
-                    static_cast<const unsigned char*>(hidden), ld_hidden * 2, rows, n_active, n,
-                    static_cast<int>(hidden_size), static_cast<unsigned char*>(out)) == cudaSuccess
-             ? BIL_OK
-             : BIL_E_CUDA;
+// The lists and the copy of the rows that count.
+template <bool BWD>
+int launch_rows(const RowsParams& r, int sms, cudaStream_t s) {
+  const int blocks = std::min(r.n, sms);
+  if (r.n <= kRowsThreads * kRowsPer && (r.n + blocks - 1) / blocks <= kRowsShare)
+    return launch_pdl(xent_rows_kernel<BWD>, blocks, kRowsThreads, 0, s, 1, r) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+  RowsParams lists = r;
+  lists.compact = nullptr;
+  if (launch_pdl(xent_rows_kernel<BWD>, 1, kRowsThreads, 0, s, 1, lists) != cudaSuccess) return BIL_E_CUDA;
+  return launch_pdl(xent_gather_kernel, std::min<int64_t>(r.n, 1 << 20), 128, 0, s, 1, r) == cudaSuccess ? BIL_OK
+                                                                                                        : BIL_E_CUDA;
 }
 
 }  // namespace
@@ -955,8 +1011,14 @@ int bil_linear_cross_entropy_fwd(const void* hidden, const void* weight, int dty
   r.targets_out = reinterpret_cast<int*>(ws + 256 + l.rows);
   r.lse = lse;
   r.loss = reduction == kNone ? loss : nullptr;
-  if (launch_pdl(xent_rows_kernel<false>, 1, kRowsThreads, 0, s, 1, r) != cudaSuccess) return BIL_E_CUDA;
-  if (int st = launch_gather(hidden, ld_hidden, hidden_size, r.rows, r.n_active, r.n, compact, s)) return st;
+  r.hidden = static_cast<const unsigned char*>(hidden);
+  r.ld_bytes = ld_hidden * 2;
+  r.width = static_cast<int>(hidden_size);
+  r.compact = compact;
+  r.done = reinterpret_cast<unsigned*>(ws + 64);
+  int sms = 0, smem = 0;
+  if (int st = bil_internal::device_limits(&sms, &smem)) return st;
+  if (int st = launch_rows<false>(r, sms, s)) return st;
   GemmParams p{};
   p.n_active = r.n_active;
   p.m_rows = -1;
@@ -991,11 +1053,10 @@ int bil_linear_cross_entropy_fwd(const void* hidden, const void* weight, int dty
   j.lse = lse;
   j.loss = r.loss;
   j.row_loss = reinterpret_cast<float*>(ws + 256 + 3 * l.rows);
-  if (launch_pdl(xent_join_kernel, (n_rows + kLanes - 1) / kLanes, kJoinSlices * kLanes, 0, s, 1, j) != cudaSuccess)
-    return BIL_E_CUDA;
-  if (reduction == kNone) return BIL_OK;
-  return launch_pdl(xent_total_kernel, 1, 1024, 0, s, 1, static_cast<const float*>(j.row_loss), r.n_active,
-                    reduction == kMean ? 1 : 0, loss) == cudaSuccess
+  j.reduction = reduction;
+  j.total = loss;
+  j.done = r.done;
+  return launch_pdl(xent_join_kernel, (n_rows + kLanes - 1) / kLanes, kJoinSlices * kLanes, 0, s, 1, j) == cudaSuccess
              ? BIL_OK
              : BIL_E_CUDA;
 }
@@ -1084,8 +1145,11 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
   if (int st = operand_map(&m_hidden_mn, compact, dtype, hidden_size, n_rows, ld_compact, true, 0)) return st;
   if (int st = make_store_map(&m_slices, slices, BIL_F32, l.padded * l.splits, hidden_size, l.ld_slice)) return st;
 
-  if (launch_pdl(xent_rows_kernel<true>, 1, kRowsThreads, 0, s, 1, r) != cudaSuccess) return BIL_E_CUDA;
-  if (int st = launch_gather(hidden, ld_hidden, hidden_size, r.rows, r.n_active, r.n, compact, s)) return st;
+  r.hidden = static_cast<const unsigned char*>(hidden);
+  r.ld_bytes = ld_hidden * 2;
+  r.width = static_cast<int>(hidden_size);
+  r.compact = compact;
+  if (int st = launch_rows<true>(r, sms, s)) return st;
 
   const int64_t row_units = l.padded / kUnitRows;
   const int num_h = static_cast<int>((hidden_size + kBN - 1) / kBN);
@@ -1121,7 +1185,7 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
       p.num_n = num_h;
       p.k_blocks = static_cast<int>((cols + kBK - 1) / kBK);
       p.splits = l.splits;
-      p.m_group = column_group(num_h, sms / 2);
+      p.m_group = kColumnGroup;
       p.cols = hidden_size;
       p.b_mn = 1;
       p.idesc = pair_idesc(dtype, false, true);
@@ -1138,7 +1202,7 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
       p.num_n = num_h;
       p.k_blocks = -1;
       p.splits = 1;
-      p.m_group = column_group(num_h, sms / 2);
+      p.m_group = kColumnGroup;
       p.cols = hidden_size;
       p.a_mn = p.b_mn = 1;
       p.idesc = pair_idesc(dtype, true, true);
@@ -1155,9 +1219,10 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
   auto spread = dhidden_dtype == BIL_F32    ? xent_spread_kernel<BIL_F32>
                 : dhidden_dtype == BIL_BF16 ? xent_spread_kernel<BIL_BF16>
                                             : xent_spread_kernel<BIL_F16>;
-  return launch_pdl(spread, std::min<int64_t>(n_rows, 1 << 20), 128, 0, s, 1, static_cast<const float*>(slices), l.splits,
+  const int chunks = static_cast<int>((hidden_size + 511) / 512);  // of a row, a block each
+  return launch_pdl(spread, std::min<int64_t>(n_rows * chunks, 1 << 20), 128, 0, s, 1, static_cast<const float*>(slices), l.splits,
                     l.padded, l.ld_slice, static_cast<const int*>(r.place), static_cast<const float*>(r.scale), r.n,
-                    static_cast<int>(hidden_size), static_cast<unsigned char*>(dhidden), ld_dhidden) == cudaSuccess
+                    static_cast<int>(hidden_size), chunks, static_cast<unsigned char*>(dhidden), ld_dhidden) == cudaSuccess
              ? BIL_OK
              : BIL_E_CUDA;
 }

@@ -25,6 +25,13 @@ from .norm import _call, _check_width, _padded, _rows, _rows_like, _weight
 EPS = 1e-5
 
 
+def _vector(w: torch.Tensor, x: torch.Tensor, width: int, index: int) -> torch.Tensor:
+    if w.get_device() == index and w.shape == (width,) and w.dtype == x.dtype and w.is_contiguous() and w.data_ptr() % 16 == 0:
+        return w
+    _need_cuda(w)
+    return _weight(w, x, width)
+
+
 def _check_stats(t: torch.Tensor, what: str, n: int, index: int) -> torch.Tensor:
     if t.dtype != torch.float32 or t.numel() != n or t.get_device() != index:
         raise ValueError(f"{what} must be float32, one per row ({n})")
@@ -40,16 +47,15 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     index = x.get_device()
     if index < 0 or weight.get_device() < 0:
         _need_cuda(x, weight, bias, residual)
-    p, word, step, rng = _random(p, seed, offset, index)
+    p, word, step, rng = _random(p, seed, offset, index) if p else (0.0, 0, 0, None)
     x2, ld_x = _rows(x, "x")
     n, width = x2.shape
     _check_width(width)
     code = _code(x2.dtype)
-    w = _weight(weight, x2, width)
+    w = _vector(weight, x2, width, index)
     b_ptr = None
     if bias is not None:
-        _need_cuda(bias)
-        b = _weight(bias, x2, width)
+        b = _vector(bias, x2, width, index)
         if b.dtype != w.dtype:
             raise TypeError("bias must have weight's type")
         b_ptr = b.data_ptr()
@@ -98,13 +104,13 @@ def layer_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, mean
     index = h.get_device()
     if index < 0 or dy.get_device() < 0 or weight.get_device() < 0 or mean.get_device() < 0 or rstd.get_device() < 0:
         _need_cuda(dy, h, weight, mean, rstd)
-    p, word, step, rng = _random(p, seed, offset, index)
+    p, word, step, rng = _random(p, seed, offset, index) if p else (0.0, 0, 0, None)
     h2, ld_h = _rows(h, "h")
     n, width = h2.shape
     _check_width(width)
     d2, ld_dy = _rows_like(dy, "dy", h)
     code = _code(h2.dtype)
-    w = _weight(weight, h2, width)
+    w = _vector(weight, h2, width, index)
     mean, rstd = _check_stats(mean, "mean", n, index), _check_stats(rstd, "rstd", n, index)
     g2, ld_g, g_ptr = None, 0, None
     if grad_h is not None:

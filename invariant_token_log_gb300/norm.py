@@ -76,8 +76,13 @@ def _check_width(width: int) -> None:
         raise ValueError(f"rows of {width} elements; the norm takes 1 to {_lib.MAX_NORM_WIDTH}")
 
 
+_functions: dict = {}  # of the library, by name
+
+
 def _call(name: str, index: int, *args) -> None:
-    fn = getattr(_lib.load(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
     st = fn(*args) if _get_device() == index else _on_device(index, fn, *args)
     if st:
         _lib.check(name, st)
