@@ -30,7 +30,9 @@
 //   warp 0      copies: this block's 128 rows of A and 128 of B (K-major in one box,
 //               MN-major in two of 64);
 //   warp 1      of the pair's first block: issues the products;
-//   warps 2-9   epilogue: a quarter of the block's rows and half of the columns each.
+//   warps 2-9   epilogue: a quarter of the block's rows and half of the columns each;
+//               what it stores goes through two boxes of 32 128-byte lines a warp and TMA
+//               (a stage of the ring is theirs).
 
 #include "launch.cuh"
 #include "tc_device.cuh"
@@ -48,27 +50,31 @@ constexpr unsigned kWatchStageFree = 64u;
 constexpr unsigned kWatchMma = 128u;
 constexpr unsigned kWatchOwnDrain = 256u;
 
-constexpr int kStages = 6;
+constexpr int kMaxStages = 6;
 constexpr unsigned kStageBytes = 2 * kStageABytes;  // 128 rows of A, 128 of B
 constexpr int kUnitRows = 2 * kBM;                  // of a pair
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kHalf = kBN / 2;                      // columns of an epilogue warp
-constexpr uint32_t kStagingBytes = 2 * kStoreBoxBytes;  // of a warp
+constexpr uint32_t kBoxBytes = 32 * 128;            // of a store: 32 rows of a 128-byte line
+constexpr uint32_t kStagingBytes = 2 * kBoxBytes;   // of a warp
 
 struct alignas(8) PairSmem {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmemBytes = 1024 + kStages * size_t(kStageBytes) + kEpiWarps * size_t(kStagingBytes) + sizeof(PairSmem);
-static_assert(kSmemBytes <= 227 * 1024, "a block's shared memory");
 
-enum Epilogue { kStats = 0, kGrad = 1, kStore = 2 };
+// kProducts: two products in one launch, dhidden's (float32, stored or added to what is there) and dweight's.
+enum Epilogue { kStats = 0, kGrad = 1, kProducts = 2 };
+constexpr size_t kRingBytes = (kMaxStages - 1) * size_t(kStageBytes) + kEpiWarps * size_t(kStagingBytes);
+static_assert(kRingBytes >= kMaxStages * size_t(kStageBytes), "either layout");
+constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(PairSmem);
+static_assert(kSmemBytes <= 227 * 1024, "a block's shared memory");
 
 struct GemmParams {
   const int* n_active;   // rows of hidden that count
@@ -79,7 +85,6 @@ struct GemmParams {
   int m_group;           // row units of a raster group
   int64_t cols;          // columns of C
   int c_rows;            // rows of it (of a slice) that may be stored
-  int a_mn, b_mn;
   uint32_t idesc;
   const int* targets;    // of the rows that count: the target, -1 for none
   int64_t col0;          // vocabulary column of column 0
@@ -91,9 +96,10 @@ struct GemmParams {
   float* target_logit;
   // kGrad
   const float4* coef;    // of a row: a, b, c, lse:  dz = a exp(z - lse) - c - [c = t] b
-  // kStore
+  // kProducts
   const float* scale;    // NULL: 1
   int slice_rows;
+  int add;
 };
 
 __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -106,26 +112,30 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// As store_box, added to what is there.
+// As tma_store_2d, added to what is there.
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, int c0, int c1, const void* src) {
   asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1), "r"(smem_u32(src))
                : "memory");
 }
-template <bool ADD>
+// A warp's box of 32 rows of 128 bytes, a lane's row in eight 16-byte words which lie
+// where TMA's 128-byte swizzle has them (word j of row i at j ^ (i mod 8): eight lanes'
+// writes meet eight different banks), handed to TMA for column x, row y.  Two buffers
+// in turn.
 __device__ __forceinline__ void put_box(unsigned char* staging, const CUtensorMap* map, int x, int y, int lane,
-                                        uint32_t& issued, const uint32_t (&w)[16]) {
-  unsigned char* box = staging + (issued & 1u) * kStoreBoxBytes;
+                                        uint32_t& issued, const uint32_t (&w)[32], bool add) {
+  unsigned char* box = staging + (issued & 1u) * kBoxBytes;
   if (lane == 0) bulk_wait_read_1();
   __syncwarp();
-  uint4* dst = reinterpret_cast<uint4*>(box + lane * 64);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (ADD)
+    if (add)
       tma_add_2d(map, x, y, box);
     else
       tma_store_2d(map, x, y, box);
@@ -148,10 +158,10 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 
 // What a launch works on, from the number of rows that count.
 struct Shape {
-  int m_rows, num_m, k_blocks, k_split;
+  int active, m_rows, num_m, k_blocks, k_split;
   int64_t per_split, total;
   __device__ __forceinline__ explicit Shape(const GemmParams& p) {
-    const int active = *p.n_active;
+    active = *p.n_active;
     m_rows = p.m_rows < 0 ? active : p.m_rows;
     num_m = (m_rows + kUnitRows - 1) / kUnitRows;
     k_blocks = p.k_blocks < 0 ? (active + kBK - 1) / kBK : p.k_blocks;
@@ -212,16 +222,22 @@ __device__ __forceinline__ void half_stats(const uint32_t (&r)[4][kChunk], int v
   zs = SUM ? __fadd_rn(lo_of(z), hi_of(z)) : 0.0f;
 }
 
-// EPI with FLAG: kStats the sums of z, kStore adding to C.  DT: the 16-bit type of dz, or C's type.
-template <int EPI, bool FLAG, int DT>
+struct Maps {
+  CUtensorMap a, b, c;
+};
+
+// SUM: kStats the sums of z too.  DT: the 16-bit type of dz, or dweight's type.  The second product (kProducts alone)
+// has its units behind the first's; the first's A is K-major, all else that kProducts reads MN-major.
+template <int EPI, bool SUM, int DT>
 __global__ void __launch_bounds__(kThreads, 1)
-    xent_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                     const __grid_constant__ CUtensorMap tmap_c, const GemmParams p) {
+    xent_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Maps maps2, const GemmParams p,
+                     const GemmParams p2) {
+  constexpr int kStages = EPI == kStats ? kMaxStages : kMaxStages - 1;  // the last is the boxes'
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* staging = base + kStages * size_t(kStageBytes);
-  PairSmem& sm = *reinterpret_cast<PairSmem*>(staging + kEpiWarps * size_t(kStagingBytes));
+  unsigned char* staging = base + kStages * size_t(kStageBytes);  // (kStats: none)
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(base + kRingBytes);
   volatile int* abort = &sm.abort;
   const int warp = threadIdx.x / kLanes;
   const int lane = threadIdx.x % kLanes;
@@ -255,7 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   asm volatile("fence.proxy.async;" ::: "memory");  // what the kernels before stored, before TMA reads it
 
-  const Shape shape(p);
+  const Shape shape(p), shape2(p2);
+  const int64_t total = shape.total + (EPI == kProducts ? shape2.total : 0);
+  auto unit = [&](int64_t u, int& m, int& n, int& split, int& k0, int& k1) {  // true: of the second product
+    const bool second = EPI == kProducts && u >= shape.total;
+    if (second)
+      shape2.unit(p2, u - shape.total, m, n, split, k0, k1);
+    else
+      shape.unit(p, u, m, n, split, k0, k1);
+    return second;
+  };
   const int64_t pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (warp == 0) {
@@ -263,9 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- this block's half of the pair's copies ----
       int64_t it = 0;
       bool ok = true;
-      for (int64_t u = pair0; u < shape.total && ok; u += pairs) {
+      for (int64_t u = pair0; u < total && ok; u += pairs) {
         int m, n, split, k0, k1;
-        shape.unit(p, u, m, n, split, k0, k1);
+        const bool second = unit(u, m, n, split, k0, k1);
+        const CUtensorMap* tmap_a = second ? &maps2.a : &maps.a;
+        const CUtensorMap* tmap_b = second ? &maps2.b : &maps.b;
         const int a_row = (2 * m + rank) * kBM, b_row = n * kBN + rank * kHalf;
         for (int kb = k0; kb < k1; ++kb, ++it) {
           const int s = static_cast<int>(it % kStages);
@@ -278,17 +305,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kStageBytes);
           unsigned char* a_dst = base + s * size_t(kStageBytes);
           unsigned char* b_dst = a_dst + kStageABytes;
-          if (p.a_mn) {
-            tma_load_2d_pair(a_dst, &tmap_a, a_row, kb * kBK, bar);
-            tma_load_2d_pair(a_dst + kMnBoxBytes, &tmap_a, a_row + kMnBox, kb * kBK, bar);
+          if (second) {
+            tma_load_2d_pair(a_dst, tmap_a, a_row, kb * kBK, bar);
+            tma_load_2d_pair(a_dst + kMnBoxBytes, tmap_a, a_row + kMnBox, kb * kBK, bar);
           } else {
-            tma_load_2d_pair(a_dst, &tmap_a, kb * kBK, a_row, bar);
+            tma_load_2d_pair(a_dst, tmap_a, kb * kBK, a_row, bar);
           }
-          if (p.b_mn) {
-            tma_load_2d_pair(b_dst, &tmap_b, b_row, kb * kBK, bar);
-            tma_load_2d_pair(b_dst + kMnBoxBytes, &tmap_b, b_row + kMnBox, kb * kBK, bar);
+          if (EPI == kProducts) {
+            tma_load_2d_pair(b_dst, tmap_b, b_row, kb * kBK, bar);
+            tma_load_2d_pair(b_dst + kMnBoxBytes, tmap_b, b_row + kMnBox, kb * kBK, bar);
           } else {
-            tma_load_2d_pair(b_dst, &tmap_b, kb * kBK, b_row, bar);
+            tma_load_2d_pair(b_dst, tmap_b, kb * kBK, b_row, bar);
           }
         }
       }
@@ -315,9 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t it = 0;
       int local = 0;
       bool ok = true;
-      for (int64_t u = pair0; u < shape.total && ok; u += pairs, ++local) {
+      for (int64_t u = pair0; u < total && ok; u += pairs, ++local) {
         int m, n, split, k0, k1;
-        shape.unit(p, u, m, n, split, k0, k1);
+        const bool second = unit(u, m, n, split, k0, k1);
+        const uint32_t idesc = second ? p2.idesc : p.idesc;
         const int b = local & 1;
         const unsigned use = static_cast<unsigned>(local >> 1);
         if (!thread_wait_cluster_watch(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma, &g_watchdog_xent)) break;
@@ -335,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBK / kUmmaK; ++k) {
             // a K step: 32 bytes along a K-major line, 16 lines of an MN-major box
-            const uint64_t adesc = p.a_mn ? smem_desc_mn(a_addr + k * kUmmaK * 128) : smem_desc(a_addr + k * kUmmaK * 2);
-            const uint64_t bdesc = p.b_mn ? smem_desc_mn(b_addr + k * kUmmaK * 128) : smem_desc(b_addr + k * kUmmaK * 2);
-            umma_f16_pair(d_tmem, adesc, bdesc, p.idesc, kb != k0 || k != 0 ? 1u : 0u);
+            const uint64_t adesc = second ? smem_desc_mn(a_addr + k * kUmmaK * 128) : smem_desc(a_addr + k * kUmmaK * 2);
+            const uint64_t bdesc = EPI == kProducts ? smem_desc_mn(b_addr + k * kUmmaK * 128) : smem_desc(b_addr + k * kUmmaK * 2);
+            umma_f16_pair(d_tmem, adesc, bdesc, idesc, kb != k0 || k != 0 ? 1u : 0u);
           }
           umma_commit_pair(&sm.empty[s]);
         }
@@ -351,12 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- epilogue: a quarter of this block's 128 rows, half of the columns ----
     const int q = warp & 3, half = (warp - 2) / 4;
     unsigned char* boxes = staging + (warp - 2) * size_t(kStagingBytes);
-    const float scale = EPI == kStore && p.scale != nullptr ? *p.scale : 1.0f;
+    const float scale2 = EPI == kProducts ? *p2.scale : 1.0f;
     int local = 0;
     uint32_t issued = 0;
-    for (int64_t u = pair0; u < shape.total; u += pairs, ++local) {
+    for (int64_t u = pair0; u < total; u += pairs, ++local) {
       int m, n, split, k0, k1;
-      shape.unit(p, u, m, n, split, k0, k1);
+      const bool second = unit(u, m, n, split, k0, k1);
       const int b = local & 1;
       const unsigned use = static_cast<unsigned>(local >> 1);
       const int row0 = (2 * m + rank) * kBM + q * 32, row = row0 + lane;
@@ -374,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float4 coef = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       int tcol = -1;  // the target's column in this warp's half
-      if constexpr (EPI != kStore) {
+      if constexpr (EPI != kProducts) {
         if (row < shape.m_rows) {
           if (EPI == kGrad) coef = p.coef[row];
           const int64_t t = p.targets[row];
@@ -402,35 +430,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx, s, zs;
         if (vcols == kHalf)
-          half_stats<FLAG, false>(r, vcols, mx, s, zs);
+          half_stats<SUM, false>(r, vcols, mx, s, zs);
         else
-          half_stats<FLAG, true>(r, vcols, mx, s, zs);
+          half_stats<SUM, true>(r, vcols, mx, s, zs);
         if (row < shape.m_rows) {
           const int64_t at = (2 * static_cast<int64_t>(n) + half) * p.ld_part + row;
           p.part_max[at] = mx;
           p.part_sum[at] = s;
-          if (FLAG) p.part_z[at] = zs;
+          if (SUM) p.part_z[at] = zs;
         }
       } else {
         // dz has zeros up to the end of a K block of the rows, which the product with them reads.
-        const int rows = min(p.c_rows, EPI == kGrad ? (shape.m_rows + kBK - 1) / kBK * kBK : shape.m_rows);
+        const int rows = EPI == kGrad ? min(p.c_rows, (shape.m_rows + kBK - 1) / kBK * kBK)
+                                      : second ? shape2.m_rows : shape.m_rows;
         const int chunks = vcols <= 0 || row0 >= rows ? 0 : (vcols + kChunk - 1) / kChunk;
         const bool none = EPI == kGrad && coef.x == 0.0f && coef.y == 0.0f && coef.z == 0.0f;
-#pragma unroll 1
+        const bool wide = EPI == kProducts && (DT == BIL_F32 || !second);  // 32 columns a box, not 64
+        const int x0 = static_cast<int>(first), y = (second ? 0 : split * p.slice_rows) + row0;
+        uint32_t w[32];
+#pragma unroll
         for (int c = 0; c < kHalf / kChunk; ++c) {
           uint32_t r[kChunk];
-          if (EPI == kStore && k0 >= k1) {  // a sum over nothing
+          if (EPI == kProducts && k0 >= k1) {  // a sum over nothing
 #pragma unroll
             for (int j = 0; j < kChunk; ++j) r[j] = 0u;
           } else {
             tmem_ld32(taddr + c * kChunk, r);
           }
           if (c == kHalf / kChunk - 1) release();
-          if (c >= chunks) continue;
-          const int x = static_cast<int>(first) + c * kChunk, y = split * p.slice_rows + row0;
+          if (c >= chunks + (wide ? 0 : chunks & 1)) continue;  // (a box begun is filled)
           if constexpr (EPI == kGrad) {
             const int t = tcol - c * kChunk;
-            uint32_t w[kChunk / 2];
 #pragma unroll
             for (int j = 0; j < kChunk; j += 2) {
               float d[2];
@@ -441,27 +471,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j + k == t) d[k] = __fsub_rn(d[k], coef.y);
                 if (none) d[k] = 0.0f;
               }
-              w[j / 2] = pack16<DT>(d[0], d[1]);
+              w[c % 2 * 16 + j / 2] = pack16<DT>(d[0], d[1]);
             }
-            put_box<false>(boxes, &tmap_c, x, y, lane, issued, w);
+            if (c % 2 == 1) put_box(boxes, &maps.c, x0 + (c - 1) * kChunk, y, lane, issued, w, false);
+          } else if (!second) {
+            put_box(boxes, &maps.c, x0 + c * kChunk, y, lane, issued, r, p.add != 0);
+          } else if constexpr (DT == BIL_F32) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) w[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[j]), scale2));
+            put_box(boxes, &maps2.c, x0 + c * kChunk, y, lane, issued, w, false);
           } else {
-            if (DT == BIL_F32) {
-              uint32_t w[16];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (h * 16 + c * kChunk >= vcols) break;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  w[j] = __float_as_uint(__fmul_rn(__uint_as_float(r[h * 16 + j]), scale));
-                put_box<FLAG>(boxes, &tmap_c, x + h * 16, y, lane, issued, w);
-              }
-            } else {
-              uint32_t w[kChunk / 2];
-#pragma unroll
-              for (int j = 0; j < kChunk; j += 2)
-                w[j / 2] = pack16<DT>(__fmul_rn(__uint_as_float(r[j]), scale), __fmul_rn(__uint_as_float(r[j + 1]), scale));
-              put_box<FLAG>(boxes, &tmap_c, x, y, lane, issued, w);
-            }
+            for (int j = 0; j < kChunk; j += 2)
+              w[c % 2 * 16 + j / 2] =
+                  pack16<DT>(__fmul_rn(__uint_as_float(r[j]), scale2), __fmul_rn(__uint_as_float(r[j + 1]), scale2));
+            if (c % 2 == 1) put_box(boxes, &maps2.c, x0 + (c - 1) * kChunk, y, lane, issued, w, false);
           }
         }
       }
@@ -826,10 +850,28 @@ uint32_t pair_idesc(int dtype, bool a_mn, bool b_mn) {
          (static_cast<uint32_t>(kBN >> 3) << 17) | (static_cast<uint32_t>(kUnitRows >> 4) << 24);
 }
 
-typedef void (*GemmKernel)(CUtensorMap, CUtensorMap, CUtensorMap, GemmParams);
+// The map of put_box's boxes: 32 rows of 128 bytes.
+int make_box_map(CUtensorMap* map, void* ptr, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return BIL_E_CUDA;
+  const int eb = dtype == BIL_F32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * eb};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / eb), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType dt = dtype == BIL_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : dtype == BIL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(map, dt, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? BIL_OK
+             : BIL_E_CUDA;
+}
+
+typedef void (*GemmKernel)(Maps, Maps, GemmParams, GemmParams);
 
 // units: the launch's work at most.
-int launch_gemm(GemmKernel kernel, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const GemmParams& p,
+int launch_gemm(GemmKernel kernel, const Maps& maps, const Maps& maps2, const GemmParams& p, const GemmParams& p2,
                 int64_t units, cudaStream_t s) {
   int sms = 0, smem_optin = 0;
   if (int st = bil_internal::device_limits(&sms, &smem_optin)) return st;
@@ -837,7 +879,7 @@ int launch_gemm(GemmKernel kernel, const CUtensorMap& a, const CUtensorMap& b, c
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) != cudaSuccess)
     return BIL_E_CUDA;
   const int64_t grid = 2 * std::max<int64_t>(1, std::min<int64_t>(units, sms / 2));
-  return launch_pdl(kernel, grid, kThreads, kSmemBytes, s, 2, a, b, c, p) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
+  return launch_pdl(kernel, grid, kThreads, kSmemBytes, s, 2, maps, maps2, p, p2) == cudaSuccess ? BIL_OK : BIL_E_CUDA;
 }
 
 // Row units of a raster group: of the products whose columns are the vocabulary, and of those whose columns are the
@@ -997,9 +1039,10 @@ int bil_linear_cross_entropy_fwd(const void* hidden, const void* weight, int dty
   }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   unsigned char* compact = ws + 256 + 4 * l.rows;
-  CUtensorMap ma, mb;
-  if (int st = make_map(&ma, compact, dtype, n_rows, hidden_size, up(hidden_size, 8), kBM)) return st;
-  if (int st = make_map(&mb, weight, dtype, vocab, hidden_size, ld_weight, kHalf)) return st;
+  Maps maps;
+  if (int st = make_map(&maps.a, compact, dtype, n_rows, hidden_size, up(hidden_size, 8), kBM)) return st;
+  if (int st = make_map(&maps.b, weight, dtype, vocab, hidden_size, ld_weight, kHalf)) return st;
+  maps.c = maps.b;  // not used
   RowsParams r{};
   r.targets = target_ids;
   r.ignore_index = ignore_index;
@@ -1034,7 +1077,7 @@ int bil_linear_cross_entropy_fwd(const void* hidden, const void* weight, int dty
   p.part_z = smooth ? reinterpret_cast<float*>(ws + l.at_part + 2 * l.part) : nullptr;
   p.ld_part = l.padded;
   p.target_logit = reinterpret_cast<float*>(ws + 256 + 2 * l.rows);
-  if (int st = launch_gemm(smooth ? xent_gemm_kernel<kStats, true, 0> : xent_gemm_kernel<kStats, false, 0>, ma, mb, mb, p,
+  if (int st = launch_gemm(smooth ? xent_gemm_kernel<kStats, true, 0> : xent_gemm_kernel<kStats, false, 0>, maps, maps, p, p,
                            l.padded / kUnitRows * p.num_n, s))
     return st;
   JoinParams j{};
@@ -1139,11 +1182,11 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
   r.z_loss = z_loss;
   const int64_t ld_compact = up(hidden_size, 8);
 
-  // Of every piece: hidden (K-major and MN-major), and dhidden's slices.
-  CUtensorMap m_hidden, m_hidden_mn, m_slices;
-  if (int st = make_map(&m_hidden, compact, dtype, n_rows, hidden_size, ld_compact, kBM)) return st;
-  if (int st = operand_map(&m_hidden_mn, compact, dtype, hidden_size, n_rows, ld_compact, true, 0)) return st;
-  if (int st = make_store_map(&m_slices, slices, BIL_F32, l.padded * l.splits, hidden_size, l.ld_slice)) return st;
+  // Of every piece: hidden, and dhidden's slices.
+  Maps grad, dh, dw;
+  if (int st = make_map(&grad.a, compact, dtype, n_rows, hidden_size, ld_compact, kBM)) return st;
+  if (int st = operand_map(&dw.b, compact, dtype, hidden_size, n_rows, ld_compact, true, 0)) return st;
+  if (int st = make_box_map(&dh.c, slices, BIL_F32, l.padded * l.splits, hidden_size, l.ld_slice)) return st;
 
   r.hidden = static_cast<const unsigned char*>(hidden);
   r.ld_bytes = ld_hidden * 2;
@@ -1157,63 +1200,55 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
     const int64_t cols = std::min(l.piece, vocab - col0);
     const int num_v = static_cast<int>((cols + kBN - 1) / kBN);
     const unsigned char* w = static_cast<const unsigned char*>(weight) + col0 * ld_weight * 2;
-    CUtensorMap m_weight, m_weight_mn, m_dz_out, m_dz, m_dz_mn;
-    if (int st = make_map(&m_weight, w, dtype, cols, hidden_size, ld_weight, kHalf)) return st;
-    if (int st = operand_map(&m_weight_mn, w, dtype, hidden_size, cols, ld_weight, true, 0)) return st;
-    if (int st = make_store_map(&m_dz_out, dz, dtype, n_rows, cols, l.piece)) return st;
-    if (int st = make_map(&m_dz, dz, dtype, n_rows, cols, l.piece, kBM)) return st;
-    if (int st = operand_map(&m_dz_mn, dz, dtype, cols, n_rows, l.piece, true, 0)) return st;
+    if (int st = make_map(&grad.b, w, dtype, cols, hidden_size, ld_weight, kHalf)) return st;
+    if (int st = make_box_map(&grad.c, dz, dtype, n_rows, cols, l.piece)) return st;
+    if (int st = make_map(&dh.a, dz, dtype, n_rows, cols, l.piece, kBM)) return st;
+    if (int st = operand_map(&dh.b, w, dtype, hidden_size, cols, ld_weight, true, 0)) return st;
+    if (int st = operand_map(&dw.a, dz, dtype, cols, n_rows, l.piece, true, 0)) return st;
+    dw.c = dw.a;
+    if (dweight != nullptr) {
+      unsigned char* out = static_cast<unsigned char*>(dweight) + col0 * ld_dweight * ew;
+      if (int st = make_box_map(&dw.c, out, dweight_dtype, cols, hidden_size, ld_dweight)) return st;
+    }
     GemmParams p{};
     p.n_active = r.n_active;
-    // the piece's dz
-    p.m_rows = -1;
-    p.num_n = num_v;
-    p.k_blocks = static_cast<int>((hidden_size + kBK - 1) / kBK);
     p.splits = 1;
-    p.m_group = kRowGroup;
-    p.cols = cols;
-    p.c_rows = r.n;
-    p.idesc = pair_idesc(dtype, false, false);
-    p.targets = r.targets_out;
-    p.col0 = col0;
-    p.coef = r.coef;
+    // the piece's dz
+    GemmParams z = p;
+    z.m_rows = -1;
+    z.num_n = num_v;
+    z.k_blocks = static_cast<int>((hidden_size + kBK - 1) / kBK);
+    z.m_group = kRowGroup;
+    z.cols = cols;
+    z.c_rows = r.n;
+    z.idesc = pair_idesc(dtype, false, false);
+    z.targets = r.targets_out;
+    z.col0 = col0;
+    z.coef = r.coef;
     if (int st = launch_gemm(dtype == BIL_BF16 ? xent_gemm_kernel<kGrad, false, BIL_BF16>
                                                : xent_gemm_kernel<kGrad, false, BIL_F16>,
-                             m_hidden, m_weight, m_dz_out, p, row_units * num_v, s))
+                             grad, grad, z, z, row_units * num_v, s))
       return st;
-    if (dhidden != nullptr) {  // dz . weight, K the piece's columns
-      p.num_n = num_h;
-      p.k_blocks = static_cast<int>((cols + kBK - 1) / kBK);
-      p.splits = l.splits;
-      p.m_group = kColumnGroup;
-      p.cols = hidden_size;
-      p.b_mn = 1;
-      p.idesc = pair_idesc(dtype, false, true);
-      p.slice_rows = p.c_rows = static_cast<int>(l.padded);
-      if (int st = launch_gemm(col0 == 0 ? xent_gemm_kernel<kStore, false, BIL_F32> : xent_gemm_kernel<kStore, true, BIL_F32>,
-                               m_dz, m_weight_mn, m_slices, p, row_units * num_h * l.splits, s))
-        return st;
-    }
-    if (dweight != nullptr) {  // dz^T . hidden, K the rows
-      CUtensorMap m_out;
-      unsigned char* out = static_cast<unsigned char*>(dweight) + col0 * ld_dweight * ew;
-      if (int st = make_store_map(&m_out, out, dweight_dtype, cols, hidden_size, ld_dweight)) return st;
-      p.m_rows = static_cast<int>(cols);
-      p.num_n = num_h;
-      p.k_blocks = -1;
-      p.splits = 1;
-      p.m_group = kColumnGroup;
-      p.cols = hidden_size;
-      p.a_mn = p.b_mn = 1;
-      p.idesc = pair_idesc(dtype, true, true);
-      p.scale = r.scale;
-      p.slice_rows = 0;
-      p.c_rows = p.m_rows;
-      GemmKernel k = dweight_dtype == BIL_F32    ? xent_gemm_kernel<kStore, false, BIL_F32>
-                     : dweight_dtype == BIL_BF16 ? xent_gemm_kernel<kStore, false, BIL_BF16>
-                                                 : xent_gemm_kernel<kStore, false, BIL_F16>;
-      if (int st = launch_gemm(k, m_dz_mn, m_hidden_mn, m_out, p, static_cast<int64_t>(num_v) * num_h, s)) return st;
-    }
+    // dz . weight, K the piece's columns, and dz^T . hidden, K the rows
+    p.num_n = num_h;
+    p.m_group = kColumnGroup;
+    p.cols = hidden_size;
+    p.scale = r.scale;
+    GemmParams p2 = p;
+    p.m_rows = dhidden != nullptr ? -1 : 0;
+    p.k_blocks = static_cast<int>((cols + kBK - 1) / kBK);
+    p.splits = l.splits;
+    p.idesc = pair_idesc(dtype, false, true);
+    p.slice_rows = static_cast<int>(l.padded);
+    p.add = col0 != 0;
+    p2.m_rows = dweight != nullptr ? static_cast<int>(cols) : 0;
+    p2.k_blocks = -1;
+    p2.idesc = pair_idesc(dtype, true, true);
+    GemmKernel k = dweight == nullptr || dweight_dtype == BIL_F32 ? xent_gemm_kernel<kProducts, false, BIL_F32>
+                   : dweight_dtype == BIL_BF16                   ? xent_gemm_kernel<kProducts, false, BIL_BF16>
+                                                                 : xent_gemm_kernel<kProducts, false, BIL_F16>;
+    if (int st = launch_gemm(k, dh, dw, p, p2, row_units * num_h * l.splits + static_cast<int64_t>(num_v) * num_h, s))
+      return st;
   }
   if (dhidden == nullptr) return BIL_OK;
   auto spread = dhidden_dtype == BIL_F32    ? xent_spread_kernel<BIL_F32>
