@@ -32,6 +32,19 @@ def _vector(w: torch.Tensor, x: torch.Tensor, width: int, index: int) -> torch.T
     return _weight(w, x, width)
 
 
+def _plain(x, weight, bias, residual, index) -> bool:
+    """Whether a call needs no copy, no padded output and no conversion."""
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or not x.is_contiguous() or shape[1] % 8 or not 0 < shape[1] <= _lib.MAX_NORM_WIDTH:
+        return False
+    for v in (weight, bias):
+        if v is not None and (v.dtype != dtype or v.shape != shape[1:] or v.get_device() != index or not v.is_contiguous() or
+                              v.data_ptr() % 16):
+            return False
+    return residual is None or (residual.shape == shape and residual.dtype == dtype and residual.get_device() == index and
+                                residual.is_contiguous())
+
+
 def _check_stats(t: torch.Tensor, what: str, n: int, index: int) -> torch.Tensor:
     if t.dtype != torch.float32 or t.numel() != n or t.get_device() != index:
         raise ValueError(f"{what} must be float32, one per row ({n})")
@@ -45,6 +58,23 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     (the stream that goes on; None without a residual and dropout, where it is x) and
     the float32 mean and rstd [*lead] that ``layer_norm_bwd`` takes."""
     index = x.get_device()
+    if not p and index >= 0 and _plain(x, weight, bias, residual, index):
+        # The common call, row-major [N, H] of whole 16-byte units and vectors of its type, without the general path's
+        # checks: the per-call host time is what bounds a few rows.
+        n, width = x.shape
+        code = _code(x.dtype)
+        y = torch.empty_like(x)
+        h, h_ptr, r_ptr = None, None, None
+        if residual is not None:
+            h = torch.empty_like(x)
+            h_ptr, r_ptr = h.data_ptr(), residual.data_ptr()
+        dev = _DEVICE_OBJECTS.get(index) or _device_object(index)
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+        _call("bil_layer_norm_fwd", index, x.data_ptr(), r_ptr, weight.data_ptr(), None if bias is None else bias.data_ptr(),
+              code, code, n, width, width, width, float(eps), 0.0, 0, 0, None, y.data_ptr(), width, h_ptr, width,
+              mean.data_ptr(), rstd.data_ptr(), _stream_handle(index))
+        return y, h, mean, rstd
     if index < 0 or weight.get_device() < 0:
         _need_cuda(x, weight, bias, residual)
     p, word, step, rng = _random(p, seed, offset, index) if p else (0.0, 0, 0, None)
