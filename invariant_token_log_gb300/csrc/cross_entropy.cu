@@ -886,10 +886,27 @@ int launch_gemm(GemmKernel kernel, const Maps& maps, const Maps& maps2, const Ge
 // same within 1% with 4, 8 and 16.)
 constexpr int kRowGroup = 16, kColumnGroup = 8;
 
-// Slices of dhidden's product (its K is the piece): as many as give the pairs work.
-int dhidden_splits(int64_t n_rows, int64_t hidden_size, int pairs) {
+// Slices of dhidden's product (its K is the piece): those that take the least time, in cycles of 512 for a K block of
+// a unit and 3500 bytes for the slices' traffic (written, and read or added to, for each piece), if that is 5% less
+// than one slice takes.  Few rows make few units: 64 x 32003 x 1104 has 5 of 501 K blocks for 76 pairs, in 15 slices
+// 75 of 34; 2048 x 151936 x 4096 has 128, two rounds of 76, in 4 slices 512, seven rounds a quarter as long.
+int dhidden_splits(int64_t n_rows, int64_t hidden_size, int64_t vocab, int64_t piece, int pairs) {
   const int64_t tiles = (n_rows + kUnitRows - 1) / kUnitRows * ((hidden_size + kBN - 1) / kBN);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, pairs / std::max<int64_t>(1, tiles))));
+  const int64_t k_blocks = (std::min(piece, vocab) + kBK - 1) / kBK;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 16 && s <= k_blocks; ++s) {
+    const double rounds = static_cast<double>((tiles * s + pairs - 1) / pairs);
+    const double cycles = rounds * static_cast<double>((k_blocks + s - 1) / s) * 512.0 +
+                          s * static_cast<double>(n_rows) * static_cast<double>(hidden_size) * 8.0 / 3500.0;
+    if (s == 1)
+      least = 0.95 * cycles;
+    else if (cycles < least) {
+      least = cycles;
+      best = s;
+    }
+  }
+  return best;
 }
 
 // Columns of a piece: the vocabulary, or what keeps dz within a gigabyte (4096 at least), in as many tiles as give
@@ -939,7 +956,7 @@ int bwd_layout(int64_t n, int64_t hidden_size, int64_t vocab, int64_t piece, Bwd
   if (int st = bil_internal::device_limits(&sms, &smem)) return st;
   l->padded = up(n, kUnitRows);
   l->piece = piece_columns(n, hidden_size, vocab, piece, sms / 2);
-  l->splits = dhidden_splits(n, hidden_size, sms / 2);
+  l->splits = dhidden_splits(n, hidden_size, vocab, l->piece, sms / 2);
   l->ld_slice = up(hidden_size, 8);
   l->rows = round256(static_cast<size_t>(l->padded) * 4);
   l->coef = round256(static_cast<size_t>(l->padded) * sizeof(float4));
