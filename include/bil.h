@@ -689,8 +689,9 @@ int bil_embedding_bwd_workspace_bytes(int64_t n, int64_t width, int64_t *bytes);
  *
  *  dy            [n, ld_dy] of dtype.
  *  padding_idx   -1: none.
- *  dweight       [vocab, ld_dweight] of dweight_dtype, dtype or BIL_F32.  Rows
- *                without a token are set to zero, or (accumulate) left alone.
+ *  dweight       [vocab, ld_dweight] of dweight_dtype, dtype or BIL_F32; not dy's
+ *                buffer (refused).  Rows without a token are set to zero, or
+ *                (accumulate) left alone.
  *  workspace     256-byte aligned device memory of at least
  *                bil_embedding_bwd_workspace_bytes bytes; two calls in flight at
  *                once need two.
@@ -767,7 +768,8 @@ int bil_linear_cross_entropy_bwd_workspace_bytes(int64_t n_rows, int64_t hidden_
  *                1 GiB, 4096 at least.
  *  dhidden       [n_rows, ld_dhidden] of dhidden_dtype, dtype or BIL_F32, rows on
  *                16-byte boundaries; NULL: not computed.
- *  dweight       [vocab, ld_dweight] of dweight_dtype, likewise (n_rows = 0: zero).
+ *  dweight       [vocab, ld_dweight] of dweight_dtype, likewise (n_rows = 0: zero);
+ *                not the weight's buffer (refused).
  * Other arguments as for the forward.  The bits are reproducible on a given GPU.
  */
 int bil_linear_cross_entropy_bwd(const void *hidden, const void *weight, int dtype, int64_t n_rows, int64_t hidden_size,

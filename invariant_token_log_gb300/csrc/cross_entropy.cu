@@ -895,7 +895,7 @@ int dhidden_splits(int64_t n_rows, int64_t hidden_size, int64_t vocab, int64_t p
   const int64_t k_blocks = (std::min(piece, vocab) + kBK - 1) / kBK;
   int best = 1;
   double least = 0.0;
-  for (int s = 1; s <= 16 && s <= k_blocks; ++s) {
+  for (int s = 1; s <= 16 && s <= k_blocks && s * up(n_rows, kUnitRows) <= INT32_MAX; ++s) {
     const double rounds = static_cast<double>((tiles * s + pairs - 1) / pairs);
     const double cycles = rounds * static_cast<double>((k_blocks + s - 1) / s) * 512.0 +
                           s * static_cast<double>(n_rows) * static_cast<double>(hidden_size) * 8.0 / 3500.0;
@@ -1150,7 +1150,7 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
     if (!rows16(dhidden, ld_dhidden, eh)) return BIL_E_ALIGN;
   }
   if (dweight != nullptr) {
-    if (ld_dweight < hidden_size) return BIL_E_INVALID_ARG;
+    if (ld_dweight < hidden_size || dweight == weight) return BIL_E_INVALID_ARG;  // (the weight is read to the end)
     if (!bil_internal::extent_ok(vocab, ld_dweight, ew)) return BIL_E_UNSUPPORTED;
     if (!rows16(dweight, ld_dweight, ew)) return BIL_E_ALIGN;
   }

@@ -551,7 +551,7 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   if (int st = check_rows(dy, n, width, ld_dy, eb)) return st;
   if (int st = check_rows(dweight, vocab, width, ld_dweight, ob)) return st;
   if (n > 0) {
-    if (ids == nullptr || workspace == nullptr) return BIL_E_INVALID_ARG;
+    if (ids == nullptr || workspace == nullptr || dweight == dy) return BIL_E_INVALID_ARG;  // (dy is read to the end)
     if (!aligned_to(ids, 8) || !aligned_to(workspace, 256)) return BIL_E_ALIGN;
     if (workspace_bytes < static_cast<int64_t>(layout_of(n, width).total)) return BIL_E_INVALID_ARG;
   }

@@ -157,7 +157,7 @@ def test_embedding_fwd(lib, kw, status):
     assert lib.bil_embedding_fwd(*{**EMBED, **kw}.values()) == status
 
 
-EMBED_BWD = dict(dy=P, dtype=_lib.BF16, n=4, width=64, lddy=64, ids=P, vocab=100, scale=1.0, pad=-1, dw=P, dwt=_lib.BF16,
+EMBED_BWD = dict(dy=P, dtype=_lib.BF16, n=4, width=64, lddy=64, ids=P, vocab=100, scale=1.0, pad=-1, dw=P2, dwt=_lib.BF16,
                  lddw=64, acc=0, ws=P, bytes=1 << 40, stream=None)
 
 
@@ -169,6 +169,7 @@ EMBED_BWD = dict(dy=P, dtype=_lib.BF16, n=4, width=64, lddy=64, ids=P, vocab=100
     (dict(dtype=9), DTYPE),
     (dict(dwt=_lib.F16), DTYPE),
     (dict(dtype=_lib.F32, dwt=_lib.BF16), DTYPE),
+    (dict(dw=P), INVALID),                      # the output over dy
     (dict(scale=INF), INVALID),
     (dict(lddy=63), INVALID),
     (dict(lddw=63), INVALID),
@@ -234,7 +235,7 @@ def test_cross_entropy_fwd(lib, kw, status):
 
 
 XENT_BWD = dict(h=P, w=P, dtype=_lib.BF16, n=4, hidden=64, ldh=64, vocab=1000, ldw=64, tgt=P, ign=-100, smooth=0.1, z=1e-4,
-                red=1, lse=P, g=P, piece=0, dh=P, dht=_lib.BF16, lddh=64, dw=P, dwt=_lib.BF16, lddw=64, ws=P, bytes=1 << 40,
+                red=1, lse=P, g=P, piece=0, dh=P, dht=_lib.BF16, lddh=64, dw=P2, dwt=_lib.BF16, lddw=64, ws=P, bytes=1 << 40,
                 stream=None)
 
 
@@ -242,6 +243,7 @@ XENT_BWD = dict(h=P, w=P, dtype=_lib.BF16, n=4, hidden=64, ldh=64, vocab=1000, l
     (dict(n=0, dw=None), OK),
     (dict(piece=-1), INVALID),
     (dict(dh=None, dw=None), INVALID),
+    (dict(dw=P), INVALID),                      # the gradient over the weight
     (dict(dht=_lib.F16), DTYPE),
     (dict(dwt=_lib.F16), DTYPE),
     (dict(lddh=63), INVALID),
