@@ -7,7 +7,8 @@ is the LM head's weight too, with a block in between.
 norm with dropout and the residual's addition, cross entropy.  ``step`` is the same with
 its gradients as a sequence of calls without autograd, which a CUDA graph can hold:
 the seed and the step of the masks are a tensor that the program writes between
-replays, and the table's two gradients are added up in one buffer.
+replays, and the table's two gradients are added up in one buffer.  (A program that captures
+the autograd form has to drop its eager graphs of the same leaves first.)
 """
 from __future__ import annotations
 

@@ -73,8 +73,9 @@ __global__ void __launch_bounds__(kLookupThreads) embedding_lookup_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// Sorting the places by token: least significant digit first, two kernels a digit
-// (the tiles' digit counts, then each tile's places to where they belong).  A few
+// Sorting the places by token: least significant digit first.  A kernel counts the
+// first digit in every tile; then one a digit moves each tile's places to where they
+// belong and counts the next digit there (whole numbers: in any order).  A few
 // blocks of small latency each; of the table's zeros, most of what the gradient
 // writes, further blocks of the same launches store a part meanwhile.
 // ---------------------------------------------------------------------------
@@ -110,7 +111,9 @@ struct SortParams {
   const uint32_t* places;
   uint32_t* keys_out;
   uint32_t* places_out;
-  uint32_t* counts;       // [tiles, kDigits]
+  uint32_t* counts;       // [tiles, kDigits] of this digit
+  uint32_t* next_counts;  // of the next one, added to; NULL: this is the last
+  uint32_t* zero_counts;  // what the next launch adds to, set to zero here; NULL: nothing
   int n, tiles, shift;
   Zeros zeros;            // by the blocks from `tiles` on
 };
@@ -134,7 +137,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
   return static_cast<uint32_t>(id >= 0 && id < p.vocab && id != p.padding ? id : p.vocab);
 }
 
-template <bool FIRST, int PER>
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
   __shared__ uint32_t counts[kDigits];
   for (int d = threadIdx.x; d < kDigits; d += kSortThreads) counts[d] = 0;
@@ -150,11 +153,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int64_t i = first + j * kSortThreads + threadIdx.x;
-    if (i < p.n) atomicAdd(&counts[(sort_key<FIRST>(p, static_cast<int>(i)) >> p.shift) & (kDigits - 1)], 1u);
+    if (i < p.n) atomicAdd(&counts[sort_key<true>(p, static_cast<int>(i)) & (kDigits - 1)], 1u);
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads)
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {
     p.counts[static_cast<int64_t>(blockIdx.x) * kDigits + d] = counts[d];
+    if (p.zero_counts != nullptr) p.zero_counts[static_cast<int64_t>(blockIdx.x) * kDigits + d] = 0u;
+  }
 }
 
 // A warp takes its 32 PER places in order, 32 at a time; those with one digit rank by
@@ -173,6 +178,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
                 static_cast<int64_t>(gridDim.x - p.tiles) * kSortThreads);
     return;
   }
+  if (p.zero_counts != nullptr)
+    for (int d = threadIdx.x; d < kDigits; d += kSortThreads)
+      p.zero_counts[static_cast<int64_t>(blockIdx.x) * kDigits + d] = 0u;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kSortThreads * PER) + warp * (PER * kLanes);
   uint32_t key[PER];
   uint32_t rank[PER];
@@ -236,6 +244,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     const uint32_t to = of_warp[warp][(key[j] >> p.shift) & (kDigits - 1)] + rank[j];
     p.keys_out[to] = key[j];
     p.places_out[to] = FIRST ? static_cast<uint32_t>(i) : p.places[i];
+    if (p.next_counts != nullptr)
+      atomicAdd(p.next_counts + static_cast<int64_t>(to / (kSortThreads * PER)) * kDigits +
+                    ((key[j] >> (p.shift + kDigitBits)) & (kDigits - 1)),
+                1u);
   }
 }
 
@@ -439,10 +451,11 @@ __global__ void __launch_bounds__(kSumThreads) embedding_join_kernel(const SumPa
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
-// Places a segment: 16, or as many as leave 2048 segments (of a power of two).
+// Places a segment: 16, or as many as leave 512 segments (of a power of two).  More segments would be more parts of
+// the most frequent tokens, which are joined one after the other.
 int segment_places(int64_t n) {
   int s = 16;
-  while (static_cast<int64_t>(s) * 2048 < n) s *= 2;
+  while (static_cast<int64_t>(s) * 512 < n) s *= 2;
   return s;
 }
 
@@ -454,7 +467,9 @@ int64_t sort_tiles(int64_t n) {
   return (n + tile - 1) / tile;
 }
 
-constexpr int64_t kEarlyZeros = 32 << 20;  // bytes of zeros in a launch of the sort: its few microseconds at 6.6 TB/s
+constexpr int64_t kEarlyZeros = 48 << 20;  // bytes of zeros in a launch of the sort: its seven microseconds at 6.6 TB/s
+
+constexpr int kMaxDigits = 4;  // of 31 bits
 
 struct Layout {
   size_t keys, counts, parts, total;
@@ -466,7 +481,7 @@ Layout layout_of(int64_t n, int64_t width) {
   l.keys = round256(static_cast<size_t>(n) * 4);
   l.counts = round256(static_cast<size_t>(tiles) * kDigits * 4);
   l.parts = round256(static_cast<size_t>(segments) * 2 * static_cast<size_t>((width + kVec - 1) / kVec * kVec) * 4);
-  l.total = 4 * l.keys + l.counts + l.parts;
+  l.total = 4 * l.keys + kMaxDigits * l.counts + l.parts;
   return l;
 }
 
@@ -573,19 +588,25 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   q.ids = ids;
   q.vocab = vocab;
   q.padding = padding_idx;
-  q.counts = reinterpret_cast<uint32_t*>(ws + 4 * l.keys);
   q.n = static_cast<int>(n);
   q.tiles = static_cast<int>(sort_tiles(n));
   Zeros zeros{static_cast<unsigned char*>(dweight), ld_dweight * ob, 0, accumulate ? 0 : vocab, width * ob};
-  int launches = 0;
-  for (int shift = 0; shift == 0 || (vocab >> shift) != 0; shift += kDigitBits) launches += 2;
+  int digits = 1;
+  while ((vocab >> (digits * kDigitBits)) != 0) ++digits;
+  const int launches = digits + 1;
   // What the sort's launches have time for; the sums' launch stores the others.
   const int64_t early = std::min(zeros.end, launches * (kEarlyZeros / zeros.row_bytes + 1));
   const bool few = sort_per(n) == kFewPer;
+  auto counts_of = [&](int digit) {
+    return digit < digits ? reinterpret_cast<uint32_t*>(ws + 4 * l.keys + static_cast<size_t>(digit) * l.counts) : nullptr;
+  };
   int at = 0;  // the pair of buffers that the next digit is written to
   for (int i = 0; i < launches; ++i) {
-    const bool first = i < 2, count = i % 2 == 0;
-    q.shift = i / 2 * kDigitBits;
+    const int digit = i == 0 ? 0 : i - 1;
+    q.shift = digit * kDigitBits;
+    q.counts = counts_of(digit);
+    q.next_counts = counts_of(digit + 1);
+    q.zero_counts = counts_of(i == 0 ? 1 : digit + 2);
     q.keys = buf[at ^ 2];
     q.places = buf[(at ^ 2) + 1];
     q.keys_out = buf[at];
@@ -596,12 +617,11 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
     const int64_t units = ((q.zeros.end - q.zeros.begin) * q.zeros.row_bytes / 16 + kSortThreads - 1) / kSortThreads;
     const int64_t zero_blocks = early == 0 ? 0 : std::max<int64_t>(1, std::min<int64_t>(units, 8 * static_cast<int64_t>(sms)));
     void (*kernel)(SortParams) =
-        count ? (first ? (few ? sort_count_kernel<true, kFewPer> : sort_count_kernel<true, kManyPer>)
-                       : (few ? sort_count_kernel<false, kFewPer> : sort_count_kernel<false, kManyPer>))
-              : (first ? (few ? sort_place_kernel<true, kFewPer> : sort_place_kernel<true, kManyPer>)
-                       : (few ? sort_place_kernel<false, kFewPer> : sort_place_kernel<false, kManyPer>));
+        i == 0   ? (few ? sort_count_kernel<kFewPer> : sort_count_kernel<kManyPer>)
+        : i == 1 ? (few ? sort_place_kernel<true, kFewPer> : sort_place_kernel<true, kManyPer>)
+                 : (few ? sort_place_kernel<false, kFewPer> : sort_place_kernel<false, kManyPer>);
     if (launch_pdl(kernel, q.tiles + zero_blocks, kSortThreads, 0, s, 1, q) != cudaSuccess) return BIL_E_CUDA;
-    if (!count) at ^= 2;
+    if (i > 0) at ^= 2;
   }
 
   SumParams p{};
@@ -622,7 +642,7 @@ int bil_embedding_bwd(const void* dy, int dtype, int64_t n, int64_t width, int64
   p.dw = static_cast<unsigned char*>(dweight);
   p.vec_dw = rows_start_on(dweight, vocab, ld_dweight * ob, 16);
   p.accumulate = accumulate != 0;
-  p.parts = reinterpret_cast<float*>(ws + 4 * l.keys + l.counts);
+  p.parts = reinterpret_cast<float*>(ws + 4 * l.keys + kMaxDigits * l.counts);
   const bool full = width % kVec == 0 && rows_start_on(dy, n, ld_dy * eb, 16);
   const int per_block = kSumThreads / p.row_threads;
   zeros.begin = early;

@@ -13,7 +13,8 @@ namespace {
 // behind that kernel's tail).  Only kernels that wait for their predecessor
 // with griddep_wait() before touching global memory are launched this way:
 // the forward's stream, cluster and merge kernels, the forward kernels of
-// topk.cu, the norm's kernels and the 8-bit LM head.  (The logits path's
+// topk.cu, the norms' kernels, the 8-bit LM head, and the kernels of dropout.cu,
+// embedding.cu and cross_entropy.cu.  (The logits path's
 // backward is not: the wait made its element-by-element loads twice as slow.)
 // cluster > 1: thread-block clusters of that many blocks along x.
 template <typename... KArgs, typename... Args>
