@@ -1367,16 +1367,13 @@ __global__ void __launch_bounds__(256) sum_f32_kernel(SumSources s, int count, i
 // The same for e4m3 elements: boxes of box_rows x 128 elements, the tensor
 // cores' type being in the instruction descriptor alone.
 int make_map8(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return BIL_E_CUDA;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK8), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BIL_OK : BIL_E_CUDA;
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(ptr), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+             ? BIL_OK
+             : BIL_E_CUDA;
 }
 
 typedef void (*GemmKernel)(CUtensorMap, CUtensorMap, CUtensorMap, LinearParams);

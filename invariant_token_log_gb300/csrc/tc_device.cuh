@@ -216,28 +216,46 @@ EncodeTiledFn encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
-  // The encoder wants a current context; a thread that has made no runtime call yet (a backward pass's) has none.
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
   return fn;
+}
+
+// Whether another try is worth it: the encoder wants a current context, and a thread that has made no runtime call yet
+// (a backward pass's) has none until its device is set.
+bool context_made() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == BIL_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+         : dtype == BIL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// A row-major map of 2 dimensions: dims, box and strides as cuTensorMapEncodeTiled takes them.
+bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint32_t estr[2] = {1, 1};
+  auto encode = [&] {
+    return fn(map, type, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return encode() || (context_made() && encode());
 }
 
 // A 2-D tensor map over a row-major [rows, cols] matrix of 16-bit elements
 // (row stride ld elements), box = box_rows x 64 elements, 128-byte swizzle;
 // reads past the matrix fill zeros.
 int make_map(CUtensorMap* map, const void* ptr, int dtype, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return BIL_E_CUDA;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt =
-      dtype == BIL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const CUresult r = fn(map, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BIL_OK : BIL_E_CUDA;
+  return encode_2d(map, dtype == BIL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   const_cast<void*>(ptr), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+             ? BIL_OK
+             : BIL_E_CUDA;
 }
 
 // The tensor map an epilogue stores a [rows, cols] output (row stride ld
@@ -245,19 +263,13 @@ int make_map(CUtensorMap* map, const void* ptr, int dtype, int64_t rows, int64_t
 // 32 columns of a 16-bit type or 16 of float32, no swizzle (a box in shared
 // memory is row-major).
 int make_store_map(CUtensorMap* map, void* ptr, int dtype, int64_t rows, int64_t cols, int64_t ld) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return BIL_E_CUDA;
   const int eb = dtype == BIL_F32 ? 4 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * eb};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / eb), static_cast<cuuint32_t>(kStoreBox)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType dt = dtype == BIL_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                 : dtype == BIL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const CUresult r = fn(map, dt, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BIL_OK : BIL_E_CUDA;
+  return encode_2d(map, map_type(dtype), ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE)
+             ? BIL_OK
+             : BIL_E_CUDA;
 }
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
