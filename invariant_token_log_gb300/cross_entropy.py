@@ -21,7 +21,7 @@ import functools
 import torch
 
 from . import _lib
-from .linear import _in_code, _ld, _matrix, _pad8
+from .linear import _IN_DTYPES, _in_code, _ld, _matrix, _pad8
 from .logp import (
     _DEVICE_OBJECTS,
     IGNORE_INDEX,
@@ -36,14 +36,19 @@ from .norm import _call, _padded
 _REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 
 
-def _operand(x: torch.Tensor, what: str) -> torch.Tensor:
-    if x.is_contiguous() and x.shape[1] % 8 == 0 and x.data_ptr() % 16 == 0:
-        return x
-    return _matrix(x, what)
-
-
 def _operands(hidden, weight, target_ids, label_smoothing, reduction):
     index = hidden.get_device()
+    lead, dtype = target_ids.shape, hidden.dtype
+    if (index >= 0 and target_ids.dtype is torch.int64 and len(lead) == 1 and dtype in _IN_DTYPES and
+            weight.dtype is dtype and target_ids.get_device() == index and weight.get_device() == index):
+        # The common call, row-major matrices and int64 [N], without the general path's conversions.
+        h_shape, w_shape = hidden.shape, weight.shape
+        if (len(h_shape) == 2 and len(w_shape) == 2 and h_shape[0] == lead[0] and h_shape[1] == w_shape[1] and
+                w_shape[0] and w_shape[1] and w_shape[1] % 8 == 0 and hidden.is_contiguous() and weight.is_contiguous() and
+                target_ids.is_contiguous() and hidden.data_ptr() % 16 == 0 and weight.data_ptr() % 16 == 0 and
+                0.0 <= label_smoothing <= 1.0 and reduction in _REDUCTIONS):
+            return (index, _DEVICE_OBJECTS.get(index) or _device_object(index), _IN_DTYPES[dtype], lead, hidden, weight,
+                    target_ids, w_shape[1], w_shape[1])
     if index < 0 or weight.get_device() < 0 or target_ids.get_device() < 0:
         _need_cuda(hidden, weight, target_ids)
     if hidden.dim() < 1 or weight.dim() != 2:
@@ -63,12 +68,12 @@ def _operands(hidden, weight, target_ids, label_smoothing, reduction):
     dev = _DEVICE_OBJECTS.get(index) or _device_object(index)
     t = _targets1d(target_ids, lead, dev)
     h2 = hidden if hidden.dim() == 2 else hidden.reshape(t.shape[0], hidden.shape[-1])
-    h2, w2 = _operand(h2, "hidden"), _operand(weight, "weight")
+    h2, w2 = _matrix(h2, "hidden"), _matrix(weight, "weight")
     if h2.shape[0] > 1 and h2.stride(0) < h2.shape[1]:
         h2 = h2.contiguous()  # an expanded tensor
     if w2.shape[0] > 1 and w2.stride(0) < w2.shape[1]:
         w2 = w2.contiguous()
-    return index, dev, code, lead, h2, w2, t
+    return index, dev, code, lead, h2, w2, t, _ld(h2), _ld(w2)
 
 
 def _scratch(workspace: torch.Tensor | None, need: int, dev: torch.device) -> tuple[torch.Tensor, int]:
@@ -107,13 +112,13 @@ def linear_cross_entropy_fwd(hidden: torch.Tensor, weight: torch.Tensor, target_
                              reduction: str = "mean", validate: bool = False, workspace: torch.Tensor | None = None):
     """(loss, lse): the float32 loss, one number or with reduction "none" [*lead], and the rows'
     lse [*lead] that ``linear_cross_entropy_bwd`` takes."""
-    index, dev, code, lead, h2, w2, t = _operands(hidden, weight, target_ids, label_smoothing, reduction)
+    index, dev, code, lead, h2, w2, t, ld_h, ld_w = _operands(hidden, weight, target_ids, label_smoothing, reduction)
     n, hs = h2.shape
     vocab = w2.shape[0]
     loss = torch.empty(lead if reduction == "none" else (), dtype=torch.float32, device=dev)
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     workspace, have = _scratch(workspace, fwd_workspace_bytes(n, hs, vocab, label_smoothing > 0.0) if n else 0, dev)
-    _call("bil_linear_cross_entropy_fwd", index, h2.data_ptr(), w2.data_ptr(), code, n, hs, _ld(h2), vocab, _ld(w2),
+    _call("bil_linear_cross_entropy_fwd", index, h2.data_ptr(), w2.data_ptr(), code, n, hs, ld_h, vocab, ld_w,
           t.data_ptr(), int(ignore_index), float(label_smoothing), float(z_loss), _REDUCTIONS[reduction],
           loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), have, 1 if validate else 0, _stream_handle(index))
     return loss, lse
@@ -128,7 +133,7 @@ def linear_cross_entropy_bwd(hidden: torch.Tensor, weight: torch.Tensor, target_
     number, or with reduction "none" [*lead]), in ``out_dtype``: the inputs' type (the
     default) or float32.  ``piece``: the columns of the vocabulary whose gradient is held
     at a time, 2 bytes for each of them and row.  One that is not needed is None."""
-    index, dev, code, lead, h2, w2, t = _operands(hidden, weight, target_ids, label_smoothing, reduction)
+    index, dev, code, lead, h2, w2, t, ld_h, ld_w = _operands(hidden, weight, target_ids, label_smoothing, reduction)
     n, hs = h2.shape
     vocab = w2.shape[0]
     if not (need_hidden or need_weight):
@@ -152,7 +157,7 @@ def linear_cross_entropy_bwd(hidden: torch.Tensor, weight: torch.Tensor, target_
         dw, _ = _padded(vocab, hs, 8, out_dtype, dev)
     piece = 0 if piece is None else int(piece)
     workspace, have = _scratch(workspace, _bwd_workspace_bytes(n, hs, vocab, piece, index) if n else 0, dev)
-    _call("bil_linear_cross_entropy_bwd", index, h2.data_ptr(), w2.data_ptr(), code, n, hs, _ld(h2), vocab, _ld(w2),
+    _call("bil_linear_cross_entropy_bwd", index, h2.data_ptr(), w2.data_ptr(), code, n, hs, ld_h, vocab, ld_w,
           t.data_ptr(), int(ignore_index), float(label_smoothing), float(z_loss), _REDUCTIONS[reduction],
           lse.data_ptr(), grad_loss.data_ptr(), piece, None if dh is None else dh.data_ptr(), oc,
           0 if dh is None else _pad8(hs), None if dw is None else dw.data_ptr(), oc, 0 if dw is None else _pad8(hs),

@@ -511,10 +511,10 @@ enum Reduction { kNone = 0, kMean = 1, kSum = 2 };
 struct RowsParams {
   const int64_t* targets;
   int64_t ignore_index, vocab;
-  int n, padded;      // padded: n up to the unit's rows
+  int n;
   int* n_active;
-  int* rows;          // [padded] the row of each that counts
-  int* targets_out;   // [padded] its target; -1: outside the vocabulary
+  int* rows;          // the row of each that counts
+  int* targets_out;   // its target; -1: outside the vocabulary
   // forward: what ignored rows give
   float* lse;         // [n]
   float* loss;        // [n] or NULL
@@ -524,7 +524,7 @@ struct RowsParams {
   int reduction;
   float smoothing, z_loss;
   int* place;         // [n] each row's place among those that count, -1: none
-  float4* coef;       // [padded]
+  float4* coef;       // by place (see GemmParams)
   float* scale;       // of the products' results
   // the copy of the rows that count (xent_gather_kernel's, or this kernel's where the rows are few)
   const unsigned char* hidden;
@@ -1057,7 +1057,6 @@ int bil_linear_cross_entropy_fwd(const void* hidden, const void* weight, int dty
   r.ignore_index = ignore_index;
   r.vocab = vocab;
   r.n = static_cast<int>(n_rows);
-  r.padded = static_cast<int>(l.padded);
   r.n_active = reinterpret_cast<int*>(ws);
   r.rows = reinterpret_cast<int*>(ws + 256);
   r.targets_out = reinterpret_cast<int*>(ws + 256 + l.rows);
@@ -1174,7 +1173,6 @@ int bil_linear_cross_entropy_bwd(const void* hidden, const void* weight, int dty
   r.ignore_index = ignore_index;
   r.vocab = vocab;
   r.n = static_cast<int>(n_rows);
-  r.padded = static_cast<int>(l.padded);
   r.n_active = reinterpret_cast<int*>(ws);
   r.scale = reinterpret_cast<float*>(ws + 128);
   r.rows = reinterpret_cast<int*>(take(l.rows));

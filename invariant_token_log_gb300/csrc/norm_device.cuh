@@ -26,6 +26,9 @@ constexpr unsigned kWatchNorm = 1024u;  // the wait for a row of a ring
 constexpr int kDrained = 2;             // of a block's abort flag: nothing is in flight any more
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
+static_assert(2 * (kMaxRowThreads / kLanes) * sizeof(float2) + kMaxStages * sizeof(uint64_t) + sizeof(DropKeys) + 32 <=
+                  bil_layout::kNormStatics,
+              "what the kernels declare beside their ring");
 static_assert(BIL_MAX_NORM_WIDTH == kMaxRowThreads * kMaxGroups * kVec, "the widest row a block holds");
 
 __device__ __forceinline__ float max_nan(float a, float b) {
