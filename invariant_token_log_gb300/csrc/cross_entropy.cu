@@ -24,6 +24,14 @@
 // nearly every row, is -2^12 to the bit: as any other number it would carry the same
 // rounding error, up to 2^-9, into every row.
 //
+// The tensor cores round an accumulator towards zero at each step of 16 products: of
+// K = 4096 in one accumulation a logit comes out 4e-6 of itself too small, and every
+// lse with it (the mean loss 2.7e-6 of itself, 7e-7 at K = 1104).  So a logit is
+// accumulated in segments of 12 K blocks, whose sums are added up in float32 in the
+// epilogue's registers: the error goes with a segment's steps (the loss within 6e-7 at
+// any K; with 16 blocks 8e-7, with 8 4e-7).  16384 x 151936 x 4096: 47.2 ms for 46.7, with
+// 8 blocks 47.9.  (The gradients' products, rounded to 16 bits, are one accumulation.)
+//
 // One GEMM body, C = A . B^T on pairs of blocks (cta_group::2, 256 x 256 a pair, K
 // blocks of 64 in a ring of six stages, two accumulators in tensor memory, so that a
 // tile's epilogue runs under the next tile's products):
@@ -56,6 +64,7 @@ constexpr int kUnitRows = 2 * kBM;                  // of a pair
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kHalf = kBN / 2;                      // columns of an epilogue warp
+constexpr int kSegment = 12;                        // K blocks of an accumulation (see below)
 constexpr uint32_t kBoxBytes = 32 * 128;            // of a store: 32 rows of a 128-byte line
 constexpr uint32_t kStagingBytes = 2 * kBoxBytes;   // of a warp
 
@@ -109,6 +118,17 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, u
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 8 columns of this thread's tensor-memory lane, waited for (few registers beside the sums that they are added to).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -271,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   asm volatile("fence.proxy.async;" ::: "memory");  // what the kernels before stored, before TMA reads it
 
+  constexpr int segment = EPI == kProducts ? INT32_MAX : kSegment;
   const Shape shape(p), shape2(p2);
   const int64_t total = shape.total + (EPI == kProducts ? shape2.total : 0);
   auto unit = [&](int64_t u, int& m, int& n, int& split, int& k0, int& k1) {  // true: of the second product
@@ -342,35 +363,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t it = 0;
       int local = 0;
       bool ok = true;
-      for (int64_t u = pair0; u < total && ok; u += pairs, ++local) {
+      for (int64_t u = pair0; u < total && ok; u += pairs) {
         int m, n, split, k0, k1;
         const bool second = unit(u, m, n, split, k0, k1);
         const uint32_t idesc = second ? p2.idesc : p.idesc;
-        const int b = local & 1;
-        const unsigned use = static_cast<unsigned>(local >> 1);
-        if (!thread_wait_cluster_watch(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma, &g_watchdog_xent)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kAccCols);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int s = static_cast<int>(it % kStages);
-          const unsigned ph = static_cast<unsigned>((it / kStages) & 1);
-          if (!thread_wait_watch(&sm.full[s], ph, abort, kWatchMma, &g_watchdog_xent, true)) {
+        int s0 = k0;
+        do {  // a segment: an accumulator of its own
+          const int s1 = k1 - s0 > segment ? s0 + segment : k1;
+          const int b = local & 1;
+          const unsigned use = static_cast<unsigned>(local >> 1);
+          if (!thread_wait_cluster_watch(&sm.acc_empty[b], (use & 1u) ^ 1u, abort, kWatchMma, &g_watchdog_xent)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(base + s * size_t(kStageBytes)), b_addr = a_addr + kStageABytes;
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(b * kAccCols);
+          for (int kb = s0; kb < s1; ++kb, ++it) {
+            const int s = static_cast<int>(it % kStages);
+            const unsigned ph = static_cast<unsigned>((it / kStages) & 1);
+            if (!thread_wait_watch(&sm.full[s], ph, abort, kWatchMma, &g_watchdog_xent, true)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(base + s * size_t(kStageBytes)), b_addr = a_addr + kStageABytes;
 #pragma unroll
-          for (int k = 0; k < kBK / kUmmaK; ++k) {
-            // a K step: 32 bytes along a K-major line, 16 lines of an MN-major box
-            const uint64_t adesc = second ? smem_desc_mn(a_addr + k * kUmmaK * 128) : smem_desc(a_addr + k * kUmmaK * 2);
-            const uint64_t bdesc = EPI == kProducts ? smem_desc_mn(b_addr + k * kUmmaK * 128) : smem_desc(b_addr + k * kUmmaK * 2);
-            umma_f16_pair(d_tmem, adesc, bdesc, idesc, kb != k0 || k != 0 ? 1u : 0u);
+            for (int k = 0; k < kBK / kUmmaK; ++k) {
+              // a K step: 32 bytes along a K-major line, 16 lines of an MN-major box
+              const uint64_t adesc = second ? smem_desc_mn(a_addr + k * kUmmaK * 128) : smem_desc(a_addr + k * kUmmaK * 2);
+              const uint64_t bdesc =
+                  EPI == kProducts ? smem_desc_mn(b_addr + k * kUmmaK * 128) : smem_desc(b_addr + k * kUmmaK * 2);
+              umma_f16_pair(d_tmem, adesc, bdesc, idesc, kb != s0 || k != 0 ? 1u : 0u);
+            }
+            umma_commit_pair(&sm.empty[s]);
           }
-          umma_commit_pair(&sm.empty[s]);
-        }
-        if (!ok) break;
-        umma_commit_pair(&sm.acc_full[b]);
+          if (!ok) break;
+          umma_commit_pair(&sm.acc_full[b]);
+          ++local;
+          s0 = s1;
+        } while (s0 < k1);
       }
       umma_commit_pair(&sm.mma_done);  // every product completes before the blocks free tensor memory
       thread_wait_watch(&sm.mma_done, 0u, abort, kWatchOwnDrain, &g_watchdog_xent, false);
@@ -382,17 +413,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale2 = EPI == kProducts ? *p2.scale : 1.0f;
     int local = 0;
     uint32_t issued = 0;
-    for (int64_t u = pair0; u < total; u += pairs, ++local) {
+    for (int64_t u = pair0; u < total; u += pairs) {
       int m, n, split, k0, k1;
       const bool second = unit(u, m, n, split, k0, k1);
-      const int b = local & 1;
-      const unsigned use = static_cast<unsigned>(local >> 1);
       const int row0 = (2 * m + rank) * kBM + q * 32, row = row0 + lane;
-      const uint32_t taddr =
-          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * kAccCols + half * kHalf);
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * kHalf);
       const int64_t first = static_cast<int64_t>(n) * kBN + half * kHalf;  // column of C
       const int vcols = static_cast<int>(p.cols - first < kHalf ? p.cols - first : kHalf);  // <= 0: none
-      auto release = [&] {
+      auto release = [&](int b) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0)
@@ -409,16 +437,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t >= p.col0 + first && t < p.col0 + first + vcols) tcol = static_cast<int>(t - p.col0 - first);
         }
       }
-      if (!warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_xent)) break;
-      tc_fence_after();
-      // The warp's columns into registers and the accumulator back at once: where K is short the next tile's products
-      // wait for it (64 x 151936 x 4096, the whole backward: 757 us, and 783 with the accumulator held to the end).
+      // The warp's columns into registers, a segment after the other, and the accumulator back at once: where K is
+      // short the next tile's products wait for it (64 x 151936 x 4096, the whole backward: 757 us, and 783 with the
+      // accumulator held to the end).
       uint32_t acc[4][kChunk];
+      if constexpr (EPI != kProducts) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_issue(taddr + c * kChunk, acc[c]);
+        for (int c = 0; c < 4 * kChunk; ++c) acc[c / kChunk][c % kChunk] = 0u;
+      }
+      bool ok = true;
+      int s0 = k0;
+      do {
+        const int s1 = k1 - s0 > segment ? s0 + segment : k1;
+        const int b = local & 1;
+        const unsigned use = static_cast<unsigned>(local >> 1);
+        ok = warp_wait_watch(&sm.acc_full[b], use & 1u, abort, kWatchAccFull, &g_watchdog_xent);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = taddr + static_cast<uint32_t>(b * kAccCols);
+        if constexpr (EPI == kProducts) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait(acc[c]);
-      release();
+          for (int c = 0; c < 4; ++c) tmem_ld32_issue(at + c * kChunk, acc[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait(acc[c]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4 * kChunk; c += 8) {
+            uint32_t r[8];
+            tmem_ld8(at + c, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t& a = acc[c / kChunk][c % kChunk + j];
+              a = __float_as_uint(__fadd_rn(__uint_as_float(a), __uint_as_float(r[j])));
+            }
+          }
+        }
+        release(b);
+        ++local;
+        s0 = s1;
+      } while (s0 < k1);
+      if (!ok) break;
       if constexpr (EPI == kStats) {
         if (row0 >= shape.m_rows || vcols <= 0) continue;
         if (__any_sync(0xffffffffu, tcol >= 0)) {
