@@ -27,10 +27,10 @@
 // The tensor cores round an accumulator towards zero at each step of 16 products: of
 // K = 4096 in one accumulation a logit comes out 4e-6 of itself too small, and every
 // lse with it (the mean loss 2.7e-6 of itself, 7e-7 at K = 1104).  So a logit is
-// accumulated in segments of 12 K blocks, whose sums are added up in float32 in the
-// epilogue's registers: the error goes with a segment's steps (the loss within 6e-7 at
-// any K; with 16 blocks 8e-7, with 8 4e-7).  16384 x 151936 x 4096: 47.2 ms for 46.7, with
-// 8 blocks 47.9.  (The gradients' products, rounded to 16 bits, are one accumulation.)
+// accumulated in even segments of at most 16 K blocks, whose sums are added up in float32
+// in the epilogue's registers: the error goes with a segment's steps, 8e-7 of the loss
+// at any K (with 12 blocks 6e-7, and 3% more time at 4096 x 151936 x 4096, with 16 0.2%).
+// (The gradients' products, rounded to 16 bits, are one accumulation.)
 //
 // One GEMM body, C = A . B^T on pairs of blocks (cta_group::2, 256 x 256 a pair, K
 // blocks of 64 in a ring of six stages, two accumulators in tensor memory, so that a
@@ -64,7 +64,7 @@ constexpr int kUnitRows = 2 * kBM;                  // of a pair
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kHalf = kBN / 2;                      // columns of an epilogue warp
-constexpr int kSegment = 12;                        // K blocks of an accumulation (see below)
+constexpr int kSegment = 16;                        // K blocks of an accumulation, at most (see below)
 constexpr uint32_t kBoxBytes = 32 * 128;            // of a store: 32 rows of a 128-byte line
 constexpr uint32_t kStagingBytes = 2 * kBoxBytes;   // of a warp
 
@@ -121,13 +121,15 @@ __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// 8 columns of this thread's tensor-memory lane, waited for (few registers beside the sums that they are added to).
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// 16 columns of this thread's tensor-memory lane, waited for (few registers beside the sums that they are added to).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   __syncwarp();
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -291,8 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   asm volatile("fence.proxy.async;" ::: "memory");  // what the kernels before stored, before TMA reads it
 
-  constexpr int segment = EPI == kProducts ? INT32_MAX : kSegment;
   const Shape shape(p), shape2(p2);
+  // K blocks of a segment: as even as can be.
+  const int segments = (shape.k_blocks + kSegment - 1) / kSegment;
+  const int segment = EPI == kProducts ? INT32_MAX : (shape.k_blocks + segments - 1) / max(1, segments);
   const int64_t total = shape.total + (EPI == kProducts ? shape2.total : 0);
   auto unit = [&](int64_t u, int& m, int& n, int& split, int& k0, int& k1) {  // true: of the second product
     const bool second = EPI == kProducts && u >= shape.total;
@@ -462,11 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c) tmem_ld_wait(acc[c]);
         } else {
 #pragma unroll
-          for (int c = 0; c < 4 * kChunk; c += 8) {
-            uint32_t r[8];
-            tmem_ld8(at + c, r);
+          for (int c = 0; c < 4 * kChunk; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(at + c, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
               uint32_t& a = acc[c / kChunk][c % kChunk + j];
               a = __float_as_uint(__fadd_rn(__uint_as_float(a), __uint_as_float(r[j])));
             }
